@@ -372,6 +372,154 @@ tkv_status tkv_replay(tkv_ctx* ctx);
 tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_gbs, double* h2d_sm_gbs,
                                  double* d2h_ce_gbs);
 
+/* ------------------------------------------------------------------------
+ * Operators over a paged cache that the caller owns.
+ *
+ * The pages have no counterpart for these calls: they are what a decode layer
+ * around the attention needs when its cache is not a tiered context -- the
+ * rotation of positions, rows into a paged cache with the rotation of k on the
+ * way, attention over that cache held in 4 bits or in 16, and rows back out.
+ *
+ * Conventions of the five calls, beyond those at the top of this file:
+ *   - They have no context and keep nothing: the caller owns every buffer, they
+ *     allocate nothing, never synchronise, can be captured into a CUDA graph, and
+ *     may be called from several host threads.  Their work is enqueued on
+ *     `stream` (NULL = the legacy default stream) of the current device, on
+ *     which all pointers must lie.
+ *   - A step's rows are ragged.  cu_tokens: device int32 [batch + 1],
+ *     ascending; sequence b owns rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of
+ *     k, v, q and out, and they are its last positions: row cu_tokens[b] + i
+ *     is position lengths[b] - n_b + i, n_b = cu_tokens[b + 1] - cu_tokens[b].
+ *     `rows` is the extent of the tensors; rows behind cu_tokens[batch] are
+ *     left as they were (a captured step can be padded).  lengths counts the
+ *     step's own tokens, so one array serves append and attention.
+ *   - Strides count elements; the channels of a head are contiguous.  Inputs
+ *     may be broadcast (stride 0); the elements of an output may not overlap.
+ *   - The device arrays (positions, page table, lengths, cu_tokens) cannot be
+ *     checked by the host.  No kernel reads or writes outside the buffers for
+ *     any value in them.  What is wrong is left out as each call says and
+ *     reported in `status`: a device int32 that the caller clears (or NULL),
+ *     raised to TKV_EINVAL (a position outside the rotary table), TKV_ECAPACITY
+ *     (a page or a position outside the cache) or TKV_ETIMEOUT, the largest. */
+
+/* Element types.  TKV_INT4 is a type of pages only. */
+enum { TKV_BF16 = 0, TKV_FP16 = 1, TKV_FP32 = 2, TKV_INT4 = 3 };
+
+/* A rotation of positions.  Of a head's channels the first 2 * pairs are
+ * turned in pairs, (j, j + pairs) or, if interleaved, (2j, 2j + 1):
+ *   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin
+ * by the angle that the table holds for pair j at position
+ * positions[pair_axis[j]][row]: with one axis, text; with several (time,
+ * height, width), each section of the pairs follows its own axis.  inverse
+ * turns by the negated angle, which is the gradient of the forward call. */
+typedef struct {
+    const float* table;         /* device fp32 [max_positions][pairs][2]: cos, sin; 8-byte aligned */
+    const int32_t* positions;   /* device int32 [num_axes][axis_stride], the row innermost; may be NULL in
+                                   tkv_paged_append with one axis: the row's position in the cache */
+    int64_t axis_stride;        /* elements from one axis to the next */
+    int32_t max_positions;      /* rows of the table */
+    int32_t pairs;              /* 1 .. 256, 2 * pairs <= head_dim */
+    int32_t num_axes;           /* 1 .. 4 */
+    int32_t interleaved;        /* 0: pair j is channels j, j + pairs; 1: channels 2j, 2j + 1 */
+    int32_t inverse;            /* 0: forward, 1: by the negated angle */
+    uint8_t pair_axis[256];     /* axis of each pair, below num_axes */
+} tkv_rotary;
+
+/* A paged cache.  Position p of sequence b lies in page page_table[b][p /
+ * page_size].  Pages, by kv_type:
+ *   TKV_BF16, TKV_FP16  [num_pages][Hkv][2][page_size][d]   (2 = K, V)
+ *   TKV_INT4            [num_pages][Hkv][page_size / 16][18 d] bytes: records of
+ *       16 positions, K codes [16][d/2] | K scales [16][d/16] | V codes [16][d/2] |
+ *       V scales [d/16][16].  A code is q + 8, q in -7..7, in four bits (channel
+ *       2j in the low half of byte j); a scale is the E4M3 number of 16
+ *       channels; the value is q * scale * gain of the KV head.  The append
+ *       writes scale = amax / (7 gain), to nearest even, saturating at 448, and
+ *       q = x / (scale gain), to nearest even; a block with an infinity or a
+ *       NaN reads as NaN.  Choose gain so that amax / (7 gain) falls in E4M3's
+ *       normal range, 2^-6 .. 448: amax / 1024 of what the head is expected to
+ *       hold leaves room on both sides. */
+typedef struct {
+    void* pages;                /* device, 16-byte aligned */
+    const int32_t* page_table;  /* device int32 [batch][max_pages] */
+    const int32_t* lengths;     /* device int32 [batch]: positions of each sequence, the step's included */
+    const float* k_gain;        /* device fp32 [Hkv], > 0; TKV_INT4 only; NULL = 1 */
+    const float* v_gain;
+    int64_t num_pages;
+    int32_t kv_type;            /* TKV_BF16, TKV_FP16 or TKV_INT4 */
+    int32_t num_kv_heads;       /* Hkv >= 1 */
+    int32_t head_dim;           /* d: 64 or 128 */
+    int32_t page_size;          /* a power of two, 16 .. 65536 */
+    int32_t batch;              /* B >= 1 */
+    int32_t max_pages;          /* pages a sequence; max_pages * page_size <= 2^30 */
+} tkv_paged;
+
+/* Rotates x into out, which may be x itself (same strides).
+ * x, out: device [rows][heads][head_dim] of dtype (TKV_BF16, TKV_FP16 or
+ * TKV_FP32), any strides that keep out's elements apart; channels behind the
+ * rotated ones are copied.  Computed in fp32, rounded once.  Fast where
+ * everything starts on 16-byte boundaries.  A position outside the table turns
+ * its pairs into NaN and raises status to TKV_EINVAL.
+ * Errors: TKV_EINVAL, TKV_ECUDA. */
+tkv_status tkv_rope(const tkv_rotary* rotary, const void* x, void* out, int32_t dtype, int64_t rows,
+                    int32_t heads, int32_t head_dim, int64_t x_row_stride, int64_t x_head_stride,
+                    int64_t out_row_stride, int64_t out_head_stride, int32_t* status, void* stream);
+
+/* Writes a step's k and v into their pages; k is rotated on the way if rotary is
+ * not NULL (before it is rounded to the pages' type).
+ * k, v: device [rows][Hkv][d] of dtype TKV_BF16 or TKV_FP16 (the pages' own type if
+ * they are 16-bit), 16-byte aligned, strides multiples of 8.
+ * A row whose position is negative or beyond the page table, or whose page is
+ * not in [0, num_pages), is dropped and raises status to TKV_ECAPACITY.  Two
+ * rows that the page table sends to the same place race: one of them stays, or
+ * a mixture.  Errors: TKV_EINVAL, TKV_ECUDA. */
+tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary* rotary, const void* k, const void* v,
+                            int32_t dtype, int64_t rows, int64_t k_row_stride, int64_t k_head_stride,
+                            int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_tokens,
+                            int32_t* status, void* stream);
+
+/* The reverse: reads positions out of the pages into k and v, addressed like an
+ * append (lengths[b] = the end of the range, n_b its extent).
+ * k, v: device [rows][Hkv][d] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, 16-byte
+ * aligned, strides multiples of 16 bytes; the values are rounded once.  A row
+ * without a place (see the append) reads as NaN and raises status.
+ * Errors: TKV_EINVAL, TKV_ECUDA. */
+tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dtype, int64_t rows,
+                            int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                            int64_t v_head_stride, const int32_t* cu_tokens, int32_t* status, void* stream);
+
+/* Attention of a step's queries over the paged cache: one query a sequence in
+ * plain decoding, several where drafted tokens are checked or a prompt is
+ * continued.  Query row cu_tokens[b] + i, at position p = lengths[b] - n_b + i,
+ * sees the positions <= p and, with window > 0, > p - window.  Query head h
+ * reads KV head h / (num_q_heads / Hkv).
+ *   out = softmax(scale q.k) v in q's type, lse = log of the sum of
+ *   exp(scale q.k) (natural; NULL = not wanted; joins partial results over
+ *   several caches); a query that sees nothing gets out = 0, lse = -infinity.
+ * q, out: device [rows][num_q_heads][d] of dtype TKV_BF16 or TKV_FP16 (the pages'
+ * own type if they are 16-bit), 16-byte aligned, strides multiples of 8; lse:
+ * device fp32 [rows][num_q_heads], contiguous.
+ * max_new and max_len are the host's estimates of the largest n_b and the largest
+ * length.  They choose how the work is split, not what is computed: any
+ * values >= 1 give right results, better ones faster.
+ * workspace: device memory of tkv_paged_attention_workspace(...) bytes, 16-byte
+ * aligned, contents irrelevant; calls that may run at the same time need one
+ * each.  Results of one call's inputs are the same every time; a
+ * sequence's last bits may depend on the lengths of the others (they move
+ * the places where its sums are split).  Positions in a page outside
+ * [0, num_pages), and a sequence's positions beyond the page table, are left
+ * out and raise status to TKV_ECAPACITY.
+ * Errors: TKV_EINVAL, TKV_ECAPACITY (workspace too small), TKV_ECUDA. */
+tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q, void* out, float* lse, int32_t dtype,
+                               int64_t rows, int32_t num_q_heads, int64_t q_row_stride, int64_t q_head_stride,
+                               int64_t out_row_stride, int64_t out_head_stride, const int32_t* cu_tokens,
+                               int32_t max_new, int32_t max_len, int32_t window, float scale, void* workspace,
+                               int64_t workspace_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace that tkv_paged_attention needs on the current device for
+ * this cache, num_q_heads and max_new (0 if the arguments are refused).  Does
+ * not depend on lengths. */
+int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_heads, int32_t max_new);
+
 /* Waits for all enqueued work and reports any device-side status word. */
 tkv_status tkv_sync(tkv_ctx* ctx);
 

@@ -21,6 +21,8 @@ Modules:
                score (s descending, lower index first on ties).
   attention -- decode-step attention over the retained tokens of one layer,
                reading each token from the container of its tier.
+  paged     -- rotary positions, 4-bit page records and ragged attention over a
+               paged cache, from the definitions in include/tkv.h.
   session   -- a decode session: prefill, per-step append + attention +
                score update, and a re-tier every Delta steps.
 
@@ -30,6 +32,6 @@ routine, a closed form, a hand-derived fixture under ``tests/golden/`` or an
 invariant).  None is "parity unpinned".
 """
 
-from . import fp8, tiering, attention, session  # noqa: F401
+from . import fp8, tiering, attention, paged, session  # noqa: F401
 
-__all__ = ["fp8", "tiering", "attention", "session"]
+__all__ = ["fp8", "tiering", "attention", "paged", "session"]

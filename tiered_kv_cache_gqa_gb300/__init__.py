@@ -22,13 +22,15 @@ TKV_OK, TKV_EINVAL, TKV_ENOMEM, TKV_ECUDA, TKV_ECAPACITY, TKV_ETIMEOUT, TKV_ESTA
 TKV_T1_COPY_ENGINE, TKV_T1_SM_COPY, TKV_T1_SPLIT, TKV_T1_MULTI_CE, TKV_T1_RESIDENT = range(5)
 TKV_T2_HBM, TKV_T2_HOST = range(2)
 TKV_HOST_AUTO, TKV_HOST_PINNED_ALLOC, TKV_HOST_HUGE_ARENA = range(3)
+TKV_BF16, TKV_FP16, TKV_FP32, TKV_INT4 = range(4)
 
 # Every function the C ABI exports (include/tkv.h).
 EXPORTS = ("tkv_create", "tkv_destroy", "tkv_append", "tkv_prefetch", "tkv_decode_step",
            "tkv_retier", "tkv_get_scores", "tkv_set_scores", "tkv_get_tiers", "tkv_set_tiers",
            "tkv_get_row", "tkv_profile_begin", "tkv_profile_end", "tkv_sync", "tkv_get_stats",
            "tkv_status_string", "tkv_decode_dense_noalloc", "tkv_capture_begin", "tkv_capture_end",
-           "tkv_replay", "tkv_measure_host_link")
+           "tkv_replay", "tkv_measure_host_link", "tkv_rope", "tkv_paged_append", "tkv_paged_gather",
+           "tkv_paged_attention", "tkv_paged_attention_workspace")
 
 
 class TkvUnavailable(RuntimeError):
@@ -90,6 +92,21 @@ class ProfEntry(ctypes.Structure):
         return {"ms": self.ms, "count": int(self.count), "bytes": self.bytes}
 
 
+class RotaryDesc(ctypes.Structure):
+    """tkv_rotary (see include/tkv.h)."""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("max_positions", ctypes.c_int32), ("pairs", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 256)]
+
+
+class PagedDesc(ctypes.Structure):
+    """tkv_paged (see include/tkv.h)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("v_gain", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("kv_type", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -124,12 +141,20 @@ def load():
     lib.tkv_sync.argtypes = [vp]
     dp = ctypes.POINTER(ctypes.c_double)
     lib.tkv_measure_host_link.argtypes = [i32, ctypes.c_int64, dp, dp, dp]
+    i64, rot, pag = ctypes.c_int64, ctypes.POINTER(RotaryDesc), ctypes.POINTER(PagedDesc)
+    lib.tkv_rope.argtypes = [rot, vp, vp, i32, i64, i32, i32, i64, i64, i64, i64, vp, vp]
+    lib.tkv_paged_append.argtypes = [pag, rot, vp, vp, i32, i64, i64, i64, i64, i64, vp, vp, vp]
+    lib.tkv_paged_gather.argtypes = [pag, vp, vp, i32, i64, i64, i64, i64, i64, vp, vp, vp]
+    lib.tkv_paged_attention.argtypes = [pag, vp, vp, vp, i32, i64, i32, i64, i64, i64, i64, vp, i32, i32, i32,
+                                        ctypes.c_float, vp, i64, vp, vp]
+    lib.tkv_paged_attention_workspace.argtypes = [pag, i32, i32]
     lib.tkv_get_stats.argtypes = [vp, ctypes.POINTER(Stats)]
     lib.tkv_status_string.argtypes = [st]
     lib.tkv_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
         if name not in ("tkv_destroy", "tkv_status_string"):
             getattr(lib, name).restype = st
+    lib.tkv_paged_attention_workspace.restype = i64
     _lib = lib
     return lib
 
@@ -144,7 +169,9 @@ def _check(rc, where):
 
 
 def _ptr(x):
-    """Device pointer of a torch tensor, or an int address."""
+    """Device pointer of a torch tensor, or an int address; None is NULL."""
+    if x is None:
+        return None
     if hasattr(x, "data_ptr"):
         return ctypes.c_void_p(x.data_ptr())
     return ctypes.c_void_p(int(x))
@@ -248,6 +275,37 @@ def tkv_measure_host_link(device, nbytes):
     v = [ctypes.c_double(0.0) for _ in range(3)]
     rc = load().tkv_measure_host_link(int(device), int(nbytes), *(ctypes.byref(x) for x in v))
     return rc, {"h2d_ce_gbs": v[0].value, "h2d_sm_gbs": v[1].value, "d2h_ce_gbs": v[2].value}
+
+
+def tkv_rope(rotary, x, out, dtype, rows, heads, head_dim, x_strides, out_strides, status=None, stream=None):
+    """Rotary positions (see include/tkv.h): rotary a RotaryDesc, strides (row, head); returns the status."""
+    return load().tkv_rope(rotary, _ptr(x), _ptr(out), dtype, rows, heads, head_dim, *x_strides, *out_strides,
+                           _ptr(status), torch_stream_handle() if stream is None else stream)
+
+
+def tkv_paged_append(cache, rotary, k, v, dtype, rows, k_strides, v_strides, cu_tokens, status=None, stream=None):
+    """Rows into a paged cache (see include/tkv.h): cache a PagedDesc, rotary a RotaryDesc or None; returns the status."""
+    return load().tkv_paged_append(cache, rotary, _ptr(k), _ptr(v), dtype, rows, *k_strides, *v_strides, _ptr(cu_tokens),
+                                   _ptr(status), torch_stream_handle() if stream is None else stream)
+
+
+def tkv_paged_gather(cache, k, v, dtype, rows, k_strides, v_strides, cu_tokens, status=None, stream=None):
+    """Rows out of a paged cache (see include/tkv.h); returns the status."""
+    return load().tkv_paged_gather(cache, _ptr(k), _ptr(v), dtype, rows, *k_strides, *v_strides, _ptr(cu_tokens),
+                                   _ptr(status), torch_stream_handle() if stream is None else stream)
+
+
+def tkv_paged_attention_workspace(cache, num_q_heads, max_new):
+    """Bytes of workspace of tkv_paged_attention on the current device; 0: the arguments are refused."""
+    return load().tkv_paged_attention_workspace(cache, num_q_heads, max_new)
+
+
+def tkv_paged_attention(cache, q, out, lse, dtype, rows, num_q_heads, q_strides, out_strides, cu_tokens, max_new,
+                        max_len, window, scale, workspace, workspace_bytes, status=None, stream=None):
+    """Attention over a paged cache (see include/tkv.h); returns the status."""
+    return load().tkv_paged_attention(cache, _ptr(q), _ptr(out), _ptr(lse), dtype, rows, num_q_heads, *q_strides,
+                                      *out_strides, _ptr(cu_tokens), max_new, max_len, window, scale, _ptr(workspace),
+                                      workspace_bytes, _ptr(status), torch_stream_handle() if stream is None else stream)
 
 
 def tkv_sync(ctx):
@@ -400,3 +458,7 @@ class TieredKV:
 
     def set_tiers(self, t):
         self._check(tkv_set_tiers(self.ctx, np.asarray(t, dtype=np.uint8)), "tkv_set_tiers")
+
+
+# ------------------------------------------------- operators over a paged cache
+from .paged import PagedCache, Rotary, rope, rope_table  # noqa: E402,F401

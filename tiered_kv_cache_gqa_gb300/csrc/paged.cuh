@@ -1,0 +1,94 @@
+// Definitions shared by the operators over a caller-owned paged cache (append, gather, attention)
+// and the rotation of positions.
+//
+// 4-bit pages.  A page holds, for every KV head, page_size / 16 records of 16 positions:
+//   K codes [16][d/2] | K scales [16][d/16] | V codes [16][d/2] | V scales [d/16][16]
+// 18 d bytes: 2,304 at d = 128, 1,152 at d = 64.  A record is the unit that attention copies (one
+// contiguous, 128-byte aligned piece of memory for 16 keys and 16 values of a head) and the 16 rows
+// of one matrix instruction.  The V scales lie the other way round than the K scales: K's products
+// run over the channels of one position, V's over the positions of one channel, and each then finds
+// the scales that it multiplies with next to one another.
+// A code is q + 8 with q in -7..7; channel 2 j in the low half of byte j, 2 j + 1 in the high half.
+// The value is q * scale * gain: scale an E4M3 number >= 0 of a block of 16 channels, gain a power of
+// two or any other positive fp32 number of the KV head.  Uniform codes and not E2M1: they expand to
+// fp16, times their scale, with one logic and one fused multiply-add instruction a pair, exactly.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/tkv.h"
+
+namespace tkv {
+
+constexpr int kGroup = 16;   // positions of a record, channels of a block
+
+template <int D>
+struct Record {
+    static constexpr int k_codes = 0, k_scales = 8 * D, v_codes = 9 * D, v_scales = 17 * D, bytes = 18 * D;
+};
+
+template <typename T> __device__ __forceinline__ float to_float(T x);
+template <> __device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// 16 bytes as elements of T
+template <typename T>
+union Vec16 {
+    uint4 u;
+    T e[16 / sizeof(T)];
+};
+
+// One pair by its angle: (x0 + i x1)(c + i s), each product and each sum rounded once, so that the
+// rotation on its own and the one on the way into the cache give the same bits.
+__device__ __forceinline__ float2 rotate_pair(float x0, float x1, float2 cs) {
+    return make_float2(__fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y)),
+                       __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y)));
+}
+
+// (cos, sin) of pair j at position p; NaN outside the table, where *bad is set.
+__device__ __forceinline__ float2 table_at(const float2* table, int pairs, int max_positions, int p, int j,
+                                           float sign, bool* bad) {
+    if ((uint32_t)p >= (uint32_t)max_positions) {
+        *bad = true;
+        return make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+    }
+    float2 cs = __ldg(table + (int64_t)p * pairs + j);
+    cs.y *= sign;
+    return cs;
+}
+
+// The status word holds the largest code that a kernel met.
+__device__ __forceinline__ void raise_status(int32_t* status, int code) {
+    if (status) atomicMax(status, code);
+}
+
+// The sequence that row `row` of a step belongs to: cu[b] <= row < cu[b + 1]; -1 behind the last.
+__device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int row) {
+    if (row < __ldg(cu) || row >= __ldg(cu + batch)) return -1;
+    int lo = 0, hi = batch;   // cu[lo] <= row < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(cu + mid) <= row) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Host-side checks shared by the entry points; TKV_OK or TKV_EINVAL.
+tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions);
+tkv_status check_paged(const tkv_paged* c);
+// element (row, head, channel) -> memory: rows and heads do not overlap, strides >= 0
+bool strides_apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t width);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int dtype_size(int t) { return t == TKV_FP32 ? 4 : 2; }
+inline bool is_dtype(int t) { return t == TKV_BF16 || t == TKV_FP16 || t == TKV_FP32; }
+
+}  // namespace tkv

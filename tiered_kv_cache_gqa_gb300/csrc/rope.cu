@@ -1,0 +1,239 @@
+// Rotary positions with one or several axes: tkv_rope.
+//
+// Pair j of a head (of `pairs` rotated ones) turns by the angle of position p = positions[axis(j)][row]:
+//   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin
+// with cos and sin from the caller's table, row p, column j.  The rotation is orthogonal, so its
+// gradient is the rotation by the negated angle: the same kernel with the sine's sign turned.
+//
+// What bounds it is memory: every value is read and written once and costs three operations.  A thread
+// keeps the cosines and sines of its 16 bytes of a head in registers and walks over heads of its
+// row, so the table (8 bytes a pair, fp32) is read once a row and not once a head.
+#include <algorithm>
+
+#include "paged.cuh"
+
+using namespace tkv;
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RopeArgs {
+    const void* x;
+    void* out;
+    const float2* table;
+    const int32_t* positions;
+    int32_t* status;
+    int64_t rows, axis_stride, x_row, x_head, out_row, out_head;
+    int heads, head_dim, pairs, max_positions, num_axes, interleaved;
+    int lanes;       // heads that the threads of a row take at once
+    bool copy_rest;  // channels behind the rotated ones are copied (out is not x)
+    float sign;
+    uint8_t pair_axis[256];
+};
+
+// Whole 16-byte pieces: E = 16 / sizeof(T) elements.  Pieces of a head: with halves, piece i takes
+// channels [i E, i E + E) and their partners `pairs` further on; with adjacent pairs, its own E / 2
+// pairs.  Behind the rotated pieces come the copied ones.
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int E = 16 / sizeof(T);
+    constexpr int NP = INTERLEAVED ? E / 2 : E;   // pairs of a piece
+    __shared__ uint8_t axis_of[256];
+    if (a.num_axes > 1) {
+        axis_of[threadIdx.x] = a.pair_axis[threadIdx.x];
+        __syncthreads();
+    }
+    const int rotated = a.pairs / NP;
+    const int pieces = rotated + (a.copy_rest ? (a.head_dim - 2 * a.pairs) / E : 0);
+    const uint32_t per_row = (uint32_t)pieces * a.lanes;
+    const int64_t total = a.rows * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = i / per_row;
+        const uint32_t in_row = (uint32_t)(i - row * per_row);
+        const int lane = in_row / pieces, piece = in_row - lane * pieces;
+        const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
+        T* out = reinterpret_cast<T*>(a.out) + row * a.out_row;
+        if (piece >= rotated) {
+            const int at = 2 * a.pairs + (piece - rotated) * E;
+            for (int h = lane; h < a.heads; h += a.lanes)
+                *reinterpret_cast<uint4*>(out + h * a.out_head + at) = *reinterpret_cast<const uint4*>(x + h * a.x_head + at);
+            continue;
+        }
+        float2 cs[NP];
+        bool bad = false;
+        const int j0 = piece * NP;
+        if (a.num_axes == 1) {
+            const int p = __ldg(a.positions + row);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) cs[k] = table_at(a.table, a.pairs, a.max_positions, p, j0 + k, a.sign, &bad);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int p = __ldg(a.positions + axis_of[j0 + k] * a.axis_stride + row);
+                cs[k] = table_at(a.table, a.pairs, a.max_positions, p, j0 + k, a.sign, &bad);
+            }
+        }
+        if (bad) raise_status(a.status, TKV_EINVAL);
+#pragma unroll 2
+        for (int h = lane; h < a.heads; h += a.lanes) {
+            const T* xh = x + h * a.x_head;
+            T* oh = out + h * a.out_head;
+            if (INTERLEAVED) {
+                Vec16<T> v;
+                v.u = *reinterpret_cast<const uint4*>(xh + piece * E);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    const float2 y = rotate_pair(to_float(v.e[2 * k]), to_float(v.e[2 * k + 1]), cs[k]);
+                    v.e[2 * k] = from_float<T>(y.x);
+                    v.e[2 * k + 1] = from_float<T>(y.y);
+                }
+                *reinterpret_cast<uint4*>(oh + piece * E) = v.u;
+            } else {
+                Vec16<T> lo, hi;
+                lo.u = *reinterpret_cast<const uint4*>(xh + j0);
+                hi.u = *reinterpret_cast<const uint4*>(xh + a.pairs + j0);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    const float2 y = rotate_pair(to_float(lo.e[k]), to_float(hi.e[k]), cs[k]);
+                    lo.e[k] = from_float<T>(y.x);
+                    hi.e[k] = from_float<T>(y.y);
+                }
+                *reinterpret_cast<uint4*>(oh + j0) = lo.u;
+                *reinterpret_cast<uint4*>(oh + a.pairs + j0) = hi.u;
+            }
+        }
+    }
+}
+
+// Any alignment and any number of pairs: a thread takes one pair (or one copied channel) of a head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs a) {
+    const int rest = a.copy_rest ? a.head_dim - 2 * a.pairs : 0;
+    const uint32_t per_head = a.pairs + rest;
+    const int64_t total = a.rows * a.heads * per_head;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t rh = i / per_head;
+        const int j = (int)(i - rh * per_head);
+        const int64_t row = rh / a.heads;
+        const int h = (int)(rh - row * a.heads);
+        const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row + h * a.x_head;
+        T* out = reinterpret_cast<T*>(a.out) + row * a.out_row + h * a.out_head;
+        if (j >= a.pairs) {
+            out[a.pairs + j] = x[a.pairs + j];
+            continue;
+        }
+        bool bad = false;
+        const int p = __ldg(a.positions + (a.num_axes > 1 ? a.pair_axis[j] : 0) * a.axis_stride + row);
+        const float2 cs = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
+        if (bad) raise_status(a.status, TKV_EINVAL);
+        const int i0 = a.interleaved ? 2 * j : j, i1 = a.interleaved ? 2 * j + 1 : j + a.pairs;
+        const float2 y = rotate_pair(to_float(x[i0]), to_float(x[i1]), cs);
+        out[i0] = from_float<T>(y.x);
+        out[i1] = from_float<T>(y.y);
+    }
+}
+
+template <typename T>
+cudaError_t launch(RopeArgs& a, bool whole, cudaStream_t st) {
+    constexpr int E = 16 / sizeof(T);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t full = (int64_t)sms * 2048;   // threads that run at once
+    if (!whole) {
+        const int64_t total = a.rows * a.heads * (a.pairs + (a.copy_rest ? a.head_dim - 2 * a.pairs : 0));
+        const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)sms * 64);
+        rope_pairs_kernel<T><<<grid, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    const int pieces = a.pairs / (a.interleaved ? E / 2 : E) + (a.copy_rest ? (a.head_dim - 2 * a.pairs) / E : 0);
+    // A thread takes up to 8 heads of its row, which reads the table once for them, as long as two
+    // waves of threads are left; a short call takes one head a thread.
+    int per_thread = (int)std::min<int64_t>(8, std::max<int64_t>(1, a.rows * a.heads * pieces / (2 * full)));
+    a.lanes = (a.heads + per_thread - 1) / per_thread;
+    const int64_t total = a.rows * a.lanes * pieces;
+    const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)1 << 30);
+    if (a.interleaved)
+        rope_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
+    else
+        rope_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace tkv {
+
+bool strides_apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t width) {
+    if (row_stride < 0 || head_stride < 0) return false;
+    if (heads == 1) return rows == 1 || row_stride >= width;
+    if (rows == 1) return head_stride >= width;
+    if (row_stride >= head_stride) return head_stride >= width && row_stride >= (heads - 1) * head_stride + width;
+    return row_stride >= width && head_stride >= (rows - 1) * row_stride + width;
+}
+
+tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions) {
+    if (!r || !r->table || (reinterpret_cast<uintptr_t>(r->table) & 7u)) return TKV_EINVAL;
+    if (need_positions && !r->positions) return TKV_EINVAL;
+    if (r->max_positions < 1 || r->pairs < 1 || r->pairs > 256 || 2 * r->pairs > head_dim) return TKV_EINVAL;
+    if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->positions)) return TKV_EINVAL;
+    if (r->axis_stride < 0) return TKV_EINVAL;
+    for (int j = 0; j < r->pairs; ++j)
+        if (r->pair_axis[j] >= r->num_axes) return TKV_EINVAL;
+    return TKV_OK;
+}
+
+}  // namespace tkv
+
+extern "C" tkv_status tkv_rope(const tkv_rotary* rotary, const void* x, void* out, int32_t dtype, int64_t rows,
+                               int32_t heads, int32_t head_dim, int64_t x_row_stride, int64_t x_head_stride,
+                               int64_t out_row_stride, int64_t out_head_stride, int32_t* status, void* stream) {
+    if (!is_dtype(dtype) || rows < 0 || rows > (int64_t)1 << 40 || heads < 1 || head_dim < 2 || head_dim > 65536)
+        return TKV_EINVAL;
+    if (check_rotary(rotary, head_dim, true) != TKV_OK) return TKV_EINVAL;
+    if (rows == 0) return TKV_OK;
+    if (!x || !out || x_row_stride < 0 || x_head_stride < 0) return TKV_EINVAL;
+    const uintptr_t size = dtype_size(dtype);
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & (size - 1)) return TKV_EINVAL;
+    if (!strides_apart(rows, out_row_stride, heads, out_head_stride, head_dim)) return TKV_EINVAL;
+    const bool in_place = x == out;
+    if (in_place && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+        return TKV_EINVAL;
+    RopeArgs a{};
+    a.x = x;
+    a.out = out;
+    a.table = reinterpret_cast<const float2*>(rotary->table);
+    a.positions = rotary->positions;
+    a.status = status;
+    a.rows = rows;
+    a.axis_stride = rotary->axis_stride;
+    a.x_row = x_row_stride;
+    a.x_head = x_head_stride;
+    a.out_row = out_row_stride;
+    a.out_head = out_head_stride;
+    a.heads = heads;
+    a.head_dim = head_dim;
+    a.pairs = rotary->pairs;
+    a.max_positions = rotary->max_positions;
+    a.num_axes = rotary->num_axes;
+    a.interleaved = rotary->interleaved != 0;
+    a.copy_rest = !in_place && head_dim > 2 * rotary->pairs;
+    a.sign = rotary->inverse ? -1.0f : 1.0f;
+    for (int j = 0; j < 256; ++j) a.pair_axis[j] = j < rotary->pairs ? rotary->pair_axis[j] : 0;
+    // 16-byte pieces: every piece starts on a 16-byte boundary and holds whole pairs
+    const int64_t E = 16 / size;
+    const bool whole = aligned16(x) && aligned16(out) && x_row_stride % E == 0 && x_head_stride % E == 0 &&
+                       out_row_stride % E == 0 && out_head_stride % E == 0 &&
+                       a.pairs % (a.interleaved ? E / 2 : E) == 0 && (!a.copy_rest || (head_dim - 2 * a.pairs) % E == 0);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dtype == TKV_BF16   ? launch<__nv_bfloat16>(a, whole, st)
+                          : dtype == TKV_FP16 ? launch<__half>(a, whole, st)
+                                              : launch<float>(a, whole, st);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TKV_ECUDA;
+    }
+    return TKV_OK;
+}
