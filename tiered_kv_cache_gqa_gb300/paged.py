@@ -13,26 +13,26 @@ stream; nothing synchronises, and every call can be captured into a CUDA graph.
     cache.append(k, v, cu_tokens, rotary=rotary, positions=positions)
     out = cache.attend(q, cu_tokens)
 """
-import ctypes
 import math
 
-from . import (TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_OK, CUDA_STREAM_LEGACY, PagedDesc, RotaryDesc, TkvError,
+from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_OK, PagedDesc, RotaryDesc, TkvError,
                load)
 
-_torch = None
+_torch = _raw_stream = _current_device = _int32 = None
+_DTYPES = {}
 
 
 def _types():
-    """torch, imported at the first call (the package itself does not need it)."""
-    global _torch, _DTYPES
+    """torch, imported at the first use (the package itself does not need it)."""
+    global _torch, _raw_stream, _current_device, _int32
     if _torch is None:
         import torch
-        _DTYPES = {torch.bfloat16: TKV_BF16, torch.float16: TKV_FP16, torch.float32: TKV_FP32}
+        _DTYPES.update({torch.bfloat16: TKV_BF16, torch.float16: TKV_FP16, torch.float32: TKV_FP32})
+        _int32 = torch.int32
+        # the handle of a device's current stream and the current device, without an object around them
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         _torch = torch
     return _torch
-
-
-_DTYPES = {}
 
 
 def _refuse(where, why):
@@ -41,35 +41,34 @@ def _refuse(where, why):
     raise e
 
 
-def _need(ok, where, why):
-    if not ok:
-        _refuse(where, why)
-
-
+# The checks below run at every call, in front of kernels of a few microseconds: they build no text unless they refuse.
 def _on(x, where, what, dtype=None, dim=None, device=None):
-    """x is a CUDA tensor of that type and dimension on that device."""
-    torch = _types()
-    _need(isinstance(x, torch.Tensor) and x.is_cuda, where, "%s is not a CUDA tensor" % what)
-    _need(dtype is None or x.dtype == dtype, where, "%s is %s, not %s" % (what, x.dtype, dtype))
-    _need(dim is None or x.dim() == dim, where, "%s has %d dimensions, not %s" % (what, x.dim(), dim))
-    _need(device is None or x.device == device, where, "%s is on %s, not on %s" % (what, x.device, device))
+    """x is a CUDA tensor, of that type and dimension, on that device."""
+    if not isinstance(x, _torch.Tensor) or not x.is_cuda:
+        _refuse(where, "%s is not a CUDA tensor" % what)
+    if dtype is not None and x.dtype != dtype:
+        _refuse(where, "%s is %s, not %s" % (what, x.dtype, dtype))
+    if dim is not None and x.dim() != dim:
+        _refuse(where, "%s has %d dimensions, not %s" % (what, x.dim(), dim))
+    if device is not None and x.get_device() != device.index:
+        _refuse(where, "%s is on %s, not on %s" % (what, x.device, device))
 
 
-def _int32(x, where, what, shape, device):
-    torch = _types()
-    _on(x, where, what, torch.int32, None, device)
-    _need(tuple(x.shape) == tuple(shape) and x.is_contiguous(), where,
-          "%s has to be a contiguous int32 tensor %s, not %s" % (what, list(shape), list(x.shape)))
+def _is_int32(x, where, what, shape, device):
+    """x is a contiguous int32 tensor of that shape."""
+    _on(x, where, what, _int32, None, device)
+    if x.shape != shape or not x.is_contiguous():
+        _refuse(where, "%s has to be a contiguous int32 tensor %s, not %s" % (what, list(shape), list(x.shape)))
 
 
 def _call(fn, where, device, *args):
     """The C call on the tensors' device, behind what its current stream holds."""
-    torch = _torch
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream or CUDA_STREAM_LEGACY)
+    i = device.index
+    if _current_device() != i:
+        with _torch.cuda.device(i):
+            rc = fn(*args, _raw_stream(i) or CUDA_STREAM_LEGACY)
     else:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream or CUDA_STREAM_LEGACY)
+        rc = fn(*args, _raw_stream(i) or CUDA_STREAM_LEGACY)
     if rc != TKV_OK:
         raise TkvError(rc, where)
 
@@ -77,8 +76,9 @@ def _call(fn, where, device, *args):
 def _status_ptr(status, where, device):
     if status is None:
         return None
-    _on(status, where, "status", _types().int32, None, device)
-    _need(status.numel() >= 1, where, "status is empty")
+    _on(status, where, "status", _int32, None, device)
+    if status.numel() < 1:
+        _refuse(where, "status is empty")
     return status.data_ptr()
 
 
@@ -89,12 +89,14 @@ def rope_table(max_positions, rot_dim, base=10000.0, device="cuda", freq=None):
     numbers: scaled or repeated ladders)."""
     torch = _types()
     pairs = rot_dim // 2
-    _need(rot_dim >= 2 and rot_dim % 2 == 0 and max_positions >= 1, "rope_table", "rot_dim is even, max_positions >= 1")
+    if rot_dim < 2 or rot_dim % 2 or max_positions < 1:
+        _refuse("rope_table", "rot_dim is %s, max_positions %s: an even number, at least 1" % (rot_dim, max_positions))
     if freq is None:
         freq = float(base) ** (-torch.arange(pairs, dtype=torch.float64, device=device) / pairs)
     else:
         freq = torch.as_tensor(freq, dtype=torch.float64, device=device)
-        _need(tuple(freq.shape) == (pairs,), "rope_table", "freq has one number a pair")
+        if freq.shape != (pairs,):
+            _refuse("rope_table", "freq is %s, not one number a pair" % list(freq.shape))
     angle = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * freq
     return torch.stack([angle.cos(), angle.sin()], dim=-1).float().contiguous()
 
@@ -108,10 +110,11 @@ class Rotary:
     def __init__(self, table, pair_axis=None, interleaved=False):
         torch, w = _types(), "Rotary"
         _on(table, w, "table", torch.float32, 3)
-        _need(table.is_contiguous() and table.shape[2] == 2 and table.shape[0] >= 1 and 1 <= table.shape[1] <= 256, w,
-              "table is contiguous [max_positions, pairs <= 256, 2], not %s" % list(table.shape))
+        if not table.is_contiguous() or table.shape[2] != 2 or table.shape[0] < 1 or not 1 <= table.shape[1] <= 256:
+            _refuse(w, "table is contiguous [max_positions, pairs <= 256, 2], not %s" % list(table.shape))
         axes = [0] * table.shape[1] if pair_axis is None else [int(x) for x in pair_axis]
-        _need(len(axes) == table.shape[1] and all(0 <= x < 4 for x in axes), w, "pair_axis has an axis 0 .. 3 for each pair")
+        if len(axes) != table.shape[1] or not all(0 <= x < 4 for x in axes):
+            _refuse(w, "pair_axis has an axis 0 .. 3 for each pair")
         self.table, self.num_axes, self.pairs = table, max(axes) + 1, table.shape[1]
         self.device = table.device
         self._forward, self._inverse = RotaryDesc(), RotaryDesc()
@@ -124,15 +127,19 @@ class Rotary:
         """A descriptor with these positions (a copy: calls from several threads do not share one)."""
         d = RotaryDesc.from_buffer_copy(self._inverse if inverse else self._forward)
         if positions is None:
-            _need(self.num_axes == 1, where, "positions are needed with %d axes" % self.num_axes)
+            if self.num_axes > 1:
+                _refuse(where, "positions are needed with %d axes" % self.num_axes)
             return d
-        _on(positions, where, "positions", _torch.int32, None, self.device)
-        shape = tuple(positions.shape)
-        ok = shape == (rows,) and self.num_axes == 1 or len(shape) == 2 and shape[0] >= self.num_axes and shape[1] == rows
-        _need(ok and (rows <= 1 or positions.stride(-1) == 1), where,
-              "positions are int32 [%d, %d], rows next to one another, not %s" % (self.num_axes, rows, list(shape)))
+        _on(positions, where, "positions", _int32, None, self.device)
+        shape, strides = positions.shape, positions.stride()
+        if len(shape) == 1:
+            ok, d.axis_stride = shape[0] == rows and self.num_axes == 1, rows
+        else:
+            ok = len(shape) == 2 and shape[0] >= self.num_axes and shape[1] == rows
+            d.axis_stride = strides[0] if ok else 0
+        if not ok or (rows > 1 and strides[-1] != 1):
+            _refuse(where, "positions are int32 [%d, %d], rows next to one another, not %s" % (self.num_axes, rows, list(shape)))
         d.positions = positions.data_ptr()
-        d.axis_stride = positions.stride(0) if len(shape) == 2 else rows
         return d
 
 
@@ -145,21 +152,27 @@ def rope(x, rotary, positions, out=None, inverse=False, status=None):
     torch = _types()
     _on(x, w, "x", None, 3)
     dt = _DTYPES.get(x.dtype)
-    rows, heads, d = x.shape
-    _need(dt is not None, w, "x is %s: bf16, fp16 or fp32" % x.dtype)
-    _need(isinstance(rotary, Rotary) and rotary.device == x.device, w, "rotary is not a Rotary on %s" % x.device)
-    _need(d <= 1 or x.stride(2) == 1, w, "the channels of x are not contiguous")
+    if dt is None:
+        _refuse(w, "x is %s: bf16, fp16 or fp32" % x.dtype)
+    if not isinstance(rotary, Rotary) or rotary.device.index != x.get_device():
+        _refuse(w, "rotary is not a Rotary on %s" % x.device)
+    if positions is None:
+        _refuse(w, "positions are needed")
+    shape, xs = x.shape, x.stride()
+    rows, heads, d = shape
     if out is None:
-        out = torch.empty((rows, heads, d), dtype=x.dtype, device=x.device)
-    else:
-        _on(out, w, "out", x.dtype, 3, x.device)
-        _need(out.shape == x.shape and (d <= 1 or out.stride(2) == 1), w, "out is not like x")
+        out = torch.empty(shape, dtype=x.dtype, device=rotary.device)
+    elif out is not x:
+        _on(out, w, "out", x.dtype, 3, rotary.device)
+        if out.shape != shape:
+            _refuse(w, "out is %s, x is %s" % (list(out.shape), list(shape)))
+    os_ = out.stride()
+    if d > 1 and (xs[2] != 1 or os_[2] != 1):
+        _refuse(w, "the channels of x and out have to be contiguous")
     desc = rotary._desc(positions, rows, w, inverse)
-    _need(positions is not None, w, "positions are needed")
-    xs, os_ = x.stride(), out.stride()
     if rows:
-        _call(load().tkv_rope, w, x.device, desc, x.data_ptr(), out.data_ptr(), dt, rows, heads, d, xs[0], xs[1], os_[0],
-              os_[1], _status_ptr(status, w, x.device))
+        _call(load().tkv_rope, w, rotary.device, desc, x.data_ptr(), out.data_ptr(), dt, rows, heads, d, xs[0], xs[1], os_[0],
+              os_[1], _status_ptr(status, w, rotary.device))
     return out
 
 
@@ -177,28 +190,34 @@ class PagedCache:
     def __init__(self, pages, page_table, lengths, k_gain=None, v_gain=None):
         torch, w = _types(), "PagedCache"
         _on(pages, w, "pages")
-        _need(pages.is_contiguous() and pages.numel() > 0, w, "pages is not contiguous, or empty")
+        if not pages.is_contiguous() or pages.numel() == 0:
+            _refuse(w, "pages is not contiguous, or empty")
         c = PagedDesc()
         if pages.dtype == torch.uint8:
-            _need(pages.dim() == 4 and pages.shape[3] in (18 * 64, 18 * 128), w,
-                  "4-bit pages are [num_pages, Hkv, page_size / 16, 18 d], d 64 or 128, not %s" % list(pages.shape))
+            if pages.dim() != 4 or pages.shape[3] not in (18 * 64, 18 * 128):
+                _refuse(w, "4-bit pages are [num_pages, Hkv, page_size / 16, 18 d], d 64 or 128, not %s" % list(pages.shape))
             c.kv_type, c.head_dim, c.page_size = TKV_INT4, pages.shape[3] // 18, pages.shape[2] * 16
         else:
-            _need(pages.dtype in (torch.bfloat16, torch.float16) and pages.dim() == 5 and pages.shape[2] == 2, w,
-                  "16-bit pages are bf16 or fp16 [num_pages, Hkv, 2, page_size, d], not %s %s" % (pages.dtype, list(pages.shape)))
-            _need(k_gain is None and v_gain is None, w, "gains belong to 4-bit pages")
+            if pages.dtype not in (torch.bfloat16, torch.float16) or pages.dim() != 5 or pages.shape[2] != 2:
+                _refuse(w, "16-bit pages are bf16 or fp16 [num_pages, Hkv, 2, page_size, d], not %s %s" % (pages.dtype, list(pages.shape)))
+            if k_gain is not None or v_gain is not None:
+                _refuse(w, "gains belong to 4-bit pages")
             c.kv_type, c.head_dim, c.page_size = _DTYPES[pages.dtype], pages.shape[4], pages.shape[3]
-        _need(c.head_dim in (64, 128), w, "head_dim is %d: 64 or 128" % c.head_dim)
-        _need(16 <= c.page_size <= 65536 and c.page_size & (c.page_size - 1) == 0, w,
-              "page_size is %d: a power of two from 16" % c.page_size)
+        if c.head_dim not in (64, 128):
+            _refuse(w, "head_dim is %d: 64 or 128" % c.head_dim)
+        if not 16 <= c.page_size <= 65536 or c.page_size & (c.page_size - 1):
+            _refuse(w, "page_size is %d: a power of two, 16 .. 65536" % c.page_size)
         _on(page_table, w, "page_table", torch.int32, 2, pages.device)
-        _need(page_table.is_contiguous() and page_table.numel() > 0, w, "page_table is not contiguous, or empty")
-        _int32(lengths, w, "lengths", (page_table.shape[0],), pages.device)
-        _need(page_table.shape[1] * c.page_size <= 1 << 30, w, "a sequence has at most 2^30 positions")
+        if not page_table.is_contiguous() or page_table.numel() == 0:
+            _refuse(w, "page_table is not contiguous, or empty")
+        _is_int32(lengths, w, "lengths", (page_table.shape[0],), pages.device)
+        if page_table.shape[1] * c.page_size > 1 << 30:
+            _refuse(w, "a sequence has at most 2^30 positions")
         for name, g in (("k_gain", k_gain), ("v_gain", v_gain)):
             if g is not None:
                 _on(g, w, name, torch.float32, 1, pages.device)
-                _need(g.shape[0] == pages.shape[1] and g.is_contiguous(), w, "%s has one number a KV head" % name)
+                if g.shape[0] != pages.shape[1] or not g.is_contiguous():
+                    _refuse(w, "%s has one number a KV head" % name)
         c.pages, c.page_table, c.lengths = pages.data_ptr(), page_table.data_ptr(), lengths.data_ptr()
         c.k_gain = None if k_gain is None else k_gain.data_ptr()
         c.v_gain = None if v_gain is None else v_gain.data_ptr()
@@ -207,7 +226,8 @@ class PagedCache:
         self.pages, self.page_table, self.lengths, self.k_gain, self.v_gain = pages, page_table, lengths, k_gain, v_gain
         self.device, self.num_kv_heads, self.head_dim, self.page_size = pages.device, c.num_kv_heads, c.head_dim, c.page_size
         self.batch, self.max_pages, self.is_int4 = c.batch, c.max_pages, c.kv_type == TKV_INT4
-        self._c, self._workspace = c, {}
+        # what each call reads of the descriptor, without a ctypes access
+        self._c, self._workspace, self._kv_type, self._cu_shape = c, {}, c.kv_type, (c.batch + 1,)
 
     @classmethod
     def empty(cls, num_pages, page_table, lengths, *, num_kv_heads, head_dim, page_size, dtype="int4", k_gain=None, v_gain=None):
@@ -223,34 +243,37 @@ class PagedCache:
         """x [rows, heads, d] of a 16-bit type that fits the pages, 16-byte pieces; its element type."""
         _on(x, where, what, None, 3, self.device)
         dt = _DTYPES.get(x.dtype)
-        _need(dt in (TKV_BF16, TKV_FP16) and (self.is_int4 or dt == self._c.kv_type), where,
-              "%s is %s, the pages are %s" % (what, x.dtype, self.pages.dtype))
-        _need(x.shape[1] == heads and x.shape[2] == self.head_dim, where,
-              "%s is %s, not [rows, %d, %d]" % (what, list(x.shape), heads, self.head_dim))
+        if dt == TKV_FP32 or dt is None or (not self.is_int4 and dt != self._kv_type):
+            _refuse(where, "%s is %s, the pages are %s" % (what, x.dtype, self.pages.dtype))
+        if x.shape[2] != self.head_dim or (heads is not None and x.shape[1] != heads):
+            _refuse(where, "%s is %s, not [rows, %s, %d]" % (what, list(x.shape), heads or "Hq", self.head_dim))
         self._pieces(x, where, what)
         return dt
 
     def _pieces(self, x, where, what):
         s = x.stride()
         e = 16 // x.element_size()
-        _need(s[2] == 1 and not (s[0] % e or s[1] % e or x.data_ptr() % 16), where,
-              "%s has to lie in 16-byte pieces: contiguous channels, aligned rows and heads" % what)
+        if s[2] != 1 or s[0] % e or s[1] % e or x.data_ptr() % 16:
+            _refuse(where, "%s has to lie in 16-byte pieces: contiguous channels, aligned rows and heads" % what)
 
     def append(self, k, v, cu_tokens, rotary=None, positions=None, status=None):
         """Writes k, v [rows, Hkv, d] (bf16 or fp16) to their places, k rotated on the way if `rotary` is given:
         by positions (int32 [rows] or [axes, rows]), or by the places in the cache if None."""
         w = "append"
         dt = self._rows(k, w, "k", self.num_kv_heads)
-        _need(self._rows(v, w, "v", self.num_kv_heads) == dt and v.shape[0] == k.shape[0], w, "v is not like k")
-        _int32(cu_tokens, w, "cu_tokens", (self.batch + 1,), self.device)
         rows = k.shape[0]
+        if self._rows(v, w, "v", self.num_kv_heads) != dt or v.shape[0] != rows:
+            _refuse(w, "v is not like k")
+        _is_int32(cu_tokens, w, "cu_tokens", self._cu_shape, self.device)
         desc = None
         if rotary is not None:
-            _need(isinstance(rotary, Rotary) and rotary.device == self.device, w, "rotary is not a Rotary on %s" % self.device)
-            _need(2 * rotary.pairs <= self.head_dim, w, "rotary turns %d channels of %d" % (2 * rotary.pairs, self.head_dim))
+            if not isinstance(rotary, Rotary) or rotary.device != self.device:
+                _refuse(w, "rotary is not a Rotary on %s" % self.device)
+            if 2 * rotary.pairs > self.head_dim:
+                _refuse(w, "rotary turns %d channels of %d" % (2 * rotary.pairs, self.head_dim))
             desc = rotary._desc(positions, rows, w)
-        else:
-            _need(positions is None, w, "positions without rotary")
+        elif positions is not None:
+            _refuse(w, "positions without rotary")
         if rows:
             ks, vs = k.stride(), v.stride()
             _call(load().tkv_paged_append, w, self.device, self._c, desc, k.data_ptr(), v.data_ptr(), dt, rows, ks[0], ks[1],
@@ -263,18 +286,25 @@ class PagedCache:
         lengths: the ends of the ranges (the cache's own lengths if None).  k, v: tensors to write to."""
         w = "gather"
         torch = _types()
-        _int32(cu_tokens, w, "cu_tokens", (self.batch + 1,), self.device)
+        _is_int32(cu_tokens, w, "cu_tokens", self._cu_shape, self.device)
         shape = (int(rows), self.num_kv_heads, self.head_dim)
-        _need(rows >= 0 and (k is None) == (v is None), w, "rows >= 0; k and v come together")
+        if rows < 0 or (k is None) != (v is None):
+            _refuse(w, "rows is at least 0; k and v come together")
         if k is None:
-            k, v = (torch.empty(shape, dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
-        for name, x in (("k", k), ("v", v)):
-            _on(x, w, name, dtype or k.dtype, 3, self.device)
-            _need(tuple(x.shape) == shape and x.dtype in _DTYPES, w, "%s is not bf16, fp16 or fp32 %s" % (name, list(shape)))
-            self._pieces(x, w, name)
+            dtype = torch.bfloat16 if dtype is None else dtype
+            if dtype not in _DTYPES:
+                _refuse(w, "dtype is %s: bf16, fp16 or fp32" % dtype)
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+            v = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            for name, x in (("k", k), ("v", v)):
+                _on(x, w, name, k.dtype if dtype is None else dtype, 3, self.device)
+                if x.shape != shape or x.dtype not in _DTYPES:
+                    _refuse(w, "%s is not bf16, fp16 or fp32 %s" % (name, list(shape)))
+                self._pieces(x, w, name)
         c = self._c
         if lengths is not None:
-            _int32(lengths, w, "lengths", (self.batch,), self.device)
+            _is_int32(lengths, w, "lengths", (self.batch,), self.device)
             c = PagedDesc.from_buffer_copy(c)
             c.lengths = lengths.data_ptr()
         if rows:
@@ -293,27 +323,30 @@ class PagedCache:
         scale: 1 / sqrt(d) if None.  out, lse: tensors to write to (rows behind cu_tokens[batch] stay as they were)."""
         w = "attend"
         torch = _types()
-        _on(q, w, "q", None, 3, self.device)
-        rows, hq, d = q.shape
-        _need(hq >= 1 and hq % self.num_kv_heads == 0, w, "%d query heads over %d KV heads" % (hq, self.num_kv_heads))
-        dt = self._rows(q, w, "q", hq)
-        _int32(cu_tokens, w, "cu_tokens", (self.batch + 1,), self.device)
+        dt = self._rows(q, w, "q", None)
+        shape = q.shape
+        rows, hq, d = shape
+        if hq < 1 or hq % self.num_kv_heads:
+            _refuse(w, "%d query heads over %d KV heads" % (hq, self.num_kv_heads))
+        _is_int32(cu_tokens, w, "cu_tokens", self._cu_shape, self.device)
         max_new = max(1, -(-rows // self.batch)) if max_new is None else int(max_new)
         max_len = self.max_pages * self.page_size if max_len is None else int(max_len)
         window = int(window)
-        _need(max_new >= 1 and window >= 0, w, "max_new >= 1, window >= 0")
-        _need(window < 1 << 31 and max_new < 1 << 31, w, "window and max_new are int32")
+        if not 1 <= max_new < 1 << 31 or not 0 <= window < 1 << 31:
+            _refuse(w, "max_new is %d, window %d: int32, at least 1 and 0" % (max_new, window))
         max_len = min(max(1, max_len), (1 << 31) - 1)
         scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
         if out is None:
-            out = torch.empty((rows, hq, d), dtype=q.dtype, device=self.device)
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
         else:
             _on(out, w, "out", q.dtype, 3, self.device)
-            _need(out.shape == q.shape, w, "out is %s, q is %s" % (list(out.shape), list(q.shape)))
+            if out.shape != shape:
+                _refuse(w, "out is %s, q is %s" % (list(out.shape), list(shape)))
             self._pieces(out, w, "out")
         if lse is not None:
             _on(lse, w, "lse", torch.float32, 2, self.device)
-            _need(tuple(lse.shape) == (rows, hq) and lse.is_contiguous(), w, "lse is a contiguous [%d, %d]" % (rows, hq))
+            if lse.shape != (rows, hq) or not lse.is_contiguous():
+                _refuse(w, "lse is a contiguous [%d, %d]" % (rows, hq))
         elif return_lse:
             lse = torch.empty((rows, hq), dtype=torch.float32, device=self.device)
         if rows:
