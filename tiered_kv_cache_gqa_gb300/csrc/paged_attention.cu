@@ -12,8 +12,8 @@
 // operation is bound by memory (at G = 8 and 4 bits, 28 operations a byte), so mma.sync is enough.
 //
 // 4 bits to fp16, exactly.  (w & 0x000F000F) | 0x64006400 is the pair (1024 + n, 1024 + n') of two codes
-// n = q + 8, and with 0x00F000F0 the pair (1024 + 16 n, ...); one fused multiply-add with s = scale / 16
-// gives (1024 + n) s - 1032 s = q s (and (1024 + 16 n) s/16 - 72 s).  Every operand and result is
+// n = q + 8, and (w & 0x00F000F0) | 0x54005400 the pair (64 + n, 64 + n'); one fused multiply-add with
+// s = scale / 16 gives (1024 + n) s - 1032 s = q s (and (64 + n) s - 72 s).  Every operand and result is
 // exact in fp16: scale has 4 bits, 129 * 15 < 2^11, and 1032 * 448 / 16 is below its largest number.
 // So K and V enter the products as stored; what is rounded is p (to fp16, 2^-11) and, for rows in
 // bf16 of a wide range, what lies 2^-29 below a row's largest channel (q is scaled by a power of two).
@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "tkv_internal.cuh"
@@ -43,6 +44,7 @@ constexpr int kMinUnits = 2;            // of a share: below, joining costs more
 constexpr int kWholeItems = 512;        // up to this length a CTA takes whole items, and nothing is joined
 constexpr float kTop = 15.0f;           // p = 2^(z - m) <= 2^15; in fp16 the smallest is 2^-24
 constexpr float kLift = 5.0f;           // a new reference lies this far below the maximum: 10 are left to grow
+constexpr float kLowest = -3.402823466e38f;   // a reference before anything is seen: 2^(-inf - it) = 0, no NaN
 constexpr int kSpinLimit = 1 << 16;     // tries of a wait, each of which the hardware suspends for a while
 
 enum PageKind { kInt4, kBf16, kFp16 };
@@ -259,7 +261,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     int b = (int)scan[kWarps];
     int64_t in_seq = scan[kWarps + 1];
     Seq s = sequence<R>(a, b);
-    uint32_t step = 0;   // tiles that this warp has taken from its ring, over all segments
+    // the ring, over all segments: the stage of the next tile, and the parity that its barrier ends with
+    int stage = 0, parity = 0;
+    auto after = [](int st, int k) { return st + k >= S ? st + k - S : st + k; };
+    const int64_t page_bytes = (int64_t)a.c.num_kv_heads * (KIND == kInt4 ? (a.c.page_size >> 4) * Rec::bytes : a.c.page_size * 4 * D);
+    const int in_page = a.c.page_size - 1;
+    const uint32_t pages = (uint32_t)min(a.c.num_pages, (int64_t)0x7FFFFFFF);
     bool failed = false;
 
     while (u < u1) {
@@ -300,17 +307,15 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             const int p = begin + t * TP + (KIND == kInt4 ? (lane & 1) * 16 : 0);
             page_next = (t < tiles_here && p < end) ? __ldg(table + (p >> a.page_shift)) : -2;
         };
-        auto issue = [&](int t, uint32_t at) {
-            const int st = at % S;
+        const uint8_t* head_pages = reinterpret_cast<const uint8_t*>(a.c.pages) + page_bytes / a.c.num_kv_heads * h;
+        auto issue = [&](int t, int st) {
             if (KIND == kInt4) {
                 if (t < tiles_here && lane < 2) {
                     const int p = begin + t * TP + lane * 16;
-                    const bool ok = page_next >= 0 && page_next < a.c.num_pages;
-                    if (ok) {
-                        const uint8_t* src = reinterpret_cast<const uint8_t*>(a.c.pages) +
-                            (((int64_t)page_next * a.c.num_kv_heads + h) * (a.c.page_size >> 4) + ((p & (a.c.page_size - 1)) >> 4)) * Rec::bytes;
+                    if ((uint32_t)page_next < pages) {
                         mbar_arrive_expect(bar0 + 8 * st, Rec::bytes);
-                        bulk_copy(ring_s + st * TB + lane * Rec::bytes, src, Rec::bytes, bar0 + 8 * st);
+                        bulk_copy(ring_s + st * TB + lane * Rec::bytes,
+                                  head_pages + page_next * page_bytes + ((p & in_page) >> 4) * Rec::bytes, Rec::bytes, bar0 + 8 * st);
                         bad_bits &= ~(1u << st);
                     } else {
                         mbar_arrive(bar0 + 8 * st);
@@ -321,17 +326,16 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             } else {
                 if (t < tiles_here) {
                     const int p = begin + t * TP;
-                    const bool ok = page_next >= 0 && page_next < a.c.num_pages;
+                    const bool ok = (uint32_t)page_next < pages;
                     if (!ok && lane == 0) raise_status(a.status, TKV_ECAPACITY);
                     if (ok) bad_bits &= ~(1u << st); else bad_bits |= 1u << st;
                     constexpr int CH = D / 8;            // 16-byte pieces of a row, stored at piece ^ (row & 7)
-                    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.c.pages) +
-                        (((int64_t)(ok ? page_next : 0) * a.c.num_kv_heads + h) * 2 * a.c.page_size + (p & (a.c.page_size - 1))) * (2 * D);
+                    const uint8_t* src = head_pages + (ok ? page_next * page_bytes : 0) + (p & in_page) * (2 * D);
                     const int64_t v_off = (int64_t)a.c.page_size * (2 * D);
 #pragma unroll
                     for (int i = 0; i < 16 * CH / 32; ++i) {
                         const int row = (i * 32 + lane) / CH, piece = lane % CH;
-                        const int n = ok && p + row < end ? 16 : 0;      // absent rows are zeros: p = 0 meets no NaN
+                        const int n = ok && p + row < end ? 16 : 0;      // absent rows are zeros
                         const uint32_t dst = ring_s + st * TB + row * (2 * D) + ((piece ^ (row & 7)) << 4);
                         cp_async16(dst, src + row * (2 * D) + piece * 16, n);
                         cp_async16(dst + 16 * D * 2, src + v_off + row * (2 * D) + piece * 16, n);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         look_up(warp);
 #pragma unroll 1
         for (int k = 0; k < S - 1; ++k) {
-            issue(warp + k * kWarps, step + k);
+            issue(warp + k * kWarps, after(stage, k));
             look_up(warp + (k + 1) * kWarps);
         }
 
@@ -409,20 +413,20 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         float o[NT][KM][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = kLowest;
             l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KM; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
         }
 #pragma unroll 1
-        for (int t = warp; t < tiles_here; t += kWarps, ++step) {
-            const int st = step % S;
+        for (int t = warp; t < tiles_here; t += kWarps) {
+            const int st = stage;
             // the slot that the last tile left is filled before this one is waited for
-            issue(t + (S - 1) * kWarps, step + S - 1);
+            issue(t + (S - 1) * kWarps, after(st, S - 1));
             look_up(t + S * kWarps);
             uint32_t bad;
             if (KIND == kInt4) {
-                if (!failed && !mbar_wait(bar0 + 8 * st, (step / S) & 1)) {
+                if (!failed && !mbar_wait(bar0 + 8 * st, parity)) {
                     failed = true;
                     if (lane == 0) raise_status(a.status, TKV_ETIMEOUT);
                 }
@@ -435,10 +439,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 bad = (bad_bits >> st) & 1 ? 3 : 0;
             }
             const int p0 = begin + t * TP;
-            const bool plain = !bad && p0 + TP - 1 <= all_until && p0 >= all_from;
+            const bool plain = !bad && p0 + TP - 1 <= all_until && p0 >= all_from;   // every row sees every position
             const uint8_t* tile_at = ring + st * TB;
             const uint32_t tile_s = ring_s + st * TB;
             constexpr int NG = TP / 16;
+            auto tile = [&](auto whole_tile) {
+            constexpr bool kPlain = decltype(whole_tile)::value;
             // The lane's four V positions of a group (the columns of its fragments): bit i set if position i lies in [from, to).
             constexpr bool kPermuted = KIND == kInt4;
             const int v0 = kPermuted ? (2 * cq) ^ (cq & 1) : 2 * cq, v1 = kPermuted ? (2 * cq + 1) ^ (cq & 1) : 2 * cq + 1;
@@ -451,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 }
                 return bits;
             };
-            // acc += V^T P^T of group g, V taken as 0 where `keep` has no bit (not looked at if `all`); with `look`
+            // acc += V^T P^T of group g, V taken as 0 where `keep` has no bit (a plain tile has them all); with `look`
             // nothing is added: whether the lane's part of V, so masked, holds an infinity or a NaN.
-            auto v_step = [&](int g, bool all, uint32_t keep, const uint32_t (&ph)[NT][2], const uint32_t (&plo)[NT][2],
+            auto v_step = [&](int g, uint32_t keep, const uint32_t (&ph)[NT][2], const uint32_t (&plo)[NT][2],
                               float (&acc)[NT][KM][4], bool look) -> bool {
                 const uint32_t m0 = (keep & 1 ? 0xFFFFu : 0u) | (keep & 2 ? 0xFFFF0000u : 0u);
                 const uint32_t m1 = (keep & 4 ? 0xFFFFu : 0u) | (keep & 8 ? 0xFFFF0000u : 0u);
@@ -463,15 +469,14 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                     // scales of the two position pairs, in the order of the slots
                     const uint8_t* vs = rec + Rec::v_scales + (D == 128 ? r : r >> 1) * 16 + 2 * cq;
                     const uint32_t swap = cq & 1 ? 0x1032u : 0x3210u;
-                    __half2 s_lo[2], s_hi[2], n_lo[2], n_hi[2];
+                    __half2 s_lo[2], n_lo[2], n_hi[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t x = half2_bits(__half2(__nv_cvt_fp8x2_to_halfraw2(*reinterpret_cast<const uint16_t*>(vs + 8 * i), __NV_E4M3)));
                         x = __byte_perm(x, 0, swap);
-                        if (!all) x &= i ? m1 : m0;
+                        if (!kPlain) x &= i ? m1 : m0;
                         odd |= (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
                         s_lo[i] = __hmul2(bits_half2(x), __half2half2(__float2half(0.0625f)));
-                        s_hi[i] = __hmul2(s_lo[i], __half2half2(__float2half(0.0625f)));
                         n_lo[i] = __hmul2(s_lo[i], __half2half2(__float2half(-1032.0f)));
                         n_hi[i] = __hmul2(s_lo[i], __half2half2(__float2half(-72.0f)));
                     }
@@ -500,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t f0 = half2_bits(__hfma2(bits_half2((x & 0x000F000Fu) | 0x64006400u), s_lo[0], n_lo[0]));
-                                const uint32_t f1 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x64006400u), s_hi[0], n_hi[0]));
+                                const uint32_t f1 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x54005400u), s_lo[0], n_hi[0]));
                                 const uint32_t f2 = half2_bits(__hfma2(bits_half2((y & 0x000F000Fu) | 0x64006400u), s_lo[1], n_lo[1]));
-                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x64006400u), s_hi[1], n_hi[1]));
+                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x54005400u), s_lo[1], n_hi[1]));
                                 const int j = 4 * wi + 2 * half + i;   // rows r and r + 8: channels (D / 8) r + 2 j and + 1
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                         uint32_t f[4];
                         const int row = (lane & 7) + ((lane >> 4) << 3), piece = 2 * j + ((lane >> 3) & 1);
                         ldmatrix4_trans(f, tile_s + 16 * D * 2 + row * (2 * D) + ((piece ^ (row & 7)) << 4));
-                        if (!all) {
+                        if (!kPlain) {
                             f[0] &= m0; f[1] &= m0; f[2] &= m1; f[3] &= m1;
                         }
                         if (look) {
@@ -575,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                     }
 #pragma unroll
                     for (int k = 0; k < W / 2; ++k) {
-                        const __half2 s16 = __half2half2(__float2half(0.0625f));
-                        const __half2 a_lo = sa[k], a_hi = __hmul2(sa[k], s16), b_lo = sb[k], b_hi = __hmul2(sb[k], s16);
+                        const __half2 a_lo = sa[k], b_lo = sb[k];
                         const __half2 a_lo0 = __hmul2(a_lo, __half2half2(__float2half(-1032.0f))), a_hi0 = __hmul2(a_lo, __half2half2(__float2half(-72.0f)));
                         const __half2 b_lo0 = __hmul2(b_lo, __half2half2(__float2half(-1032.0f))), b_hi0 = __hmul2(b_lo, __half2half2(__float2half(-72.0f)));
 #pragma unroll
@@ -585,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t f0 = half2_bits(__hfma2(bits_half2((x & 0x000F000Fu) | 0x64006400u), a_lo, a_lo0));
-                                const uint32_t f2 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x64006400u), a_hi, a_hi0));
+                                const uint32_t f2 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x54005400u), a_lo, a_hi0));
                                 const uint32_t f1 = half2_bits(__hfma2(bits_half2((y & 0x000F000Fu) | 0x64006400u), b_lo, b_lo0));
-                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x64006400u), b_hi, b_hi0));
+                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x54005400u), b_lo, b_hi0));
                                 const int step_k = 2 * (2 * k + w2) + i;
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma_f16(z[g][nt], f0, f1, f2, f3, qf[nt][step_k][0], qf[nt][step_k][1]);
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                     z[g][nt][2] *= zs0[nt];
                     z[g][nt][3] *= zs1[nt];
                 }
-                if (!plain) {
+                if (!kPlain) {
                     const bool here = !((bad >> g) & 1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         const float mn = fmaxf(m[nt][e], x - kLift);
-                        const float f = m[nt][e] == -INFINITY ? 0.0f : exp2_approx(m[nt][e] - mn);
+                        const float f = exp2_approx(m[nt][e] - mn);
                         m[nt][e] = mn;
                         l[nt][e] *= f;
 #pragma unroll
@@ -673,10 +677,8 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 uint32_t ph[NT][2], plo[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    // a row that has seen nothing yet: z = -inf, and 2^(-inf) = 0
-                    const float b0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
-                    const float p00 = exp2_approx(z[g][nt][0] - b0), p01 = exp2_approx(z[g][nt][1] - b1);
-                    const float p10 = exp2_approx(z[g][nt][2] - b0), p11 = exp2_approx(z[g][nt][3] - b1);
+                    const float p00 = exp2_approx(z[g][nt][0] - m[nt][0]), p01 = exp2_approx(z[g][nt][1] - m[nt][1]);
+                    const float p10 = exp2_approx(z[g][nt][2] - m[nt][0]), p11 = exp2_approx(z[g][nt][3] - m[nt][1]);
                     l[nt][0] += p00 + p10;
                     l[nt][1] += p01 + p11;
                     if (KIND == kBf16) {
@@ -694,9 +696,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                     }
                 }
                 // ---- O^T += V^T P^T
-                const bool odd = !plain && several && __any_sync(0xffffffffu, v_step(g, plain, keep[g], ph, plo, o, true));
+                const bool odd = !kPlain && several && __any_sync(0xffffffffu, v_step(g, keep[g], ph, plo, o, true));
                 if (!odd) {
-                    v_step(g, plain, keep[g], ph, plo, o, false);
+                    v_step(g, keep[g], ph, plo, o, false);
                 } else {
                     // An infinity or a NaN in V where some rows look and others do not: 0 times it is no 0, so each
                     // row gets products of its own, without the positions that it does not see.
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < KM; ++j) x[nt][j][0] = x[nt][j][1] = x[nt][j][2] = x[nt][j][3] = 0.0f;
-                        v_step(g, false, keep[g] & v_bits(p0 + 16 * g, a.window > 0 ? to - a.window + 1 : 0, to + 1), ph, plo, x, false);
+                        v_step(g, keep[g] & v_bits(p0 + 16 * g, a.window > 0 ? to - a.window + 1 : 0, to + 1), ph, plo, x, false);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -723,13 +725,18 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                     }
                 }
             }
+            };
+            if (plain) tile(std::true_type{});
+            else tile(std::false_type{});
+            stage = after(st, 1);
+            parity ^= stage == 0;
             __syncwarp();   // every lane has read the slot before the next turn fills it again
         }
         if (KIND != kInt4) asm volatile("cp.async.wait_all;" ::: "memory");
         if (failed) {
             // a copy did not come in time: the status says so, the rows are NaN, nothing more is issued, and
             // what may still be in flight is given as long again
-            for (int k = 0; k < S; ++k) mbar_wait(bar0 + 8 * ((step + k) % S), ((step + k) / S) & 1);
+            for (int k = 0; k < S; ++k) mbar_wait(bar0 + 8 * after(stage, k), parity ^ (stage + k >= S));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = 0.0f, l[nt][0] = l[nt][1] = NAN;
         }
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         for (int i = tid; i < R * D / 4; i += kThreads) {
             const int row = i / (D / 4), d = (i % (D / 4)) * 4;
             if (row0 + row >= seq_rows) continue;
-            float mm = -INFINITY;
+            float mm = kLowest;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * R + row].x);
             float sum = 0.0f;
@@ -778,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float2 v = ml[w * R + row];
-                const float f = v.x == -INFINITY ? 0.0f : exp2_approx(v.x - mm);
+                const float f = exp2_approx(v.x - mm);
                 const float4 x = *reinterpret_cast<const float4*>(merge + (w * R + row) * C::row_stride + d);
                 sum += v.y * f;
                 acc.x += x.x * f;
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 const int t = (row0 + row) / a.group, g = row0 + row - t * a.group;
                 const int64_t out_row = s.first_row + t;
                 const int head = h * a.group + g;
-                const float inv = mm == -INFINITY ? 0.0f : gain_v / sum;
+                const float inv = sum == 0.0f ? 0.0f : gain_v / sum;
                 const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
                 uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + out_row * a.out_row + head * a.out_head + d;
                 uint2 w;
@@ -802,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 }
                 *reinterpret_cast<uint2*>(to) = w;
                 if (a.lse && d == 0)
-                    a.lse[out_row * a.hq + head] = mm == -INFINITY ? -INFINITY : (mm + log2f(sum)) * 0.69314718056f;
+                    a.lse[out_row * a.hq + head] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718056f;
             } else {
                 float* rec = a.part + ((int64_t)(blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * R + row) * (D + 4);
                 *reinterpret_cast<float4*>(rec + d) = acc;
@@ -844,16 +851,15 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const __grid_co
         const float* rec0 = a.part + ((int64_t)(blockIdx.x * 2 + 1) * R + row) * (D + 4);
         const int64_t next = (int64_t)2 * R * (D + 4);
         const float* rec1 = rec0 + (int64_t)R * (D + 4);   // record 0 of the next CTA
-        float mm = -INFINITY, sum = 0.0f;
+        float mm = kLowest, sum = 0.0f;
         float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll 4
         for (int i = 0; i < pieces; ++i) {
             const float* rec = i == 0 ? rec0 : rec1 + (i - 1) * next;
             const float2 v = *reinterpret_cast<const float2*>(rec + D);
             const float4 x = *reinterpret_cast<const float4*>(rec + d);
-            if (v.x == -INFINITY) continue;
             const float mn = fmaxf(mm, v.x);
-            const float f = mm == -INFINITY ? 0.0f : exp2_approx(mm - mn), g = exp2_approx(v.x - mn);
+            const float f = exp2_approx(mm - mn), g = exp2_approx(v.x - mn);
             mm = mn;
             sum = sum * f + v.y * g;
             acc.x = acc.x * f + x.x * g;
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const __grid_co
         const int t = (row0 + row) / a.group, g = row0 + row - t * a.group;
         const int64_t out_row = s.first_row + t;
         const int head = h * a.group + g;
-        const float inv = mm == -INFINITY ? 0.0f : gain_v / sum;
+        const float inv = sum == 0.0f ? 0.0f : gain_v / sum;
         uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + out_row * a.out_row + head * a.out_head + d;
         uint2 w;
         if (!out_fp16) {
@@ -875,7 +881,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const __grid_co
         }
         *reinterpret_cast<uint2*>(to) = w;
         if (a.lse && d == 0)
-            a.lse[out_row * a.hq + head] = mm == -INFINITY ? -INFINITY : (mm + log2f(sum)) * 0.69314718056f;
+            a.lse[out_row * a.hq + head] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718056f;
     }
 }
 
