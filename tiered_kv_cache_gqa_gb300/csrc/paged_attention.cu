@@ -94,6 +94,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+    return y;
+}
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
@@ -504,10 +510,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                             uint32_t y = __byte_perm(w[2][wi], w[3][wi], half ? 0x7632 : 0x5410);
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t f0 = half2_bits(__hfma2(bits_half2((x & 0x000F000Fu) | 0x64006400u), s_lo[0], n_lo[0]));
-                                const uint32_t f1 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x54005400u), s_lo[0], n_hi[0]));
-                                const uint32_t f2 = half2_bits(__hfma2(bits_half2((y & 0x000F000Fu) | 0x64006400u), s_lo[1], n_lo[1]));
-                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x54005400u), s_lo[1], n_hi[1]));
+                                const uint32_t f0 = half2_bits(__hfma2(bits_half2(and_or(x, 0x000F000Fu, 0x64006400u)), s_lo[0], n_lo[0]));
+                                const uint32_t f1 = half2_bits(__hfma2(bits_half2(and_or(x, 0x00F000F0u, 0x54005400u)), s_lo[0], n_hi[0]));
+                                const uint32_t f2 = half2_bits(__hfma2(bits_half2(and_or(y, 0x000F000Fu, 0x64006400u)), s_lo[1], n_lo[1]));
+                                const uint32_t f3 = half2_bits(__hfma2(bits_half2(and_or(y, 0x00F000F0u, 0x54005400u)), s_lo[1], n_hi[1]));
                                 const int j = 4 * wi + 2 * half + i;   // rows r and r + 8: channels (D / 8) r + 2 j and + 1
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
@@ -588,10 +594,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                             uint32_t x = wa[2 * k + w2], y = wb[2 * k + w2];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t f0 = half2_bits(__hfma2(bits_half2((x & 0x000F000Fu) | 0x64006400u), a_lo, a_lo0));
-                                const uint32_t f2 = half2_bits(__hfma2(bits_half2((x & 0x00F000F0u) | 0x54005400u), a_lo, a_hi0));
-                                const uint32_t f1 = half2_bits(__hfma2(bits_half2((y & 0x000F000Fu) | 0x64006400u), b_lo, b_lo0));
-                                const uint32_t f3 = half2_bits(__hfma2(bits_half2((y & 0x00F000F0u) | 0x54005400u), b_lo, b_hi0));
+                                const uint32_t f0 = half2_bits(__hfma2(bits_half2(and_or(x, 0x000F000Fu, 0x64006400u)), a_lo, a_lo0));
+                                const uint32_t f2 = half2_bits(__hfma2(bits_half2(and_or(x, 0x00F000F0u, 0x54005400u)), a_lo, a_hi0));
+                                const uint32_t f1 = half2_bits(__hfma2(bits_half2(and_or(y, 0x000F000Fu, 0x64006400u)), b_lo, b_lo0));
+                                const uint32_t f3 = half2_bits(__hfma2(bits_half2(and_or(y, 0x00F000F0u, 0x54005400u)), b_lo, b_hi0));
                                 const int step_k = 2 * (2 * k + w2) + i;
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma_f16(z[g][nt], f0, f1, f2, f3, qf[nt][step_k][0], qf[nt][step_k][1]);
