@@ -498,6 +498,9 @@ tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dt
  * q, out: device [rows][num_q_heads][d] of dtype TKV_BF16 or TKV_FP16 (the pages'
  * own type if they are 16-bit), 16-byte aligned, strides multiples of 8; lse:
  * device fp32 [rows][num_q_heads], contiguous.
+ * A step's size is limited: (rows * num_q_heads / Hkv / 8 + batch) * Hkv *
+ * (max_pages * page_size / 32) tiles (half as many positions a tile with 16-bit
+ * pages) are at most 2 * 10^9; a longer prompt enters in parts.
  * max_new and max_len are the host's estimates of the largest n_b and the largest
  * length.  They choose how the work is split, not what is computed: any
  * values >= 1 give right results, better ones faster.

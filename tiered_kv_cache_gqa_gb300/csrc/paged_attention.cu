@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kWarps = 7, kThreads = (kWarps + 1) * 32;   // warps that compute, and one that copies
 constexpr int kCombineWarps = 8;
-constexpr int kMinPositions = 256;      // of a CTA's share: below, joining costs more than it brings
+constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, joining costs more than it brings
 constexpr int kWholeItems = 512;        // up to this length a CTA takes whole items, and nothing is left to join
 constexpr int kSpinLimit = 1 << 18;     // tries of a wait
 
@@ -83,7 +83,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------ the deal
 // What sequence b brings: its queries n, the positions that exist (len) and that its last query counts from (full), where
@@ -107,29 +106,33 @@ __device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
     return s;
 }
 
-__device__ __forceinline__ int64_t weight(const PagedAttnArgs& a, const Seq& s) { return (int64_t)s.tiles * a.c.num_kv_heads * s.units; }
+// Tiles of a sequence.  The host has made sure that the batch's tiles are fewer than 2^31.
+__device__ __forceinline__ int weight(const PagedAttnArgs& a, const Seq& s) { return s.tiles * a.c.num_kv_heads * s.units; }
 
 // All tiles of the batch; *before, *own: those of the sequences before this thread's and of its own (blocks of
-// ceil(batch / threads) sequences a thread).  `sums`: an int64 of shared memory a warp.
+// ceil(batch / threads) sequences a thread).  `sums`: an int of shared memory a warp.
 template <int R, int TP, int WARPS>
-__device__ __forceinline__ int64_t scan_batch(const PagedAttnArgs& a, int64_t* sums, int64_t* before, int64_t* own) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ int scan_batch(const PagedAttnArgs& a, int* sums, int* before, int* own) {
     constexpr int threads = WARPS * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.c.batch + threads - 1) / threads;
-    int64_t mine = 0;
+    int mine = 0;
+#pragma unroll 1
     for (int b = tid * per; b < min(a.c.batch, (tid + 1) * per); ++b) mine += weight(a, sequence<R, TP>(a, b));
-    int64_t sum = mine;
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += x;
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int64_t base = 0, total = 0;
+    int base = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) base += sums[w];
-        total += sums[w];
+        const int x = sums[w];
+        base += w < warp ? x : 0;
+        total += x;
     }
     *before = base + sum - mine;
     *own = mine;
@@ -137,34 +140,33 @@ __device__ __forceinline__ int64_t scan_batch(const PagedAttnArgs& a, int64_t* s
 }
 
 // Where tile u of the deal lies: its sequence, and the tiles of that sequence before it.  All threads call it with the
-// same targets u0, u0 + step, .. (count of them, those below total); a barrier follows before `where` is read.
+// same targets u0, u0 + step, .. (COUNT of them; those not below the total are left out); a barrier follows before
+// `where` is read.
 struct Where {
-    int64_t in_seq;
-    int b;
+    int b, in_seq;
 };
 
-template <int R, int TP, int WARPS>
-__device__ __forceinline__ void locate(const PagedAttnArgs& a, int64_t u0, int64_t step, int count, int64_t before, int64_t own, Where* where) {
+template <int R, int TP, int WARPS, int COUNT>
+__device__ __forceinline__ void locate(const PagedAttnArgs& a, int u0, int step, int before, int own, Where* where) {
     const int per = (a.c.batch + WARPS * 32 - 1) / (WARPS * 32);
-    for (int k = 0; k < count; ++k) {
-        const int64_t u = u0 + k * step;
-        if (u < before || u >= before + own) continue;
-        int64_t left = u - before;
-        int b = threadIdx.x * per;
+#pragma unroll 1
+    for (int k = 0; k < COUNT; ++k) {
+        const int left0 = u0 + k * step - before;
+        if (left0 < 0 || left0 >= own) continue;
+        int left = left0, b = threadIdx.x * per;
+#pragma unroll 1
         for (; per > 1; ++b) {
-            const int64_t w = weight(a, sequence<R, TP>(a, b));
+            const int w = weight(a, sequence<R, TP>(a, b));
             if (left < w) break;
             left -= w;
         }
-        where[k].b = b;
-        where[k].in_seq = left;
+        where[k] = Where{b, left};
     }
 }
 
-template <int TP>
-__device__ __forceinline__ int64_t share_of(const PagedAttnArgs& a, int64_t total) {
-    const int64_t even = (total + a.grid - 1) / a.grid;
-    return a.whole_items ? max(even, (int64_t)1) : max(even, (int64_t)(kMinPositions / TP));
+__device__ __forceinline__ int share_of(const PagedAttnArgs& a, int total) {
+    const int even = (int)(((uint32_t)total + a.grid - 1) / (uint32_t)a.grid);
+    return max(even, a.whole_items ? 1 : kMinTiles);
 }
 
 // ------------------------------------------------------------------ shapes
@@ -193,10 +195,10 @@ struct Shared {
         uint8_t ring[kWarps][C::warp_ring];
         float merge[kWarps][C::R][C::row_stride];
     };
-    uint64_t full[kWarps][C::stages], empty[kWarps][C::stages];
+    uint64_t full[kWarps][C::stages], empty[kWarps][C::stages], known[kWarps][C::queue];   // a tile is there, is used; a piece is known
     Piece queue[kWarps][C::queue];
     float2 ml[kWarps][C::R];            // reference and sum of a warp's rows
-    int64_t sums[kWarps + 1];
+    int sums[kWarps + 1];
     Where where[kWarps], ends[2];
     int flags[kWarps], last[kWarps];    // of each warp's last piece, and its place in the queue
     uint8_t bad[kWarps][C::stages][2];  // records of a stage that have no page
@@ -278,10 +280,10 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     Seq s{};
     if (left) {
         s = sequence<R, TP>(a, b);
-        const int64_t item = from.in_seq / s.units;
-        unit = (int)(from.in_seq - item * s.units);
-        h = (int)(item / s.tiles);
-        row_tile = (int)(item - (int64_t)h * s.tiles);
+        const int item = from.in_seq / s.units;
+        unit = from.in_seq - item * s.units;
+        h = item / s.tiles;
+        row_tile = item - h * s.tiles;
     }
     // the piece that is copied: tiles, the next one's position, where its rows see nothing, its page table, page 0 of its head
     int tiles = 0, pos = 0, end = 0, pieces = 0, page = -2;
@@ -323,6 +325,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 p.flags = kValid | (unit ? kContinues : 0) | (unit + p.tiles == s.units ? kEnds : 0);
                 if (k == 0) {
                     sh.queue[w][pieces & (C::queue - 1)] = p;
+                    mbar_arrive(smem_u32(&sh.known[w][pieces & (C::queue - 1)]));
                     if (s.full > s.len) raise_status(a.status, TKV_ECAPACITY);
                 }
                 ++pieces;
@@ -333,13 +336,6 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 table = a.c.page_table + (int64_t)b * a.c.max_pages;
                 pages = reinterpret_cast<const uint8_t*>(a.c.pages) + head_bytes * h;
                 look_up();
-                // the piece's rows of q, which are read when its turn comes
-                for (int row = p.rows.row0 + k; row < min(p.rows.seq_rows, p.rows.row0 + R); row += 4) {
-                    const int t = query_of(row, a.group, a.group_mul);
-                    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + (s.first_row + t) * a.q_row + (h * a.group + row - t * a.group) * a.q_head;
-                    prefetch_l2(q);
-                    if (D == 128) prefetch_l2(q + 64);
-                }
                 unit += tiles;
                 if (unit == s.units) {
                     unit = 0;
@@ -423,32 +419,33 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             mbar_init(smem_u32(&sh.full[lane][s]), KIND == kInt4 ? 2 : 32);   // the lanes that bring a tile
             mbar_init(smem_u32(&sh.empty[lane][s]), 1);
         }
+        for (int s = 0; s < C::queue; ++s) mbar_init(smem_u32(&sh.known[lane][s]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
     // -------------------------------------------------------- this CTA's tiles of the deal, and each warp's
-    int64_t before, own;
-    const int64_t total = scan_batch<R, TP, kWarps + 1>(a, sh.sums, &before, &own);
-    const int64_t share = share_of<TP>(a, total);
-    int64_t u0 = min(total, (int64_t)blockIdx.x * share), u1 = min(total, u0 + share);
+    int before, own;
+    const int total = scan_batch<R, TP, kWarps + 1>(a, sh.sums, &before, &own);
+    const int share = share_of(a, total);
+    int u0 = (int)min((int64_t)total, (int64_t)blockIdx.x * share), u1 = min(total, u0 + share);
     if (a.whole_items) {
         // both ends move up to the next item's begin
-        locate<R, TP, kWarps + 1>(a, u0, share, 2, before, own, sh.ends);
+        locate<R, TP, kWarps + 1, 2>(a, u0, share, before, own, sh.ends);
         __syncthreads();
-        auto up = [&](int64_t u, const Where& w) {
+        auto up = [&](int u, const Where& w) {
             if (u >= total) return total;
-            const int units = sequence<R, TP>(a, w.b).units, c = (int)(w.in_seq % units);
+            const int units = sequence<R, TP>(a, w.b).units, c = w.in_seq % units;
             return c ? u + units - c : u;
         };
-        const int64_t v0 = up(u0, sh.ends[0]), v1 = up(u0 + share, sh.ends[1]);
+        const int v0 = up(u0, sh.ends[0]);
+        u1 = up(u0 + share, sh.ends[1]);
         u0 = v0;
-        u1 = v1;
     }
     if (u0 >= u1) return;
-    const int per_warp = (int)((u1 - u0 + kWarps - 1) / kWarps);
-    locate<R, TP, kWarps + 1>(a, u0, per_warp, kWarps, before, own, sh.where);
+    const int per_warp = (u1 - u0 + kWarps - 1) / kWarps;
+    locate<R, TP, kWarps + 1, kWarps>(a, u0, per_warp, before, own, sh.where);
     __syncthreads();
-    auto tiles_of = [&](int w) { return (int)max((int64_t)0, min((int64_t)per_warp, u1 - u0 - (int64_t)w * per_warp)); };
+    auto tiles_of = [&](int w) { return max(0, min(per_warp, u1 - u0 - w * per_warp)); };
 
     int taken = 0;                       // pieces of this warp
     Sums<D, NT> sums;
@@ -464,15 +461,18 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         bool failed = false;
 #pragma unroll 1
         while (left > 0 && !failed) {
-            // the piece is in the queue when its first tile has come
-            failed = __any_sync(0xffffffffu, !mbar_wait(full0 + 8 * stage, parity));
+            const int place = taken & (C::queue - 1);
+            failed = __any_sync(0xffffffffu, !mbar_wait(smem_u32(&sh.known[warp][place]), (taken / C::queue) & 1));
             if (failed) break;
-            const Piece& piece = sh.queue[warp][taken++ & (C::queue - 1)];   // stays where it is: its place is taken again much later
+            const Piece& piece = sh.queue[warp][place];   // stays where it is: its place is taken again much later
+            ++taken;
             const int all_from = piece.rows.all_from, all_until = piece.rows.all_until, tiles = piece.tiles;
             Query<D, NT> q;
             load_query<D, NT, KIND>(reinterpret_cast<const uint16_t*>(a.q), a.q_row, a.q_head, a.q_fp16, a.group, a.group_mul, a.scale_log2,
                                     KIND == kInt4 && a.c.k_gain ? __ldg(a.c.k_gain + piece.rows.h) : 1.0f, lane, piece.rows, q);
             sums.clear();
+            failed = __any_sync(0xffffffffu, !mbar_wait(full0 + 8 * stage, parity));
+            if (failed) break;
             int p0 = piece.begin;
 #pragma unroll 1
             for (int t = 1;; ++t, p0 += TP) {
@@ -480,9 +480,13 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 const uint32_t at_s = smem_u32(at);
                 const uint32_t bad = sh.bad[warp][stage][0] | (KIND == kInt4 ? sh.bad[warp][stage][1] << 1 : 0);
                 if (!bad && p0 + TP <= all_until && p0 >= all_from)
-                    attend_tile<D, NT, KIND, true>(at, at_s, lane, p0, 0, piece.rows, a.group, a.group_mul, a.window, q, sums);
-                else
-                    attend_tile<D, NT, KIND, false>(at, at_s, lane, p0, bad, piece.rows, a.group, a.group_mul, a.window, q, sums);
+                    attend_tile<D, NT, KIND, T::groups, true>(at, at_s, lane, p0, false, piece.rows, a.group, a.group_mul, a.window, q, sums);
+                else {
+#pragma unroll 1
+                    for (int g = 0; g < T::groups; ++g)
+                        attend_tile<D, NT, KIND, 1, false>(at + g * Record<D>::bytes, at_s, lane, p0 + 16 * g, (bad >> g) & 1, piece.rows, a.group,
+                                                           a.group_mul, a.window, q, sums);
+                }
                 __syncwarp();   // every lane has read the slot
                 if (t == tiles) break;
                 if (lane == 0) mbar_arrive(empty0 + 8 * stage);
@@ -547,22 +551,20 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         for (int nt = 0; nt < NT; ++nt) store_rows<D, KIND>(sums.o[nt], lane, sh.merge[warp][8 * nt]);
     }
     __syncthreads();
-    for (int g = 0; g < kWarps; ++g) {
-        // warp g's piece is the first of its item here; the warps behind it that hold no other item follow, and the
-        // record of the one in which the item ended
-        if (!(sh.flags[g] & kValid) || (g > 0 && (sh.flags[g] & kContinues))) continue;
-        int w1 = g, tail = -1;
-        bool ends = sh.flags[g] & kEnds;
-        while (!ends && w1 + 1 < kWarps && (sh.flags[w1 + 1] & kValid)) {
-            if (sh.flags[w1 + 1] & kHead) {
-                tail = w1 + 1;
-                break;
-            }
-            ends = sh.flags[++w1] & kEnds;
-        }
-        const bool complete = !(sh.flags[g] & kContinues) && (ends || tail >= 0);
+    // A warp's piece that is the first of its item here leads; the warps behind it that hold nothing else follow, and the
+    // record of the one in which the item ended.
+    const int f = lane < kWarps ? sh.flags[lane] : 0;
+    const uint32_t valid = __ballot_sync(0xffffffffu, f & kValid), continues = __ballot_sync(0xffffffffu, f & kContinues);
+    const uint32_t ends = __ballot_sync(0xffffffffu, f & kEnds), heads = __ballot_sync(0xffffffffu, f & kHead);
+    const uint32_t leads = valid & ~(continues & ~1u);
+#pragma unroll 1
+    for (uint32_t todo = leads; todo; todo &= todo - 1) {
+        const int g = __ffs(todo) - 1;
+        const int w1 = __ffs((leads | heads | ~valid) & (~1u << g)) - 2;   // the last that follows
+        const int tail = (heads >> (w1 + 1)) & 1 && !((ends >> w1) & 1) ? w1 + 1 : -1;
+        const bool begins = !((continues >> g) & 1), complete = begins && (((ends >> w1) & 1) || tail >= 0);
         const Rows& rows = sh.queue[g][sh.last[g]].rows;
-        float* record = complete ? nullptr : a.part + ((int64_t)blockIdx.x * 2 + (sh.flags[g] & kContinues ? 0 : 1)) * R * (D + 4);
+        float* record = complete ? nullptr : a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * R * (D + 4);
         const float* tail_record = a.part + ((int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + tail) * R * (D + 4);
         const float gain = gain_of(rows.h);
         for (int i = tid; i < R * LANES; i += kThreads) {
@@ -607,21 +609,21 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 template <int D, int NT, int TP>
 __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a, bool fp16, float gain16) {
     constexpr int R = 8 * NT;
-    __shared__ int64_t sums[kCombineWarps];
+    __shared__ int sums[kCombineWarps];
     __shared__ Where at;
-    int64_t before, own;
-    const int64_t total = scan_batch<R, TP, kCombineWarps>(a, sums, &before, &own);
-    const int64_t share = share_of<TP>(a, total);
-    const int64_t cut = (int64_t)(blockIdx.x + 1) * share;
-    locate<R, TP, kCombineWarps>(a, cut, 0, cut < total ? 1 : 0, before, own, &at);
+    int before, own;
+    const int total = scan_batch<R, TP, kCombineWarps>(a, sums, &before, &own);
+    const int share = share_of(a, total);
+    const int cut = (int)min((int64_t)total, (int64_t)(blockIdx.x + 1) * share);
+    locate<R, TP, kCombineWarps, 1>(a, cut, 0, before, own, &at);
     __syncthreads();
     int pieces = 0;
     Rows rows{};
     if (cut < total) {
         const Seq s = sequence<R, TP>(a, at.b);
-        const int item = (int)(at.in_seq / s.units), c = (int)(at.in_seq - (int64_t)item * s.units);
+        const int item = at.in_seq / s.units, c = at.in_seq - item * s.units;
         if (c > 0 && c <= share) {   // something is cut here, and it began in this share
-            pieces = (int)((cut - c + s.units - 1) / share) - (int)blockIdx.x + 1;
+            pieces = (cut - c + s.units - 1) / share - (int)blockIdx.x + 1;
             rows.h = item / s.tiles;
             rows.row0 = (item - rows.h * s.tiles) * R;
             rows.first_row = s.first_row;
@@ -790,6 +792,10 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = row_tiles(a.group, max_new);
+    // tiles are counted in 32 bits
+    const double tile_bound = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads *
+                              ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
+    if (tile_bound > 2.0e9) return TKV_EINVAL;
     const cudaError_t e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, st) : launch_kind<128, 2>(a, st))
                                                  : (nt == 1 ? launch_kind<64, 1>(a, st) : launch_kind<64, 2>(a, st));
     if (e != cudaSuccess) {

@@ -336,11 +336,11 @@ __device__ __forceinline__ float2 v_values(const uint8_t* tile, int g, int r, in
 }
 
 // ------------------------------------------------------------------ a tile
-// PLAIN: every row sees every position of the tile.  bad: bit g set if group g's page is none.
-template <int D, int NT, int KIND, bool PLAIN>
-__device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s, int lane, int p0, uint32_t bad, const Rows& rows,
+// NG groups of 16 positions from p0 on.  PLAIN: every row sees every one of them; bad: their page is none.
+template <int D, int NT, int KIND, int NG, bool PLAIN>
+__device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s, int lane, int p0, bool bad, const Rows& rows,
                                             int group, uint32_t mul, int window, const Query<D, NT>& q, Sums<D, NT>& a) {
-    constexpr int NG = TileOf<D, KIND>::groups, KM = D / 16;
+    constexpr int KM = D / 16;
     const int r = lane >> 2, cq = lane & 3;
     float z[NG][NT][4];
     uint32_t keep[NG];   // which of the lane's four V positions of a group any row sees
@@ -359,7 +359,7 @@ __device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s
         }
         keep[g] = 15;
         if (!PLAIN) {
-            const bool here = !((bad >> g) & 1);
+            const bool here = !bad;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
