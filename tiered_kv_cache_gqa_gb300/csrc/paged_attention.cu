@@ -34,7 +34,7 @@ struct PagedAttnArgs {
     void* out;
     float* lse;
     const int32_t* cu;
-    float* part;                         // records [R][D + 4] (O at its reference m, m, l): [grid][2], then [grid][kWarps]
+    float4* part;                        // records (below): [grid][2], then [grid][kWarps]
     int32_t* status;
     int64_t rows, q_row, q_head, out_row, out_head;
     int hq, group, window, page_shift, grid, whole_items, q_fp16;
@@ -178,7 +178,6 @@ struct Config {
     static constexpr int stages = KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : 6) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
     static constexpr int queue = stages <= 6 ? 8 : 16;   // pieces: the one computed, one a stage, one not yet copied
     static constexpr int warp_ring = stages * TileOf<D, KIND>::bytes;
-    static constexpr int row_stride = D + 4;   // floats of a row on its way out: the lanes' 16-byte stores spread over the banks
 };
 
 // A warp's part of an item.
@@ -193,11 +192,11 @@ struct Shared {
     using C = Config<D, NT, KIND>;
     union {
         uint8_t ring[kWarps][C::warp_ring];
-        float merge[kWarps][C::R][C::row_stride];
+        float4 merge[kWarps][NT * (D / 16) * 32];
     };
     uint64_t full[kWarps][C::stages], empty[kWarps][C::stages], known[kWarps][C::queue];   // a tile is there, is used; a piece is known
     Piece queue[kWarps][C::queue];
-    float2 ml[kWarps][C::R];            // reference and sum of a warp's rows
+    float4 ml[kWarps][C::R / 2];        // references and sums of a warp's rows, two rows each
     int sums[kWarps + 1];
     Where where[kWarps], ends[2];
     int flags[kWarps], last[kWarps];    // of each warp's last piece, and its place in the queue
@@ -205,62 +204,75 @@ struct Shared {
 };
 
 // ------------------------------------------------------------------ out
-// Four channels of a row: to out (and lse), or to a record.
-template <int D>
-__device__ __forceinline__ void emit(const PagedAttnArgs& a, const Rows& rows, int row, int d, float4 x, float m, float l, float* record,
-                                     bool fp16, float gain) {
-    if (record) {
-        float* to = record + row * (D + 4);
-        *reinterpret_cast<float4*>(to + d) = x;
-        if (d == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, l);
-        return;
-    }
-    const int t = query_of(rows.row0 + row, a.group, a.group_mul), head = rows.h * a.group + rows.row0 + row - t * a.group;
-    const int64_t out_row = rows.first_row + t;
-    const float inv = l == 0.0f ? 0.0f : gain / l;
-    uint2 w;
-    if (fp16)
-        w = make_uint2(half2_bits(__floats2half2_rn(x.x * inv, x.y * inv)), half2_bits(__floats2half2_rn(x.z * inv, x.w * inv)));
-    else
-        w = make_uint2(bf162_bits(__floats2bfloat162_rn(x.x * inv, x.y * inv)), bf162_bits(__floats2bfloat162_rn(x.z * inv, x.w * inv)));
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + out_row * a.out_row + head * a.out_head + d) = w;
-    if (a.lse && d == 0) a.lse[out_row * a.hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
-}
-
-// The sums of a lane's rows over its lanes, into ml.
+// A record of a cut item: the accumulators as the lanes hold them, float4 j of row tile nt and lane at [(nt D/16 + j) 32 +
+// lane] (rows 8 nt + 2 cq and + 1, each in two channels), then m and l of two rows each, [4 nt + cq].  Everything that
+// joins pieces adds float4s in this order, so that little code stands behind the tiles: it comes cold into the
+// instruction cache at the very end, and with the memory busy 80 instructions took 3 us there.
 template <int D, int NT>
-__device__ __forceinline__ void reduce_sums(const Sums<D, NT>& s, int lane, float2* ml) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x = s.l[nt][e];
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            x += __shfl_xor_sync(0xffffffffu, x, 8);
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            if (lane < 4) ml[nt * 8 + 2 * lane + e] = make_float2(s.m[nt][e], x);
-        }
+struct Rec4 {
+    static constexpr int sums = NT * (D / 16) * 32, size = sums + NT * 4;   // float4s
+};
+
+// The channels of component c of float4 j: row 2 cq + (c & 1).
+template <int D, int KIND>
+__device__ __forceinline__ int channel_of(int r, int j, int c) { return KIND == kInt4 ? (D / 8) * r + 2 * j + (c >> 1) : 16 * j + r + 8 * (c >> 1); }
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {
+    return fp16 ? half2_bits(__floats2half2_rn(a, b)) : bf162_bits(__floats2bfloat162_rn(a, b));
 }
 
-// The fragments of eight rows of O^T -> rows of D + 4 floats.
+// Where a row's out (and lse) lies; null: no such row.
+__device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, const Rows& rows, int row, float** lse) {
+    if (rows.row0 + row >= rows.seq_rows) return nullptr;
+    const int t = query_of(rows.row0 + row, a.group, a.group_mul), head = rows.h * a.group + rows.row0 + row - t * a.group;
+    if (lse) *lse = a.lse ? a.lse + (int64_t)(rows.first_row + t) * a.hq + head : nullptr;
+    return reinterpret_cast<uint16_t*>(a.out) + (rows.first_row + t) * a.out_row + head * a.out_head;
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718056f; }
+__device__ __forceinline__ float inverse(float l, float gain) { return l == 0.0f ? 0.0f : gain / l; }   // a row that saw nothing is 0
+
+// float4 j of row tile nt, of rows with these m and l, to out (lse with j = 0, lane row 0).
 template <int D, int KIND>
-__device__ __forceinline__ void store_rows(const float (&o)[D / 16][4], int lane, float* to) {
-    const int r = lane >> 2, cq = lane & 3;
+__device__ __forceinline__ void emit4(const PagedAttnArgs& a, const Rows& rows, int nt, int j, int lane, float4 x, float4 ml, float gain, bool fp16) {
+    const int r = lane >> 2, row = 8 * nt + 2 * (lane & 3);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        float* row = to + (2 * cq + e) * (D + 4);
+        float* lse;
+        uint16_t* to = out_row(a, rows, row + e, &lse);
+        if (!to) continue;
+        const float m = e ? ml.z : ml.x, l = e ? ml.w : ml.y, inv = inverse(l, gain);
+        const uint32_t w = pack16((e ? x.y : x.x) * inv, (e ? x.w : x.z) * inv, fp16);
         if (KIND == kInt4) {
-#pragma unroll
-            for (int j = 0; j < D / 16; j += 2)
-                *reinterpret_cast<float4*>(row + (D / 8) * r + 2 * j) = make_float4(o[j][e], o[j][e + 2], o[j + 1][e], o[j + 1][e + 2]);
+            *reinterpret_cast<uint32_t*>(to + channel_of<D, KIND>(r, j, 0)) = w;
         } else {
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                row[16 * j + r] = o[j][e];
-                row[16 * j + r + 8] = o[j][e + 2];
-            }
+            to[channel_of<D, KIND>(r, j, 0)] = (uint16_t)w;
+            to[channel_of<D, KIND>(r, j, 2)] = (uint16_t)(w >> 16);
         }
+        if (lse && j == 0 && r == 0) *lse = lse_of(m, l);
     }
+}
+
+// (ml, x) += (ml2, x2): sums of two rows at their references.
+__device__ __forceinline__ void join(float4& ml, float4& x, float4 ml2, float4 x2) {
+    const float m0 = fmaxf(ml.x, ml2.x), m1 = fmaxf(ml.z, ml2.z);
+    const float f0 = exp2_approx(ml.x - m0), g0 = exp2_approx(ml2.x - m0), f1 = exp2_approx(ml.z - m1), g1 = exp2_approx(ml2.z - m1);
+    ml = make_float4(m0, ml.y * f0 + ml2.y * g0, m1, ml.w * f1 + ml2.w * g1);
+    x = make_float4(x.x * f0 + x2.x * g0, x.y * f1 + x2.y * g1, x.z * f0 + x2.z * g0, x.w * f1 + x2.w * g1);
+}
+
+// The sums of a lane's two rows over the lanes that share them: (m, l, m, l).
+template <int D, int NT>
+__device__ __forceinline__ float4 reduce_sums(const Sums<D, NT>& s, int nt) {
+    float l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] = s.l[nt][e];
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+    }
+    return make_float4(s.m[nt][0], l[0], s.m[nt][1], l[1]);
 }
 
 // ------------------------------------------------------------------ copying
@@ -409,7 +421,7 @@ template <int D, int NT, int KIND>
 __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_attention_kernel(const __grid_constant__ PagedAttnArgs a) {
     using C = Config<D, NT, KIND>;
     using T = TileOf<D, KIND>;
-    constexpr int R = C::R, S = C::stages, TP = T::positions, TB = T::bytes, LANES = D / 4;
+    constexpr int R = C::R, S = C::stages, TP = T::positions, TB = T::bytes;
     extern __shared__ __align__(128) uint8_t smem[];
     Shared<D, NT, KIND>& sh = *reinterpret_cast<Shared<D, NT, KIND>*>(smem);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -500,32 +512,48 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 flags |= piece.flags;
                 break;
             }
-            // The item ends here and others follow: out by way of the slot just read.  If it began before this warp's
-            // share, to a record: the CTA's first for the first warp (it joins the CTA before), else the warp's own.
-            float* record = nullptr;
-            if (piece.flags & kContinues) {
-                record = a.part + (warp ? (int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + warp : (int64_t)blockIdx.x * 2) * R * (D + 4);
-                flags = kHead;
-            }
-            float* stg = reinterpret_cast<float*>(sh.ring[warp] + stage * TB);
-            const float gain = gain_of(piece.rows.h);
-            reduce_sums<D, NT>(sums, lane, sh.ml[warp]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                store_rows<D, KIND>(sums.o[nt], lane, stg);
-                __syncwarp();
-                for (int i = lane; i < 8 * LANES; i += 32) {
-                    const int row = i / LANES, d = (i % LANES) * 4;
-                    if (piece.rows.row0 + nt * 8 + row < piece.rows.seq_rows) {
-                        const float2 v = sh.ml[warp][nt * 8 + row];
-                        emit<D>(a, piece.rows, nt * 8 + row, d, *reinterpret_cast<const float4*>(stg + row * (D + 4) + d), v.x, v.y, record, fp16, gain);
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a copy lands there again
-                __syncwarp();
-            }
             if (lane == 0) mbar_arrive(empty0 + 8 * stage);
             if (++stage == S) stage = 0, parity ^= 1;
+            // The item ends here and others follow.  If it began before this warp's share, to a record: the CTA's first for
+            // the first warp (it joins the CTA before), else the warp's own.
+            const bool cut = piece.flags & kContinues;
+            float4* record = a.part + (warp ? (int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + warp : (int64_t)blockIdx.x * 2) * Rec4<D, NT>::size;
+            if (cut) flags = kHead;
+            const float gain = gain_of(piece.rows.h);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float4 ml = reduce_sums<D, NT>(sums, nt);
+                if (cut) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        record[(nt * (D / 16) + j) * 32 + lane] = make_float4(sums.o[nt][j][0], sums.o[nt][j][1], sums.o[nt][j][2], sums.o[nt][j][3]);
+                    if (lane < 4) record[Rec4<D, NT>::sums + 4 * nt + lane] = ml;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = lane >> 2;
+                        float* lse;
+                        uint16_t* to = out_row(a, piece.rows, 8 * nt + 2 * (lane & 3) + e, &lse);
+                        if (!to) continue;
+                        const float l = e ? ml.w : ml.y, inv = inverse(l, gain);
+                        uint32_t w[D / 16];
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) w[j] = pack16(sums.o[nt][j][e] * inv, sums.o[nt][j][e + 2] * inv, fp16);
+                        if (KIND == kInt4) {   // D / 8 channels next to one another
+#pragma unroll
+                            for (int j = 0; j < D / 16; j += 4)
+                                *reinterpret_cast<uint4*>(to + channel_of<D, KIND>(r, j, 0)) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                to[channel_of<D, KIND>(r, j, 0)] = (uint16_t)w[j];
+                                to[channel_of<D, KIND>(r, j, 2)] = (uint16_t)(w[j] >> 16);
+                            }
+                        }
+                        if (lse && r == 0) *lse = lse_of(e ? ml.z : ml.x, l);
+                    }
+                }
+            }
         }
         if (failed) {
             // A copy did not come in time: the status says so, the piece's rows are NaN and what follows stays unwritten;
@@ -537,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             for (int nt = 0; nt < NT; ++nt) sums.l[nt][0] = sums.l[nt][1] = NAN;
             flags |= taken ? sh.queue[warp][(taken - 1) & (C::queue - 1)].flags : 0;
         }
-        if (taken) reduce_sums<D, NT>(sums, lane, sh.ml[warp]);
         if (lane == 0) {
             sh.flags[warp] = flags;
             sh.last[warp] = (taken - 1) & (C::queue - 1);
@@ -548,7 +575,13 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     __syncthreads();   // every warp is done with its ring
     if (taken) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) store_rows<D, KIND>(sums.o[nt], lane, sh.merge[warp][8 * nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+            const float4 ml = reduce_sums<D, NT>(sums, nt);
+            if (lane < 4) sh.ml[warp][4 * nt + lane] = ml;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                sh.merge[warp][(nt * (D / 16) + j) * 32 + lane] = make_float4(sums.o[nt][j][0], sums.o[nt][j][1], sums.o[nt][j][2], sums.o[nt][j][3]);
+        }
     }
     __syncthreads();
     // A warp's piece that is the first of its item here leads; the warps behind it that hold nothing else follow, and the
@@ -564,51 +597,37 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         const int tail = (heads >> (w1 + 1)) & 1 && !((ends >> w1) & 1) ? w1 + 1 : -1;
         const bool begins = !((continues >> g) & 1), complete = begins && (((ends >> w1) & 1) || tail >= 0);
         const Rows& rows = sh.queue[g][sh.last[g]].rows;
-        float* record = complete ? nullptr : a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * R * (D + 4);
-        const float* tail_record = a.part + ((int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + tail) * R * (D + 4);
+        float4* record = a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * Rec4<D, NT>::size;
+        const float4* tail_record = a.part + ((int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + tail) * Rec4<D, NT>::size;
         const float gain = gain_of(rows.h);
-        for (int i = tid; i < R * LANES; i += kThreads) {
-            const int row = i / LANES, d = (i % LANES) * 4;
-            if (rows.row0 + row >= rows.seq_rows) continue;
-            float2 tv = make_float2(kLowest, 0.0f);
-            float4 tx = make_float4(0, 0, 0, 0);
-            if (tail >= 0) {
-                tv = *reinterpret_cast<const float2*>(tail_record + row * (D + 4) + D);
-                tx = *reinterpret_cast<const float4*>(tail_record + row * (D + 4) + d);
+#pragma unroll 1
+        for (int i = tid; i < Rec4<D, NT>::sums; i += kThreads) {
+            const int two = i / (D / 16 * 32) * 4 + (i & 3);   // its two rows
+            float4 ml = make_float4(kLowest, 0.0f, kLowest, 0.0f), x = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int w = g; w <= w1 + (tail >= 0); ++w)
+                join(ml, x, w <= w1 ? sh.ml[w][two] : tail_record[Rec4<D, NT>::sums + two], w <= w1 ? sh.merge[w][i] : tail_record[i]);
+            if (complete) {
+                emit4<D, KIND>(a, rows, i / (D / 16 * 32), i / 32 % (D / 16), lane, x, ml, gain, fp16);
+            } else {
+                record[i] = x;
+                if (i % (D / 16 * 32) < 4) record[Rec4<D, NT>::sums + two] = ml;
             }
-            float2 v[kWarps];
-            float m = tv.x;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                v[w] = w >= g && w <= w1 ? sh.ml[w][row] : make_float2(kLowest, 0.0f);
-                m = fmaxf(m, v[w].x);
-            }
-            const float tf = exp2_approx(tv.x - m);
-            float l = tv.y * tf;
-            float4 acc = make_float4(tx.x * tf, tx.y * tf, tx.z * tf, tx.w * tf);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < g || w > w1) continue;
-                const float f = exp2_approx(v[w].x - m);
-                const float4 x = *reinterpret_cast<const float4*>(&sh.merge[w][row][d]);
-                l += v[w].y * f;
-                acc.x += x.x * f;
-                acc.y += x.y * f;
-                acc.z += x.z * f;
-                acc.w += x.w * f;
-            }
-            emit<D>(a, rows, row, d, acc, m, l, record, fp16, gain);
         }
     }
 }
 
 // ------------------------------------------------------------------ joining cut items
 // CTA i takes the item that is cut at the end of share i, if it began in share i: its pieces are record 1 of CTA i and
-// record 0 of the CTAs after it.  A row's lanes first read the pieces' references and sums, one each, and turn them
-// into weights; the sums of O then have no order to wait for but their own.
-template <int D, int NT, int TP>
-__global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a, bool fp16, float gain16) {
-    constexpr int R = 8 * NT;
+// record 0 of the CTAs after it.  The pieces' references and sums are turned into weights first, a piece a lane and two
+// rows a warp at a time; the sums of O then have no order to wait for but their own.
+template <int D, int NT, int KIND>
+__global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a, bool fp16) {
+    constexpr int R = 8 * NT, TP = TileOf<D, KIND>::positions, SLOTS = Rec4<D, NT>::sums, SIZE = Rec4<D, NT>::size;
+    constexpr int PER = SLOTS / (kCombineWarps * 32) > 0 ? SLOTS / (kCombineWarps * 32) : 1;   // float4s a thread
+    __shared__ float2 weight_of[32][4 * NT];   // of a piece, for two rows
+    __shared__ float4 scale_ml[4 * NT];        // two rows: what the sums so far are scaled by; in the end m and l
+    __shared__ float4 total_ml[4 * NT];
     __shared__ int sums[kCombineWarps];
     __shared__ Where at;
     int before, own;
@@ -633,53 +652,68 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     // what the main kernel wrote is read after this; every CTA waits, so that the grid ends after it
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (pieces == 0) return;
-    const float gain = gain16 * (a.c.kv_type == TKV_INT4 && a.c.v_gain ? __ldg(a.c.v_gain + rows.h) : 1.0f);
-    const int lane = threadIdx.x & 31, d = lane * (D / 32);
-    for (int row = threadIdx.x >> 5; row < R; row += kCombineWarps) {   // a warp a row, D / 32 channels a lane
-        if (rows.row0 + row >= rows.seq_rows) continue;
-        auto record = [&](int i) { return a.part + ((int64_t)(2 * (blockIdx.x + i) + (i ? 0 : 1)) * R + row) * (D + 4); };
-        float m = kLowest, l = 0.0f;
-        float acc[4] = {0, 0, 0, 0};
-        for (int i0 = 0; i0 < pieces; i0 += 32) {
-            float2 v = make_float2(kLowest, 0.0f);
-            if (i0 + lane < pieces) v = *reinterpret_cast<const float2*>(record(i0 + lane) + D);
-            float top = v.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? __ldg(a.c.v_gain + rows.h) : 1.0f) : 1.0f;
+    auto record = [&](int i) { return a.part + (int64_t)(2 * (blockIdx.x + i) + (i ? 0 : 1)) * SIZE; };
+    float4 x[PER];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = fmaxf(top, m);
-            const float f = exp2_approx(m - top), w = exp2_approx(v.x - top);
-            m = top;
-            float add = v.y * w;
+    for (int k = 0; k < PER; ++k) x[k] = make_float4(0, 0, 0, 0);
+    float4 ml = make_float4(kLowest, 0.0f, kLowest, 0.0f);   // of warp w's two rows, w < 4 NT
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+        const int n = min(32, pieces - i0);
+        if (warp < 4 * NT) {
+            float4 v = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+            if (lane < n) v = record(i0 + lane)[SLOTS + warp];
+            float m0 = v.x, m1 = v.z;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-            l = l * f + add;
+            for (int o = 16; o; o >>= 1) {
+                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            }
+            m0 = fmaxf(m0, ml.x);
+            m1 = fmaxf(m1, ml.z);
+            const float w0 = exp2_approx(v.x - m0), w1 = exp2_approx(v.z - m1), f0 = exp2_approx(ml.x - m0), f1 = exp2_approx(ml.z - m1);
+            float l0 = v.y * w0, l1 = v.w * w1;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[k] *= f;
-            const int n = min(32, pieces - i0);
-            for (int i = 0; i < n; i += 8) {   // eight loads in flight; behind the last piece its weight is 0
-                float4 x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float* rec = record(i0 + min(i + k, n - 1)) + d;
-                    if (D == 128) {
-                        x[k] = *reinterpret_cast<const float4*>(rec);
-                    } else {
-                        const float2 y = *reinterpret_cast<const float2*>(rec);
-                        x[k] = make_float4(y.x, y.y, 0.0f, 0.0f);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float wk = i + k < n ? __shfl_sync(0xffffffffu, w, (i + k) & 31) : 0.0f;
-                    acc[0] += x[k].x * wk; acc[1] += x[k].y * wk; acc[2] += x[k].z * wk; acc[3] += x[k].w * wk;
-                }
+            for (int o = 16; o; o >>= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+            }
+            ml = make_float4(m0, ml.y * f0 + l0, m1, ml.w * f1 + l1);
+            weight_of[lane][warp] = make_float2(w0, w1);
+            if (lane == 0) {
+                scale_ml[warp] = make_float4(f0, f1, 0.0f, 0.0f);
+                total_ml[warp] = ml;
             }
         }
-        if (D == 64) {   // two lanes' channels into one
-            acc[2] = __shfl_down_sync(0xffffffffu, acc[0], 1);
-            acc[3] = __shfl_down_sync(0xffffffffu, acc[1], 1);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + k * kCombineWarps * 32;
+            if (i >= SLOTS) break;
+            const int two = i / (D / 16 * 32) * 4 + (i & 3);
+            const float4 f = scale_ml[two];
+            float4 sum = make_float4(x[k].x * f.x, x[k].y * f.y, x[k].z * f.x, x[k].w * f.y);
+#pragma unroll 1
+            for (int p = 0; p < n; p += 8) {   // eight loads in flight; behind the last piece its weight is 0
+                float4 y[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = record(i0 + min(p + q, n - 1))[i];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float2 w = p + q < n ? weight_of[p + q][two] : make_float2(0.0f, 0.0f);
+                    sum = make_float4(sum.x + y[q].x * w.x, sum.y + y[q].y * w.y, sum.z + y[q].z * w.x, sum.w + y[q].w * w.y);
+                }
+            }
+            x[k] = sum;
         }
-        if (D == 128 || !(lane & 1)) emit<D>(a, rows, row, d, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l, nullptr, fp16, gain);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = tid + k * kCombineWarps * 32;
+        if (i >= SLOTS) break;
+        emit4<D, KIND>(a, rows, i / (D / 16 * 32), i / 32 % (D / 16), lane, x[k], total_ml[i / (D / 16 * 32) * 4 + (i & 3)], gain, fp16);
     }
 }
 
@@ -701,7 +735,6 @@ cudaError_t launch(PagedAttnArgs& a, cudaStream_t st) {
     using C = Config<D, NT, KIND>;
     constexpr int smem = sizeof(Shared<D, NT, KIND>);
     static_assert(C::ctas * (smem + 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
-    static_assert(8 * C::row_stride * 4 <= TileOf<D, KIND>::bytes, "eight rows leave by way of a slot");
     int dev = 0;
     cudaError_t e = device_ctas(C::ctas, &a.grid, &dev);
     // the kernel's shared-memory limit, once a device
@@ -723,8 +756,7 @@ cudaError_t launch(PagedAttnArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const bool fp16 = KIND == kFp16 || (KIND == kInt4 && a.q_fp16);
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, NT, TileOf<D, KIND>::positions>, (const PagedAttnArgs)a, fp16,
-                              KIND == kInt4 ? 16.0f : 1.0f);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, NT, KIND>, (const PagedAttnArgs)a, fp16);
 }
 
 template <int D, int NT>
@@ -775,7 +807,7 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.out = out;
     a.lse = lse;
     a.cu = cu_tokens;
-    a.part = reinterpret_cast<float*>(workspace);
+    a.part = reinterpret_cast<float4*>(workspace);
     a.status = status;
     a.rows = rows;
     a.q_row = q_row_stride;
