@@ -54,6 +54,32 @@ __device__ __forceinline__ float2 rotate_pair(float x0, float x1, float2 cs) {
                        __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y)));
 }
 
+// Two fp32 numbers an instruction.  A packed product and a packed sum of the same rounding may be fused into one; these two
+// have different ones.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2_rz(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // (cos, sin) of pair j at position p; NaN outside the table, where *bad is set.
 __device__ __forceinline__ float2 table_at(const float2* table, int pairs, int max_positions, int p, int j,
                                            float sign, bool* bad) {

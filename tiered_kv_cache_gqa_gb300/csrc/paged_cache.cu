@@ -1,14 +1,17 @@
 // Rows into and out of a paged cache: tkv_paged_append (k rotated on the way) and tkv_paged_gather.
 //
 // A step's rows are ragged: sequence b owns rows cu[b] .. cu[b + 1], which are the last positions of its
-// lengths[b].  A thread takes one block of 16 channels of a row and walks over KV heads, K and V, so the
-// 16 cosines and sines (or none, for V) stay in its registers; the eight (four) threads of a head's
-// row and the rows of a record lie next to one another in memory.
+// lengths[b].  A thread of the append takes, of a row of K and of V, 16 bytes of channels and the 16 bytes that hold
+// their partners (or 16 bytes alone, where k is not rotated by halves), and walks over KV heads: each value is read
+// once, and the row's place and the 8 cosines and sines are found once for all its heads; two neighbours share a scale.  A thread of
+// the gather writes 16 bytes of K and of V.  So each instruction of a warp reads and writes whole sectors: with 32 bytes
+// a thread, in two halves, the gather sent 164 MB to L2 for the 75 MB that it wrote.
 //
 // What bounds both is memory: 2 bytes a value on one side, 0.5625 (codes and scales) or 2 on the other.
 #include <algorithm>
+#include <type_traits>
 
-#include "paged.cuh"
+#include "paged_tile.cuh"
 
 using namespace tkv;
 
@@ -29,7 +32,8 @@ struct RowArgs {
     int lanes;                 // heads that the threads of a row take at once
     int page_shift;
     float sign;
-    uint8_t pair_axis[256];
+    int units;                 // append: threads of a row
+    alignas(16) uint8_t pair_axis[256];
 };
 
 // Where row `row` of the step lies: page and position in the page; false for no row (behind the last
@@ -49,224 +53,335 @@ __device__ __forceinline__ bool place_of_row(const RowArgs& a, int64_t row, int6
     return true;
 }
 
-// 16 values -> 16 codes (8 bytes) and the byte of their scale.
-//   scale = e4m3(max |x| / (7 gain)), to nearest even; q = round(x / (scale * gain)), to nearest even,
-// both quotients divided and not multiplied by a reciprocal, so that a tie stays one.  A block that
-// holds an infinity or a NaN gets the NaN scale: it reads as NaN, not as something finite.
-__device__ __forceinline__ uint2 quantise_block(const float (&x)[16], float gain, uint8_t* scale_byte) {
-    uint32_t top = 0;   // |x| as bits: NaN > infinity > finite
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    const float amax = __uint_as_float(top);
-    const bool bad = top >= 0x7F800000u;
+// max(|a|, |b|, |c|); NaN if one of them is
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// The largest |x| of a block, of which 8 values are the neighbouring lane's (xor 1); NaN if one is.  The whole warp calls it
+// (but the lanes that have left): a mask of its own for each pair of lanes made the shuffle sixteen times as long.
+__device__ __forceinline__ float block_max(const float (&x)[8]) {
+    const float m = max3_abs(max3_abs(max3_abs(x[0], x[1], x[2]), x[3], x[4]), max3_abs(x[5], x[6], x[7]), 0.0f);
+    return max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.0f);
+}
+
+// 8 values of a block with that maximum -> 8 codes and the byte of the block's scale.
+//   scale = e4m3(max |x| / (7 gain)), to nearest even; q = x / step, step = scale * gain, to nearest even.
+// The quotients are products with 1 / (7 gain) and 1 / step, cut towards zero.  Where gain is a power of two, 7 gain and
+// step (four bits) have rounded reciprocals that are never below the true ones (for 7 and all eight steps; by less than
+// 2^-24), so the cut product of an exact tie is the tie, and it goes to the even side as the quotient would; elsewhere
+// only a quotient within 2^-22 of a tie could round to the other side.
+// Adding 1.5 * 2^23 + 8 rounds to an integer whose low four bits are q + 8.
+// A block that holds an infinity or a NaN gets the NaN scale: it reads as NaN, not as something finite.
+__device__ __forceinline__ uint32_t quantise_half(float (&x)[8], float amax, float gain, float inv_7_gain, uint8_t* scale_byte) {
+    const bool bad = !(amax < INFINITY);
     const __nv_fp8_storage_t s8 =
-        bad ? (__nv_fp8_storage_t)0x7F : __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(7.0f, gain)), __NV_SATFINITE, __NV_E4M3);
-    const __half_raw hr = __nv_cvt_fp8_to_halfraw(s8, __NV_E4M3);
-    const float step = __fmul_rn(__half2float(__half(hr)), gain);
+        bad ? (__nv_fp8_storage_t)0x7F : __nv_cvt_float_to_fp8(__fmul_rz(amax, inv_7_gain), __NV_SATFINITE, __NV_E4M3);
     *scale_byte = (uint8_t)s8;
-    uint32_t w[2] = {0, 0};
-    const bool zero = bad || !(step > 0.0f);
+    const float step = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3))), gain);
+    const float inv = step > 0.0f ? __frcp_rn(step) : 0.0f;
+    if (amax * inv >= 7.5f) {   // a scale that saturated, or was rounded down far below 2^-6; elsewhere |x| <= 7.44 steps
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float y = zero ? 0.0f : __fdiv_rn(x[i], step);
-        const int q = __float2int_rn(fminf(fmaxf(y, -7.0f), 7.0f)) + 8;
-        w[i >> 3] |= (uint32_t)q << (4 * (i & 7));
+        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -7.0f * step), 7.0f * step);
     }
-    return make_uint2(w[0], w[1]);
+    uint32_t pair[4];
+    const F2 inv2 = f2(inv, inv), to_int = f2(12582920.0f, 12582920.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = parts(add2(mul2_rz(f2(x[2 * i], x[2 * i + 1]), inv2), to_int));
+        pair[i] = __float_as_uint(q.y) * 16u + __float_as_uint(q.x);   // the low byte holds both codes
+    }
+    const uint32_t codes = __byte_perm(__byte_perm(pair[0], pair[1], 0x0040), __byte_perm(pair[2], pair[3], 0x0040), 0x5410);
+    return bad ? 0x88888888u : codes;
 }
 
+// 16 bytes as floats, and back.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
-    Vec16<T> a, b;
-    a.u = *reinterpret_cast<const uint4*>(p);
-    b.u = *(reinterpret_cast<const uint4*>(p) + 1);
+__device__ __forceinline__ void unpack(uint4 u, float (&x)[16 / sizeof(T)]) {
+    Vec16<T> v;
+    v.u = u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = to_float(a.e[i]);
-        x[8 + i] = to_float(b.e[i]);
-    }
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = to_float(v.e[i]);
 }
-
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
-    constexpr int E = 16 / sizeof(T);
+__device__ __forceinline__ uint4 pack(const float* x) {
+    Vec16<T> v;
 #pragma unroll
-    for (int k = 0; k < 16 / E; ++k) {
-        Vec16<T> o;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o.e[i] = from_float<T>(x[k * E + i]);
-        *(reinterpret_cast<uint4*>(p) + k) = o.u;
-    }
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) v.e[i] = from_float<T>(x[i]);
+    return v.u;
 }
 
-// How a block of 16 channels of k is rotated.
+// How k is rotated.
 //   kNone      not at all
-//   kHalves    pairs % 16 == 0: the partners are a whole block, `pairs` channels away
-//   kAdjacent  pairs % 8 == 0: the block holds its own 8 pairs
+//   kHalves    pairs % 16 == 0: the partners of 8 channels lie `pairs` channels away, in another block
+//   kAdjacent  pairs % 4 == 0: 8 channels hold their own 4 pairs
 //   kAny       channel by channel, partners read one at a time
 enum Turn { kNone, kHalves, kAdjacent, kAny };
 
-// The block's 16 cosines and sines, one a channel (kHalves, kAny) or one a pair (kAdjacent: the first 8).
-template <int TURN>
-__device__ __forceinline__ void block_angles(const RowArgs& a, const uint8_t* axis_of, int64_t row, int own_position,
-                                             int block, float2 (&cs)[16]) {
+// cs[i] = (cos, sin) of pair j0 + i at the row's positions; j0 a multiple of N, the table's rows of 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_angles(const RowArgs& a, const int (&p)[4], int j0, float2 (&cs)[N]) {
     bool bad = false;
+    if (a.num_axes == 1) {
+        const bool in = (uint32_t)p[0] < (uint32_t)a.max_positions;
+        const float4* at = reinterpret_cast<const float4*>(a.table + (int64_t)(in ? p[0] : 0) * a.pairs + j0);
+        const float nan = __int_as_float(0x7FC00000);
 #pragma unroll
-    for (int i = 0; i < (TURN == kAdjacent ? 8 : 16); ++i) {
-        const int ch = 16 * block + (TURN == kAdjacent ? 2 * i : i);
-        cs[i] = make_float2(1.0f, 0.0f);
-        if (ch >= 2 * a.pairs) continue;
-        const int j = TURN == kAdjacent || (TURN == kAny && a.interleaved) ? ch >> 1 : ch < a.pairs ? ch : ch - a.pairs;
-        const int p = a.positions ? __ldg(a.positions + (a.num_axes > 1 ? axis_of[j] : 0) * a.axis_stride + row) : own_position;
-        cs[i] = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
+        for (int i = 0; i < N / 2; ++i) {
+            const float4 v = __ldg(at + i);
+            cs[2 * i] = in ? make_float2(v.x, v.y * a.sign) : make_float2(nan, nan);
+            cs[2 * i + 1] = in ? make_float2(v.z, v.w * a.sign) : make_float2(nan, nan);
+        }
+        bad = !in;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int x = a.pair_axis[j0 + i];
+            cs[i] = table_at(a.table, a.pairs, a.max_positions, x == 0 ? p[0] : x == 1 ? p[1] : x == 2 ? p[2] : p[3], j0 + i, a.sign, &bad);
+        }
     }
     if (bad) raise_status(a.status, TKV_EINVAL);
 }
 
-// Block `block` of head row k, rotated.
-template <typename T, int TURN>
-__device__ __forceinline__ void rotated_block(const RowArgs& a, const T* k, int block, const float2 (&cs)[16], float (&x)[16]) {
-    load16(k + 16 * block, x);
-    if (TURN == kNone || 16 * block >= 2 * a.pairs) return;
-    if (TURN == kHalves) {
-        const bool first = 16 * block < a.pairs;
-        float y[16];
-        load16(k + 16 * block + (first ? a.pairs : -a.pairs), y);
+// Channels 8 chunk .. + 7 of head row k, turned one at a time (kAny).
+template <typename T>
+__device__ __forceinline__ void turn_any(const RowArgs& a, const T* k, int64_t row, int own_position, int chunk, float (&x)[8]) {
+    bool bad = false;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const int ch = 8 * chunk + i;
+        if (ch >= 2 * a.pairs) break;
+        const bool first = a.interleaved ? !(ch & 1) : ch < a.pairs;
+        const int j = a.interleaved ? ch >> 1 : first ? ch : ch - a.pairs;
+        const int p = a.positions ? __ldg(a.positions + a.pair_axis[j] * a.axis_stride + row) : own_position;
+        const float2 cs = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
+        const float own = to_float(k[ch]), other = to_float(k[a.interleaved ? ch ^ 1 : first ? ch + a.pairs : ch - a.pairs]);
+        const float y = first ? rotate_pair(own, other, cs).x : rotate_pair(other, own, cs).y;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = first ? rotate_pair(x[i], y[i], cs[i]).x : rotate_pair(y[i], x[i], cs[i]).y;
-    } else if (TURN == kAdjacent) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 y = rotate_pair(x[2 * i], x[2 * i + 1], cs[i]);
-            x[2 * i] = y.x;
-            x[2 * i + 1] = y.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int ch = 16 * block + i;
-            if (ch >= 2 * a.pairs) continue;
-            const bool first = a.interleaved ? !(ch & 1) : ch < a.pairs;
-            const float other = to_float(k[a.interleaved ? ch ^ 1 : first ? ch + a.pairs : ch - a.pairs]);
-            x[i] = first ? rotate_pair(x[i], other, cs[i]).x : rotate_pair(other, x[i], cs[i]).y;
-        }
+        for (int c = 0; c < 8; ++c) x[c] = c == i ? y : x[c];
     }
+    if (bad) raise_status(a.status, TKV_EINVAL);
 }
 
-template <typename T, int D, bool INT4, int TURN>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int NB = D / 16;
-    __shared__ uint8_t axis_of[256];
-    if (TURN != kNone && a.num_axes > 1) {
-        axis_of[threadIdx.x] = a.pair_axis[threadIdx.x];
-        __syncthreads();
+// Where a chunk of a row goes (4-bit pages: its codes and its block's scale), in the page of the first head, and its
+// partner; from head to head it moves by the size of a head's page.
+template <typename T, int D, bool INT4>
+struct Target {
+    uint8_t *to, *scale;
+    int partner, scale_partner;
+    __device__ __forceinline__ Target(uint8_t* page, int page_size, int off, int which, int chunk, int pair_chunks) {
+        using R = Record<D>;
+        if (INT4) {
+            const int r = off & 15;
+            uint8_t* rec = page + (off >> 4) * R::bytes;
+            to = rec + (which ? R::v_codes : R::k_codes) + r * (D / 2) + 4 * chunk;
+            scale = rec + (which ? R::v_scales + (chunk >> 1) * 16 + r : R::k_scales + r * (D / 16) + (chunk >> 1));
+            partner = 4 * pair_chunks;
+            scale_partner = (pair_chunks >> 1) * (which ? 16 : 1);
+        } else {
+            to = page + ((int64_t)which * page_size + off) * (2 * D) + 16 * chunk;
+            scale = nullptr;
+            partner = 16 * pair_chunks;
+            scale_partner = 0;
+        }
     }
-    // block fastest, then the row, then the head lane: eight threads a head's row, whole records a warp
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int block = (int)(i % NB);
-    const int64_t row = i / NB;
-    const int lane = blockIdx.y;
-    if (row >= a.rows) return;
+    // x, and y to the partner's place if there is one
+    __device__ __forceinline__ void put(float (&x)[8], float (&y)[8], bool two, int chunk, float gain) {
+        if (INT4) {
+            const float inv_7_gain = __frcp_rn(__fmul_rn(7.0f, gain));
+            const float x_max = block_max(x), y_max = block_max(y);
+            uint8_t s;
+            *reinterpret_cast<uint32_t*>(to) = quantise_half(x, x_max, gain, inv_7_gain, &s);
+            if (!(chunk & 1)) *scale = s;
+            if (two) {
+                *reinterpret_cast<uint32_t*>(to + partner) = quantise_half(y, y_max, gain, inv_7_gain, &s);
+                if (!(chunk & 1)) scale[scale_partner] = s;
+            }
+        } else {
+            *reinterpret_cast<uint4*>(to) = pack<T>(x);
+            if (two) *reinterpret_cast<uint4*>(to + partner) = pack<T>(y);
+        }
+    }
+};
+
+// blockIdx.y: the first head.  The threads of a row are an even number, so neighbours share its place.
+// 18,432 rows of 8 heads of 128 into 4-bit pages: 33 us (97 MB, 2.9 TB/s; 27 us without the rotation).  What bounds it there
+// is instructions, about 80 for 8 values; three CTAs an SM were faster than two (36 us) and than four (36 us, spills).
+template <typename T, int D, bool INT4, int TURN>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ RowArgs a) {
+    const int rows_here = kThreads / a.units;
+    const int unit = threadIdx.x % a.units;
+    const int64_t row = (int64_t)blockIdx.x * rows_here + threadIdx.x / a.units;
+    if (threadIdx.x >= rows_here * a.units || row >= a.rows) return;
+    // units of kHalves: the pairs of chunks, then the chunks behind the rotated ones
+    const int pair_chunks = TURN == kHalves ? a.pairs / 8 : 0;
+    const int chunk = TURN == kHalves && unit >= pair_chunks ? unit + pair_chunks : unit;
+    const bool two = TURN == kHalves && unit < pair_chunks;
+    const bool turned = TURN != kNone && 8 * chunk < 2 * a.pairs;
+    const T* k = reinterpret_cast<const T*>(a.k) + row * a.k_row;
+    const T* k_at = k + blockIdx.y * a.k_head + 8 * chunk;
+    const T* v_at = reinterpret_cast<const T*>(a.v) + row * a.v_row + blockIdx.y * a.v_head + 8 * chunk;
+    // The next head's values are read while the last one's are worked on, the first one's and the positions before the row's
+    // place is looked for: what a thread waits for is memory, several times in a row.
+    uint4 raw[4] = {};
+    auto read = [&](int h) {
+        if (h >= a.c.num_kv_heads) return;
+        raw[0] = __ldg(reinterpret_cast<const uint4*>(k_at));
+        raw[2] = __ldg(reinterpret_cast<const uint4*>(v_at));
+        if (two) {
+            raw[1] = __ldg(reinterpret_cast<const uint4*>(k_at + a.pairs));
+            raw[3] = __ldg(reinterpret_cast<const uint4*>(v_at + a.pairs));
+        }
+        k_at += a.lanes * a.k_head;
+        v_at += a.lanes * a.v_head;
+    };
+    read(blockIdx.y);
+    int p[4] = {0, 0, 0, 0};
+    if (turned && a.positions) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x < a.num_axes) p[x] = __ldg(a.positions + x * a.axis_stride + row);
+    }
     int64_t page;
     int off, position;
     if (!place_of_row(a, row, &page, &off, &position)) {
-        if (page == -1 && block == 0 && lane == 0) raise_status(a.status, TKV_ECAPACITY);
+        if (page == -1 && unit == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
         return;
     }
-    float2 cs[16];
-    if (TURN != kNone && 16 * block < 2 * a.pairs) block_angles<TURN>(a, axis_of, row, position, block, cs);
-    const T* k = reinterpret_cast<const T*>(a.k) + row * a.k_row;
-    const T* v = reinterpret_cast<const T*>(a.v) + row * a.v_row;
-    for (int h = lane; h < a.c.num_kv_heads; h += a.lanes) {
-        float x[16], y[16];
-        rotated_block<T, TURN>(a, k + h * a.k_head, block, cs, x);
-        load16(v + h * a.v_head + 16 * block, y);
+    constexpr int NCS = TURN == kHalves ? 8 : 4;
+    float2 cs[NCS];
+    if ((TURN == kHalves || TURN == kAdjacent) && turned) {
+        if (!a.positions) p[0] = position;
+        load_angles<NCS>(a, p, NCS * chunk, cs);
+    }
+    const int64_t head_bytes = INT4 ? (int64_t)(a.c.page_size >> 4) * Record<D>::bytes : (int64_t)a.c.page_size * (4 * D);
+    uint8_t* head = reinterpret_cast<uint8_t*>(a.c.pages) + (page * a.c.num_kv_heads + blockIdx.y) * head_bytes;
+    Target<T, D, INT4> kt(head, a.c.page_size, off, 0, chunk, pair_chunks), vt(head, a.c.page_size, off, 1, chunk, pair_chunks);
+    const int64_t next = a.lanes * head_bytes;
+#pragma unroll 1
+    for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes) {
+        float x[8], y[8], vx[8], vy[8];
+        unpack<T>(raw[0], x);
+        unpack<T>(raw[2], vx);
+        unpack<T>(raw[1], y);
+        unpack<T>(raw[3], vy);
+        read(h + a.lanes);
+        if (TURN == kHalves && turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 z = rotate_pair(x[i], y[i], cs[i % NCS]);
+                x[i] = z.x;
+                y[i] = z.y;
+            }
+        } else if (TURN == kAdjacent && turned) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 z = rotate_pair(x[2 * i], x[2 * i + 1], cs[i % NCS]);
+                x[2 * i] = z.x;
+                x[2 * i + 1] = z.y;
+            }
+        } else if (TURN == kAny && turned) {
+            turn_any(a, k + h * a.k_head, row, position, chunk, x);
+        }
+        kt.put(x, y, two, chunk, INT4 && a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f);
+        vt.put(vx, vy, two, chunk, INT4 && a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f);
+        kt.to += next;
+        vt.to += next;
         if (INT4) {
-            using R = Record<D>;
-            const int r = off & 15;
-            uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) +
-                           ((page * a.c.num_kv_heads + h) * (a.c.page_size / kGroup) + (off >> 4)) * R::bytes;
-            const float kg = a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f, vg = a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f;
-            uint8_t s;
-            const uint2 kc = quantise_block(x, kg, &s);
-            *reinterpret_cast<uint2*>(rec + R::k_codes + r * (D / 2) + 8 * block) = kc;
-            rec[R::k_scales + r * NB + block] = s;
-            const uint2 vc = quantise_block(y, vg, &s);
-            *reinterpret_cast<uint2*>(rec + R::v_codes + r * (D / 2) + 8 * block) = vc;
-            rec[R::v_scales + block * 16 + r] = s;
-        } else {
-            T* base = reinterpret_cast<T*>(a.c.pages) + ((page * a.c.num_kv_heads + h) * 2 * a.c.page_size + off) * D + 16 * block;
-            store16(base, x);
-            store16(base + (int64_t)a.c.page_size * D, y);
+            kt.scale += next;
+            vt.scale += next;
         }
     }
 }
 
-// 8 bytes of codes -> the values q * scale * gain: the product of code and scale is exact, one rounding.
-__device__ __forceinline__ void expand_block(uint2 w, uint8_t scale_byte, float gain, float (&x)[16]) {
-    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)scale_byte, __NV_E4M3);
-    const float s = __half2float(__half(hr));
+// N codes (4 bits each, from bit 0) -> the values q * scale * gain, one rounding: the pairs of codes i and i + 4 become
+// q * scale / 16 in fp16, exactly (as in the attention), and are multiplied by 16 gain in fp32.
+template <int N>
+__device__ __forceinline__ void expand(uint32_t word, uint8_t scale_byte, float gain, float (&x)[N]) {
+    const __half s = __hmul(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)scale_byte, __NV_E4M3)), __float2half(0.0625f));
+    const __half2 s2 = __half2half2(s), n1032 = __hmul2(s2, both(-1032.0f)), n72 = __hmul2(s2, both(-72.0f));
+    const float g16 = 16.0f * gain;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int q = (int)(((i < 8 ? w.x : w.y) >> (4 * (i & 7))) & 15u) - 8;
-        x[i] = __fmul_rn(__fmul_rn((float)q, s), gain);
+    for (int i = 0; i < 4; i += 2) {
+        const uint32_t w = word >> (4 * i);
+        const float2 lo = __half22float2(bits_half2(expand_low(w, s2, n1032))), hi = __half22float2(bits_half2(expand_high(w, s2, n72)));
+        x[i] = __fmul_rn(lo.x, g16);
+        x[i + 1] = __fmul_rn(hi.x, g16);
+        if (N == 8) {
+            x[(i + 4) % N] = __fmul_rn(lo.y, g16);
+            x[(i + 5) % N] = __fmul_rn(hi.y, g16);
+        }
     }
 }
 
-// TO: element type of the outputs; T: of 16-bit pages.
+// TO: element type of the outputs; T: of 16-bit pages.  blockIdx.y: the first head.
 template <typename TO, typename T, int D, bool INT4>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int NB = D / 16;
+    constexpr int N = 16 / sizeof(TO), NC = D / N;   // values of a thread, threads of a row
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int block = (int)(i % NB);
-    const int64_t row = i / NB;
+    const int chunk = (int)(i % NC);
+    const int64_t row = i / NC;
     const int lane = blockIdx.y;
     if (row >= a.rows) return;
     int64_t page;
     int off = 0, position;
     const bool good = place_of_row(a, row, &page, &off, &position);
     if (page == -2) return;
-    if (!good && block == 0 && lane == 0) raise_status(a.status, TKV_ECAPACITY);
-    TO* k = reinterpret_cast<TO*>(const_cast<void*>(a.k)) + row * a.k_row;
-    TO* v = reinterpret_cast<TO*>(const_cast<void*>(a.v)) + row * a.v_row;
+    if (!good && chunk == 0 && lane == 0) raise_status(a.status, TKV_ECAPACITY);
+    TO* k = reinterpret_cast<TO*>(const_cast<void*>(a.k)) + row * a.k_row + lane * a.k_head + N * chunk;
+    TO* v = reinterpret_cast<TO*>(const_cast<void*>(a.v)) + row * a.v_row + lane * a.v_head + N * chunk;
+    using R = Record<D>;
+    const int r = off & 15, block = N * chunk / 16;
+    const int64_t head_bytes = INT4 ? (int64_t)(a.c.page_size >> 4) * R::bytes : (int64_t)a.c.page_size * (4 * D);
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(a.c.pages) + ((good ? page : 0) * a.c.num_kv_heads + lane) * head_bytes +
+                          (INT4 ? (off >> 4) * R::bytes : off * (2 * D));
+#pragma unroll 4   // the pages are read-only here: four heads' loads go out before the first is stored
     for (int h = lane; h < a.c.num_kv_heads; h += a.lanes) {
-        float x[16], y[16];
+        float x[N], y[N];
         if (!good) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = y[j] = __int_as_float(0x7FC00000);
+            for (int j = 0; j < N; ++j) x[j] = y[j] = __int_as_float(0x7FC00000);
         } else if (INT4) {
-            using R = Record<D>;
-            const int r = off & 15;
-            const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.c.pages) +
-                                 ((page * a.c.num_kv_heads + h) * (a.c.page_size / kGroup) + (off >> 4)) * R::bytes;
-            const uint2 kc = *reinterpret_cast<const uint2*>(rec + R::k_codes + r * (D / 2) + 8 * block);
-            const uint2 vc = *reinterpret_cast<const uint2*>(rec + R::v_codes + r * (D / 2) + 8 * block);
-            const uint8_t ks = rec[R::k_scales + r * NB + block], vs = rec[R::v_scales + block * 16 + r];
-            expand_block(kc, ks, a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f, x);
-            expand_block(vc, vs, a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f, y);
+            using Codes = typename std::conditional<N == 8, uint32_t, uint16_t>::type;
+            const Codes kc = __ldg(reinterpret_cast<const Codes*>(from + R::k_codes + r * (D / 2)) + chunk);
+            const Codes vc = __ldg(reinterpret_cast<const Codes*>(from + R::v_codes + r * (D / 2)) + chunk);
+            const uint8_t ks = __ldg(from + R::k_scales + r * (D / 16) + block), vs = __ldg(from + R::v_scales + block * 16 + r);
+            expand<N>(kc, ks, a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f, x);
+            expand<N>(vc, vs, a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f, y);
         } else {
-            const T* base = reinterpret_cast<const T*>(a.c.pages) + ((page * a.c.num_kv_heads + h) * 2 * a.c.page_size + off) * D + 16 * block;
-            load16(base, x);
-            load16(base + (int64_t)a.c.page_size * D, y);
+            using Raw = typename std::conditional<N == 8, uint4, uint2>::type;
+            union {
+                Raw u;
+                T e[N];
+            } kr, vr;
+            kr.u = __ldg(reinterpret_cast<const Raw*>(from) + chunk);
+            vr.u = __ldg(reinterpret_cast<const Raw*>(from + (int64_t)a.c.page_size * (2 * D)) + chunk);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                x[j] = to_float(kr.e[j]);
+                y[j] = to_float(vr.e[j]);
+            }
         }
-        store16(k + h * a.k_head + 16 * block, x);
-        store16(v + h * a.v_head + 16 * block, y);
+        *reinterpret_cast<uint4*>(k) = pack<TO>(x);
+        *reinterpret_cast<uint4*>(v) = pack<TO>(y);
+        from += a.lanes * head_bytes;
+        k += a.lanes * a.k_head;
+        v += a.lanes * a.v_head;
     }
 }
 
-// Threads of a launch: a row's blocks in x, heads at once in y.  A thread walks over up to 8 heads
-// as long as a wave of threads is left (the table and the row's place are then read once for them).
-cudaError_t geometry(RowArgs& a, dim3* grid) {
+// How many heads the threads of a row take at once: a thread walks over up to 8 of them as long as 1,024 threads an SM
+// are left (the angles and the row's place are then read once for them).
+cudaError_t spread_heads(RowArgs& a, int64_t threads_a_head) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = a.rows * (a.c.head_dim / 16);
     const int hkv = a.c.num_kv_heads;
-    const int per_thread = (int)std::min<int64_t>(8, std::max<int64_t>(1, blocks * hkv / ((int64_t)sms * 1024)));
+    const int per_thread = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads_a_head * hkv / ((int64_t)sms * 1024)));
     a.lanes = std::min(65535, (hkv + per_thread - 1) / per_thread);
-    *grid = dim3((unsigned)((blocks + kThreads - 1) / kThreads), a.lanes);
     return cudaSuccess;
 }
 
@@ -360,13 +475,15 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
         a.interleaved = rotary->interleaved != 0;
         a.sign = rotary->inverse ? -1.0f : 1.0f;
         for (int j = 0; j < 256; ++j) a.pair_axis[j] = j < rotary->pairs ? rotary->pair_axis[j] : 0;
-        turn = a.interleaved ? (a.pairs % 8 == 0 ? kAdjacent : kAny) : (a.pairs % 16 == 0 ? kHalves : kAny);
+        turn = !aligned16(rotary->table) ? kAny : a.interleaved ? (a.pairs % 4 == 0 ? kAdjacent : kAny) : (a.pairs % 16 == 0 ? kHalves : kAny);
     }
     if (rows == 0) return TKV_OK;
     a.status = status;
-    dim3 grid;
-    cudaError_t e = geometry(a, &grid);
+    a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);
+    const int rows_a_block = kThreads / a.units;
+    cudaError_t e = spread_heads(a, rows * a.units);
     if (e == cudaSuccess) {
+        const dim3 grid((unsigned)((rows + rows_a_block - 1) / rows_a_block), a.lanes);
         if (dtype == TKV_BF16) append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream);
         else append_type<__half>(a, turn, grid, (cudaStream_t)stream);
         e = cudaGetLastError();
@@ -391,9 +508,10 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
         return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     a.status = status;
-    dim3 grid;
-    cudaError_t e = geometry(a, &grid);
+    const int64_t threads = rows * (cache->head_dim * dtype_size(dtype) / 16);
+    cudaError_t e = spread_heads(a, threads);
     if (e == cudaSuccess) {
+        const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), a.lanes);
         cudaStream_t st = (cudaStream_t)stream;
         if (dtype == TKV_BF16) gather_type<__nv_bfloat16>(a, grid, st);
         else if (dtype == TKV_FP16) gather_type<__half>(a, grid, st);
