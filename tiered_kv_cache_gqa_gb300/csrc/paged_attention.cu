@@ -508,15 +508,18 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             }
             if (failed) break;
             left -= tiles;
-            if (left == 0) {
-                flags |= piece.flags;
-                break;
-            }
-            if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-            if (++stage == S) stage = 0, parity ^= 1;
-            // The item ends here and others follow.  If it began before this warp's share, to a record: the CTA's first for
-            // the first warp (it joins the CTA before), else the warp's own.
             const bool cut = piece.flags & kContinues;
+            if (left == 0) {
+                if (cut || !(piece.flags & kEnds)) {   // the last piece, of an item that others hold parts of
+                    flags |= piece.flags;
+                    break;
+                }
+            } else {
+                if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+                if (++stage == S) stage = 0, parity ^= 1;
+            }
+            // The item ends here.  If it began before this warp's share, to a record: the CTA's first for the first warp (it
+            // joins the CTA before), else the warp's own.
             float4* record = a.part + (warp ? (int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + warp : (int64_t)blockIdx.x * 2) * Rec4<D, NT>::size;
             if (cut) flags = kHead;
             const float gain = gain_of(piece.rows.h);
@@ -590,9 +593,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     const uint32_t valid = __ballot_sync(0xffffffffu, f & kValid), continues = __ballot_sync(0xffffffffu, f & kContinues);
     const uint32_t ends = __ballot_sync(0xffffffffu, f & kEnds), heads = __ballot_sync(0xffffffffu, f & kHead);
     const uint32_t leads = valid & ~(continues & ~1u);
-#pragma unroll 1
-    for (uint32_t todo = leads; todo; todo &= todo - 1) {
-        const int g = __ffs(todo) - 1;
+    // all groups at once, each with its share of the CTA's warps
+    const int groups = __popc(leads), team = groups <= 1 ? 8 : groups == 2 ? 4 : groups <= 4 ? 2 : 1;
+    if (warp / team < groups) {
+        const int g = (int)__fns(leads, 0, warp / team + 1);
         const int w1 = __ffs((leads | heads | ~valid) & (~1u << g)) - 2;   // the last that follows
         const int tail = (heads >> (w1 + 1)) & 1 && !((ends >> w1) & 1) ? w1 + 1 : -1;
         const bool begins = !((continues >> g) & 1), complete = begins && (((ends >> w1) & 1) || tail >= 0);
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         const float4* tail_record = a.part + ((int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + tail) * Rec4<D, NT>::size;
         const float gain = gain_of(rows.h);
 #pragma unroll 1
-        for (int i = tid; i < Rec4<D, NT>::sums; i += kThreads) {
+        for (int i = warp % team * 32 + lane; i < Rec4<D, NT>::sums; i += team * 32) {
             const int two = i / (D / 16 * 32) * 4 + (i & 3);   // its two rows
             float4 ml = make_float4(kLowest, 0.0f, kLowest, 0.0f), x = make_float4(0, 0, 0, 0);
 #pragma unroll 1
@@ -654,13 +658,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     if (pieces == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? __ldg(a.c.v_gain + rows.h) : 1.0f) : 1.0f;
-    auto record = [&](int i) { return a.part + (int64_t)(2 * (blockIdx.x + i) + (i ? 0 : 1)) * SIZE; };
+    const float4* first = a.part + (int64_t)2 * blockIdx.x * SIZE;
+    auto record = [&](int i) { return first + (i ? 2 * i * SIZE : SIZE); };
     float4 x[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) x[k] = make_float4(0, 0, 0, 0);
     float4 ml = make_float4(kLowest, 0.0f, kLowest, 0.0f);   // of warp w's two rows, w < 4 NT
     for (int i0 = 0; i0 < pieces; i0 += 32) {
         const int n = min(32, pieces - i0);
+        float4 y[PER][8];   // eight loads in flight, the first of them while the weights are worked out
+        auto read = [&](int p) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[k][q] = record(i0 + min(p + q, n - 1))[min(tid + k * kCombineWarps * 32, SLOTS - 1)];
+        };
+        read(0);
         if (warp < 4 * NT) {
             float4 v = make_float4(kLowest, 0.0f, kLowest, 0.0f);
             if (lane < n) v = record(i0 + lane)[SLOTS + warp];
@@ -687,25 +700,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int i = tid + k * kCombineWarps * 32;
-            if (i >= SLOTS) break;
-            const int two = i / (D / 16 * 32) * 4 + (i & 3);
-            const float4 f = scale_ml[two];
-            float4 sum = make_float4(x[k].x * f.x, x[k].y * f.y, x[k].z * f.x, x[k].w * f.y);
 #pragma unroll 1
-            for (int p = 0; p < n; p += 8) {   // eight loads in flight; behind the last piece its weight is 0
-                float4 y[8];
+        for (int p = 0; p < n; p += 8) {
+            if (p) read(p);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = record(i0 + min(p + q, n - 1))[i];
+            for (int k = 0; k < PER; ++k) {
+                const int two = min(tid + k * kCombineWarps * 32, SLOTS - 1) / (D / 16 * 32) * 4 + (tid & 3);
+                if (p == 0) {
+                    const float4 f = scale_ml[two];
+                    x[k] = make_float4(x[k].x * f.x, x[k].y * f.y, x[k].z * f.x, x[k].w * f.y);
+                }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 8; ++q) {   // behind the last piece its weight is 0
                     const float2 w = p + q < n ? weight_of[p + q][two] : make_float2(0.0f, 0.0f);
-                    sum = make_float4(sum.x + y[q].x * w.x, sum.y + y[q].y * w.y, sum.z + y[q].z * w.x, sum.w + y[q].w * w.y);
+                    x[k] = make_float4(x[k].x + y[k][q].x * w.x, x[k].y + y[k][q].y * w.y, x[k].z + y[k][q].z * w.x, x[k].w + y[k][q].w * w.y);
                 }
             }
-            x[k] = sum;
         }
         __syncthreads();
     }
