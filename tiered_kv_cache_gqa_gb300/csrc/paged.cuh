@@ -97,6 +97,31 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicMax(status, code);
 }
 
+// cs[i] = (cos, sin) of pair j0 + i at a row's positions p, one an axis; table, rows of it and j0 lie on 16 bytes.
+template <int N, typename Args>
+__device__ __forceinline__ void load_angles(const Args& a, const int (&p)[4], int j0, float2 (&cs)[N]) {
+    bool bad = false;
+    if (a.num_axes == 1) {
+        const bool in = (uint32_t)p[0] < (uint32_t)a.max_positions;
+        const float4* at = reinterpret_cast<const float4*>(a.table + (int64_t)(in ? p[0] : 0) * a.pairs + j0);
+        const float nan = __int_as_float(0x7FC00000);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float4 v = __ldg(at + i);
+            cs[2 * i] = in ? make_float2(v.x, v.y * a.sign) : make_float2(nan, nan);
+            cs[2 * i + 1] = in ? make_float2(v.z, v.w * a.sign) : make_float2(nan, nan);
+        }
+        bad = !in;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int x = a.pair_axis[j0 + i];
+            cs[i] = table_at(a.table, a.pairs, a.max_positions, x == 0 ? p[0] : x == 1 ? p[1] : x == 2 ? p[2] : p[3], j0 + i, a.sign, &bad);
+        }
+    }
+    if (bad) raise_status(a.status, TKV_EINVAL);
+}
+
 // The sequence that row `row` of a step belongs to: cu[b] <= row < cu[b + 1]; -1 behind the last.
 __device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int row) {
     if (row < __ldg(cu) || row >= __ldg(cu + batch)) return -1;

@@ -120,31 +120,6 @@ __device__ __forceinline__ uint4 pack(const float* x) {
 //   kAny       channel by channel, partners read one at a time
 enum Turn { kNone, kHalves, kAdjacent, kAny };
 
-// cs[i] = (cos, sin) of pair j0 + i at the row's positions; j0 a multiple of N, the table's rows of 16 bytes.
-template <int N>
-__device__ __forceinline__ void load_angles(const RowArgs& a, const int (&p)[4], int j0, float2 (&cs)[N]) {
-    bool bad = false;
-    if (a.num_axes == 1) {
-        const bool in = (uint32_t)p[0] < (uint32_t)a.max_positions;
-        const float4* at = reinterpret_cast<const float4*>(a.table + (int64_t)(in ? p[0] : 0) * a.pairs + j0);
-        const float nan = __int_as_float(0x7FC00000);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float4 v = __ldg(at + i);
-            cs[2 * i] = in ? make_float2(v.x, v.y * a.sign) : make_float2(nan, nan);
-            cs[2 * i + 1] = in ? make_float2(v.z, v.w * a.sign) : make_float2(nan, nan);
-        }
-        bad = !in;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int x = a.pair_axis[j0 + i];
-            cs[i] = table_at(a.table, a.pairs, a.max_positions, x == 0 ? p[0] : x == 1 ? p[1] : x == 2 ? p[2] : p[3], j0 + i, a.sign, &bad);
-        }
-    }
-    if (bad) raise_status(a.status, TKV_EINVAL);
-}
-
 // Channels 8 chunk .. + 7 of head row k, turned one at a time (kAny).
 template <typename T>
 __device__ __forceinline__ void turn_any(const RowArgs& a, const T* k, int64_t row, int own_position, int chunk, float (&x)[8]) {
