@@ -133,6 +133,28 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int
     return lo;
 }
 
+// The operators' kernels start while the kernel before them in the stream ends (programmatic launches): each reads and writes
+// memory only behind wait_for_previous, which lasts until the kernel before it is done and its writes can be seen.  A
+// kernel that calls let_next_start first lets its successor start although its predecessor still runs: the successor
+// then may not read anything before its own wait.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename Args, typename... Rest>
+cudaError_t launch_behind(void (*kernel)(Args, Rest...), dim3 grid, int threads, int smem, cudaStream_t st, const Args& args, Rest... rest) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args, rest...);
+}
+
 // Host-side checks shared by the entry points; TKV_OK or TKV_EINVAL.
 tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions);
 tkv_status check_paged(const tkv_paged* c);

@@ -424,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     constexpr int R = C::R, S = C::stages, TP = T::positions, TB = T::bytes;
     extern __shared__ __align__(128) uint8_t smem[];
     Shared<D, NT, KIND>& sh = *reinterpret_cast<Shared<D, NT, KIND>*>(smem);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kWarps && lane < kWarps) {
         for (int s = 0; s < S; ++s) {
@@ -434,6 +433,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
         for (int s = 0; s < C::queue; ++s) mbar_init(smem_u32(&sh.known[lane][s]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+
+    wait_for_previous();
+    let_next_start();   // the joining kernel, which reads lengths and cu_tokens before its own wait: not earlier than here
 
     // -------------------------------------------------------- this CTA's tiles of the deal, and each warp's
     int before, own;
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
         }
     }
     // what the main kernel wrote is read after this; every CTA waits, so that the grid ends after it
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     if (pieces == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? __ldg(a.c.v_gain + rows.h) : 1.0f) : 1.0f;
@@ -754,19 +756,9 @@ cudaError_t launch(PagedAttnArgs& a, cudaStream_t st) {
         if (e == cudaSuccess && dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    paged_attention_kernel<D, NT, KIND><<<a.grid, kThreads, smem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.whole_items) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(kCombineWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    if ((e = launch_behind(paged_attention_kernel<D, NT, KIND>, dim3(a.grid), kThreads, smem, st, a)) != cudaSuccess || a.whole_items) return e;
     const bool fp16 = KIND == kFp16 || (KIND == kInt4 && a.q_fp16);
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, NT, KIND>, (const PagedAttnArgs)a, fp16);
+    return launch_behind(paged_combine_kernel<D, NT, KIND>, dim3(a.grid), kCombineWarps * 32, 0, st, a, fp16);
 }
 
 template <int D, int NT>

@@ -186,6 +186,8 @@ struct Target {
 // is instructions, about 80 for 8 values; three CTAs an SM were faster than two (36 us) and than four (36 us, spills).
 template <typename T, int D, bool INT4, int TURN>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ RowArgs a) {
+    let_next_start();
+    wait_for_previous();
     const int rows_here = kThreads / a.units;
     const int unit = threadIdx.x % a.units;
     const int64_t row = (int64_t)blockIdx.x * rows_here + threadIdx.x / a.units;
@@ -294,6 +296,8 @@ __device__ __forceinline__ void expand(uint32_t word, uint8_t scale_byte, float 
 // TO: element type of the outputs; T: of 16-bit pages.  blockIdx.y: the first head.
 template <typename TO, typename T, int D, bool INT4>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ RowArgs a) {
+    let_next_start();
+    wait_for_previous();
     constexpr int N = 16 / sizeof(TO), NC = D / N;   // values of a thread, threads of a row
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int chunk = (int)(i % NC);
@@ -361,33 +365,32 @@ cudaError_t spread_heads(RowArgs& a, int64_t threads_a_head) {
 }
 
 template <typename T, int D, bool INT4>
-void append_turn(const RowArgs& a, int turn, dim3 grid, cudaStream_t st) {
-    if (turn == kNone) append_kernel<T, D, INT4, kNone><<<grid, kThreads, 0, st>>>(a);
-    else if (turn == kHalves) append_kernel<T, D, INT4, kHalves><<<grid, kThreads, 0, st>>>(a);
-    else if (turn == kAdjacent) append_kernel<T, D, INT4, kAdjacent><<<grid, kThreads, 0, st>>>(a);
-    else append_kernel<T, D, INT4, kAny><<<grid, kThreads, 0, st>>>(a);
+cudaError_t append_turn(const RowArgs& a, int turn, dim3 grid, cudaStream_t st) {
+    return launch_behind(turn == kNone       ? append_kernel<T, D, INT4, kNone>
+                         : turn == kHalves   ? append_kernel<T, D, INT4, kHalves>
+                         : turn == kAdjacent ? append_kernel<T, D, INT4, kAdjacent>
+                                             : append_kernel<T, D, INT4, kAny>,
+                         grid, kThreads, 0, st, a);
 }
 
 template <typename T>
-void append_type(const RowArgs& a, int turn, dim3 grid, cudaStream_t st) {
+cudaError_t append_type(const RowArgs& a, int turn, dim3 grid, cudaStream_t st) {
     const bool int4 = a.c.kv_type == TKV_INT4;
-    if (a.c.head_dim == 128)
-        int4 ? append_turn<T, 128, true>(a, turn, grid, st) : append_turn<T, 128, false>(a, turn, grid, st);
-    else
-        int4 ? append_turn<T, 64, true>(a, turn, grid, st) : append_turn<T, 64, false>(a, turn, grid, st);
+    if (a.c.head_dim == 128) return int4 ? append_turn<T, 128, true>(a, turn, grid, st) : append_turn<T, 128, false>(a, turn, grid, st);
+    return int4 ? append_turn<T, 64, true>(a, turn, grid, st) : append_turn<T, 64, false>(a, turn, grid, st);
 }
 
 template <typename TO, int D>
-void gather_pages(const RowArgs& a, dim3 grid, cudaStream_t st) {
-    if (a.c.kv_type == TKV_INT4) gather_kernel<TO, __half, D, true><<<grid, kThreads, 0, st>>>(a);
-    else if (a.c.kv_type == TKV_FP16) gather_kernel<TO, __half, D, false><<<grid, kThreads, 0, st>>>(a);
-    else gather_kernel<TO, __nv_bfloat16, D, false><<<grid, kThreads, 0, st>>>(a);
+cudaError_t gather_pages(const RowArgs& a, dim3 grid, cudaStream_t st) {
+    return launch_behind(a.c.kv_type == TKV_INT4   ? gather_kernel<TO, __half, D, true>
+                         : a.c.kv_type == TKV_FP16 ? gather_kernel<TO, __half, D, false>
+                                                   : gather_kernel<TO, __nv_bfloat16, D, false>,
+                         grid, kThreads, 0, st, a);
 }
 
 template <typename TO>
-void gather_type(const RowArgs& a, dim3 grid, cudaStream_t st) {
-    if (a.c.head_dim == 128) gather_pages<TO, 128>(a, grid, st);
-    else gather_pages<TO, 64>(a, grid, st);
+cudaError_t gather_type(const RowArgs& a, dim3 grid, cudaStream_t st) {
+    return a.c.head_dim == 128 ? gather_pages<TO, 128>(a, grid, st) : gather_pages<TO, 64>(a, grid, st);
 }
 
 // The checks that append and gather share.
@@ -459,9 +462,8 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
     cudaError_t e = spread_heads(a, rows * a.units);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((rows + rows_a_block - 1) / rows_a_block), a.lanes);
-        if (dtype == TKV_BF16) append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream);
-        else append_type<__half>(a, turn, grid, (cudaStream_t)stream);
-        e = cudaGetLastError();
+        e = dtype == TKV_BF16 ? append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream)
+                              : append_type<__half>(a, turn, grid, (cudaStream_t)stream);
     }
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
@@ -488,10 +490,9 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), a.lanes);
         cudaStream_t st = (cudaStream_t)stream;
-        if (dtype == TKV_BF16) gather_type<__nv_bfloat16>(a, grid, st);
-        else if (dtype == TKV_FP16) gather_type<__half>(a, grid, st);
-        else gather_type<float>(a, grid, st);
-        e = cudaGetLastError();
+        e = dtype == TKV_BF16   ? gather_type<__nv_bfloat16>(a, grid, st)
+            : dtype == TKV_FP16 ? gather_type<__half>(a, grid, st)
+                                : gather_type<float>(a, grid, st);
     }
     if (e != cudaSuccess) {
         (void)cudaGetLastError();

@@ -38,6 +38,8 @@ struct RopeArgs {
 // 16,384 rows of 64 heads of 128 in bf16, three axes: 94 us (545 MB, 5.8 TB/s).
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    let_next_start();
+    wait_for_previous();
     constexpr int E = 16 / sizeof(T);
     constexpr int NP = INTERLEAVED ? E / 2 : E;   // pairs of a piece
     const int rotated = a.pairs / NP;
@@ -92,6 +94,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // Any alignment and any number of pairs: a thread takes one pair (or one copied channel) of a head.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs a) {
+    let_next_start();
+    wait_for_previous();
     const int rest = a.copy_rest ? a.head_dim - 2 * a.pairs : 0;
     const uint32_t per_head = a.pairs + rest;
     const int64_t total = a.rows * a.heads * per_head;
@@ -134,8 +138,7 @@ cudaError_t launch(RopeArgs& a, bool whole, cudaStream_t st) {
     if (!whole) {
         const int64_t total = a.rows * a.heads * (a.pairs + (a.copy_rest ? a.head_dim - 2 * a.pairs : 0));
         const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)sms * 64);
-        rope_pairs_kernel<T><<<grid, kThreads, 0, st>>>(a);
-        return cudaGetLastError();
+        return launch_behind(rope_pairs_kernel<T>, dim3(grid), kThreads, 0, st, a);
     }
     const int pieces = pieces_of<T>(a);
     // A thread takes up to 8 heads of its row, which reads the table once for them, as long as two
@@ -144,11 +147,8 @@ cudaError_t launch(RopeArgs& a, bool whole, cudaStream_t st) {
     a.lanes = std::min(65535, (a.heads + per_thread - 1) / per_thread);
     const int rows_here = kThreads / pieces;
     const dim3 grid((unsigned)((a.rows + rows_here - 1) / rows_here), a.lanes);
-    if (a.interleaved)
-        rope_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
-    else
-        rope_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.interleaved ? launch_behind(rope_kernel<T, true>, grid, kThreads, 0, st, a)
+                         : launch_behind(rope_kernel<T, false>, grid, kThreads, 0, st, a);
 }
 
 }  // namespace
