@@ -387,7 +387,7 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  *     `stream` (NULL = the legacy default stream) of the current device, on
  *     which all pointers must lie.
  *   - A step's rows are ragged.  cu_tokens: device int32 [batch + 1],
- *     ascending; sequence b owns rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of
+ *     not descending; sequence b owns rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of
  *     k, v, q and out, and they are its last positions: row cu_tokens[b] + i
  *     is position lengths[b] - n_b + i, n_b = cu_tokens[b + 1] - cu_tokens[b].
  *     `rows` is the extent of the tensors; rows behind cu_tokens[batch] are
@@ -399,7 +399,8 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  *     checked by the host.  No kernel reads or writes outside the buffers for
  *     any value in them.  What is wrong is left out as each call says and
  *     reported in `status`: a device int32 that the caller clears (or NULL),
- *     raised to TKV_EINVAL (a position outside the rotary table), TKV_ECAPACITY
+ *     raised to TKV_EINVAL (a position outside the rotary table; in the attention
+ *     a sequence whose cu_tokens descend or leave the rows), TKV_ECAPACITY
  *     (a page or a position outside the cache) or TKV_ETIMEOUT, the largest. */
 
 /* Element types.  TKV_INT4 is a type of pages only. */
@@ -435,7 +436,8 @@ typedef struct {
  *       channels; the value is q * scale * gain of the KV head.  The append
  *       writes scale = amax / (7 gain), to nearest even, saturating at 448, and
  *       q = x / (scale gain), to nearest even; a block with an infinity or a
- *       NaN reads as NaN.  Choose gain so that amax / (7 gain) falls in E4M3's
+ *       NaN reads as NaN.  A quotient within 2^-22 of a tie may go to either side
+ *       where gain is not a power of two.  Choose gain so that amax / (7 gain) falls in E4M3's
  *       normal range, 2^-6 .. 448: amax / 1024 of what the head is expected to
  *       hold leaves room on both sides. */
 typedef struct {
@@ -455,7 +457,7 @@ typedef struct {
 
 /* Rotates x into out, which may be x itself (same strides).
  * x, out: device [rows][heads][head_dim] of dtype (TKV_BF16, TKV_FP16 or
- * TKV_FP32), any strides that keep out's elements apart; channels behind the
+ * TKV_FP32), rows up to 2^31 - 1, any strides that keep out's elements apart; channels behind the
  * rotated ones are copied.  Computed in fp32, rounded once.  Fast where
  * everything starts on 16-byte boundaries.  A position outside the table turns
  * its pairs into NaN and raises status to TKV_EINVAL.
@@ -496,7 +498,8 @@ tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dt
  *   exp(scale q.k) (natural; NULL = not wanted; joins partial results over
  *   several caches); a query that sees nothing gets out = 0, lse = -infinity.
  * q, out: device [rows][num_q_heads][d] of dtype TKV_BF16 or TKV_FP16 (the pages'
- * own type if they are 16-bit), 16-byte aligned, strides multiples of 8; lse:
+ * own type if they are 16-bit), 16-byte aligned, strides multiples of 8, not
+ * overlapping; lse:
  * device fp32 [rows][num_q_heads], contiguous.
  * A step's size is limited: (rows * num_q_heads / Hkv / 8 + batch) * Hkv *
  * (max_pages * page_size / 32) tiles (half as many positions a tile with 16-bit
@@ -510,7 +513,8 @@ tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dt
  * sequence's last bits may depend on the lengths of the others (they move
  * the places where its sums are split).  Positions in a page outside
  * [0, num_pages), and a sequence's positions beyond the page table, are left
- * out and raise status to TKV_ECAPACITY.
+ * out and raise status to TKV_ECAPACITY.  A sequence whose cu_tokens descend or
+ * leave the rows is left out and raises it to TKV_EINVAL.
  * Errors: TKV_EINVAL, TKV_ECAPACITY (workspace too small), TKV_ECUDA. */
 tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q, void* out, float* lse, int32_t dtype,
                                int64_t rows, int32_t num_q_heads, int64_t q_row_stride, int64_t q_head_stride,

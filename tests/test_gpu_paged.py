@@ -571,3 +571,74 @@ def test_binding_refuses():
     assert tkv.tkv_paged_attention(p.cache._c, q, q.clone(), None, tkv.TKV_BF16, 1, 4, (256, 64), (256, 64), p.cu_t, 1, 20, 0, 0.1,
                                    small, 16) == tkv.TKV_ECAPACITY
     assert p.cache.attend(q[:0], p.cu_t).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+@pytest.mark.parametrize("window,n", [(700, 1), (513, 3), (1500, 2)])
+def test_windows_over_items_that_are_cut(kind, dtype, window, n):
+    p = Pool(kind, [2900, 31, 760, 1024], [n, n, n, n], d=128, page=32).fill()
+    q = queries(p, 4, dtype=dtype)
+    want = p.oracle(q, window=window)
+    for ln in (2900, 20):
+        close(p, *p.cache.attend(q, p.cu_t, max_new=n, max_len=ln, window=window, return_lse=True), want, dtype)
+
+
+def test_offsets_that_descend_are_reported():
+    """Rows that several sequences count: 40 of 65,536 rows each are more tiles than 32 bits count."""
+    batch, rows, page, pages_a_seq = 80, 65536, 256, 64
+    table, lens = torch.zeros(batch, pages_a_seq, dtype=torch.int32, device="cuda"), ints([page * pages_a_seq] * batch)
+    cache = tkv.PagedCache.empty(1, table, lens, num_kv_heads=8, head_dim=64, page_size=page)
+    q = torch.zeros(rows, 64, 64, dtype=BF16, device="cuda")
+    out = torch.full_like(q, 3.0)
+    status = ints([0])
+    cache.attend(q, ints([0, rows] * (batch // 2) + [0]), max_new=rows, out=out, status=status)
+    assert status.item() == tkv.TKV_EINVAL and bool((out == 3.0).all())
+    # one sequence that leaves the rows: it is left out, the others are not
+    p = Pool("int4", [100, 60, 40], [1, 1, 1], page=16).fill()
+    q = queries(p, 4)
+    out = torch.full_like(q, 3.0)
+    status.zero_()
+    p.cache.attend(q, ints([0, 1, 2, 9]), out=out, status=status)
+    assert status.item() == tkv.TKV_EINVAL and bool((out[2] == 3.0).all())
+    close(p, out[:2], None, tuple(x[:2] for x in p.oracle(q)), BF16)
+
+
+@pytest.mark.parametrize("max_len", [64, 2000])
+def test_kernels_behind_other_work(max_len):
+    """Behind a fill, a copy and an event of another stream, eagerly and captured, each call sees what they wrote."""
+    p = Pool("int4", [64, 37, 50], [1, 1, 1], page=16, max_pages=128).fill()
+    rot = tkv.Rotary(tkv.rope_table(2048, p.d))
+    k, v = (torch.randn(3, p.hkv, p.d, device="cuda").to(BF16) for _ in range(2))
+    q0, lens0 = queries(p, 4), p.lens.clone()
+    q, out = torch.empty_like(q0), torch.empty_like(q0)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        p.lens.zero_()
+        out.fill_(7.0)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            p.lens.copy_(lens0)
+            turned = tkv.rope(q0, rot, lens0)
+        p.cache.gather(p.cu_t, 3, lengths=lens0)
+        here.wait_stream(side)
+        p.cache.append(k, v, p.cu_t, rotary=rot)
+        q.copy_(turned)
+        p.cache.attend(q, p.cu_t, max_len=max_len, out=out)
+        q.zero_()
+        p.lens.zero_()
+
+    with torch.cuda.stream(main):
+        step()
+    torch.cuda.synchronize()
+    p.lens.copy_(lens0)
+    want = p.cache.attend(tkv.rope(q0, rot, lens0), p.cu_t, max_len=max_len)
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)

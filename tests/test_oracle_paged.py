@@ -173,3 +173,17 @@ def test_binding_refuses_host_tensors():
 def test_descriptors_match_the_header(cname, pyname):
     from test_abi import header_struct_fields
     assert [f[0] for f in getattr(tkv, pyname)._fields_] == header_struct_fields(cname)
+
+
+def test_unaligned_and_overlapping_arguments_are_refused():
+    """Words that a kernel reads as int32 or fp32 lie on 4 bytes; a score's scale stays finite in powers of two; out is not q."""
+    for c in (cache(page_table=0x20002), cache(lengths=0x30001), cache(k_gain=0x40002), cache(v_gain=0x40003)):
+        assert call_append(c) == tkv.TKV_EINVAL
+    assert call_append(cu=0x300002) == tkv.TKV_EINVAL and call_append(rot=rotary(positions=0x20001)) == tkv.TKV_EINVAL
+    assert call_rope(rot=rotary(positions=0x20002)) == tkv.TKV_EINVAL and call_rope(rows=1 << 31) == tkv.TKV_EINVAL
+
+    def attention(out=0x200000, lse=None, cu=0x300000, scale=0.125, status=None):
+        return tkv.tkv_paged_attention(cache(), 0x100000, out, lse, tkv.TKV_BF16, 4, 4, (256, 64), (256, 64), cu, 1, 64, 0, scale,
+                                       0x400000, 1 << 40, status=status, stream=1)
+    for kw in (dict(out=0x100000), dict(lse=0x500002), dict(cu=0x300001), dict(scale=3e38), dict(status=0x600002)):
+        assert attention(**kw) == tkv.TKV_EINVAL

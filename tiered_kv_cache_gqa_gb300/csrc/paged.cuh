@@ -161,6 +161,7 @@ tkv_status check_paged(const tkv_paged* c);
 // element (row, head, channel) -> memory: rows and heads do not overlap, strides >= 0
 bool strides_apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t width);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int dtype_size(int t) { return t == TKV_FP32 ? 4 : 2; }
 inline bool is_dtype(int t) { return t == TKV_BF16 || t == TKV_FP16 || t == TKV_FP32; }
 

@@ -25,8 +25,14 @@ namespace {
 constexpr int kWarps = 7, kThreads = (kWarps + 1) * 32;   // warps that compute, and one that copies
 constexpr int kCombineWarps = 8;
 constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, joining costs more than it brings
-constexpr int kWholeItems = 512;        // up to this length a CTA takes whole items, and nothing is left to join
+// Up to these numbers of positions in sight a CTA takes whole items, and nothing is left to join: always; where the items
+// may be as many as the SMs.  One launch instead of two, but uneven shares.  Cut against whole, 8 KV heads of
+// d 128 in 4 bits: batch 1, 256 positions 8.3 and 7.3 us, 512 positions 8.3 and 9.0, 1,024 positions 8.5 and 11.0; batch
+// 64, 512 positions 19.1 and 16.0, 1,024 positions 27.0 and 25.5, 4,096 positions 65.0 and 68.9; d 64, batch 67 with a
+// window of 700 positions, 16.2 and 20.3.
+constexpr int kWholeShort = 256, kWholeMany = 512;
 constexpr int kSpinLimit = 1 << 18;     // tries of a wait
+constexpr double kLog2E = 1.4426950408889634;
 
 struct PagedAttnArgs {
     tkv_paged c;
@@ -85,7 +91,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 // ------------------------------------------------------------------ the deal
-// What sequence b brings: its queries n, the positions that exist (len) and that its last query counts from (full), where
+// What sequence b brings: its queries n (-1: cu_tokens makes no sense there), the positions that exist (len) and that its last query counts from (full), where
 // its tiles begin, how many an item has, and the tiles of rows.
 struct Seq {
     int first_row, n, len, full, lo, units, tiles;
@@ -97,44 +103,55 @@ __device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
     const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
     s.full = max(0, __ldg(a.c.lengths + b));
     s.first_row = c0;
-    s.n = (c0 < 0 || c1 <= c0 || c1 > a.rows) ? 0 : c1 - c0;
+    s.n = (c0 < 0 || c1 < c0 || c1 > a.rows) ? -1 : c1 - c0;
     s.len = min(s.full, a.c.max_pages << a.page_shift);
     s.lo = 0;
     if (a.window > 0) s.lo = max(0, min(s.len, s.full - s.n - a.window + 1)) & ~31;
     s.units = max(1, (s.len - s.lo + TP - 1) / TP);   // a row that sees nothing is written too
-    s.tiles = s.n ? (int)(((int64_t)s.n * a.group + R - 1) / R) : 0;
+    s.tiles = s.n > 0 ? (int)(((int64_t)s.n * a.group + R - 1) / R) : 0;
     return s;
 }
 
 // Tiles of a sequence.  The host has made sure that the batch's tiles are fewer than 2^31.
 __device__ __forceinline__ int weight(const PagedAttnArgs& a, const Seq& s) { return s.tiles * a.c.num_kv_heads * s.units; }
 
-// All tiles of the batch; *before, *own: those of the sequences before this thread's and of its own (blocks of
-// ceil(batch / threads) sequences a thread).  `sums`: an int of shared memory a warp.
+// Tiles are counted in 32 bits: the host refuses a step of more than kMostTiles, and if cu_tokens counts rows more than
+// once all the same, sums stay at kTooMany.  A share more than that is still below 2^31.
+constexpr int kMostTiles = 2000000000, kTooMany = 2050000000;
+__device__ __forceinline__ int add_up_to(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kTooMany); }
+
+// All tiles of the batch (kTooMany: or more); *before, *own: those of the sequences before this thread's and of its own (blocks of
+// ceil(batch / threads) sequences a thread).  `sums`: an int of shared memory a warp;
+// `status`: raised where cu_tokens descends or leaves the rows, or null.
 template <int R, int TP, int WARPS>
-__device__ __forceinline__ int scan_batch(const PagedAttnArgs& a, int* sums, int* before, int* own) {
+__device__ __forceinline__ int scan_batch(const PagedAttnArgs& a, int* sums, int* before, int* own, int32_t* status) {
     constexpr int threads = WARPS * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.c.batch + threads - 1) / threads;
     int mine = 0;
 #pragma unroll 1
-    for (int b = tid * per; b < min(a.c.batch, (tid + 1) * per); ++b) mine += weight(a, sequence<R, TP>(a, b));
+    for (int b = tid * per; b < min(a.c.batch, (tid + 1) * per); ++b) {
+        const Seq s = sequence<R, TP>(a, b);
+        mine = add_up_to(mine, weight(a, s));
+        if (s.n < 0) raise_status(status, TKV_EINVAL);
+    }
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
+        if (lane >= o) sum = add_up_to(sum, x);
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int base = 0, total = 0;
+    uint32_t base = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         const int x = sums[w];
-        base += w < warp ? x : 0;
-        total += x;
+        base += w < warp ? (uint32_t)x : 0u;
+        total = add_up_to(total, x);
     }
-    *before = base + sum - mine;
+    *before = (int)(base + (uint32_t)(sum - mine));
     *own = mine;
     return total;
 }
@@ -439,7 +456,11 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 
     // -------------------------------------------------------- this CTA's tiles of the deal, and each warp's
     int before, own;
-    const int total = scan_batch<R, TP, kWarps + 1>(a, sh.sums, &before, &own);
+    const int total = scan_batch<R, TP, kWarps + 1>(a, sh.sums, &before, &own, blockIdx.x == 0 ? a.status : nullptr);
+    if (total == kTooMany) {
+        if (tid == 0) raise_status(a.status, TKV_EINVAL);
+        return;
+    }
     const int share = share_of(a, total);
     int u0 = (int)min((int64_t)total, (int64_t)blockIdx.x * share), u1 = min(total, u0 + share);
     if (a.whole_items) {
@@ -637,9 +658,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     __shared__ int sums[kCombineWarps];
     __shared__ Where at;
     int before, own;
-    const int total = scan_batch<R, TP, kCombineWarps>(a, sums, &before, &own);
+    const int total = scan_batch<R, TP, kCombineWarps>(a, sums, &before, &own, nullptr);
     const int share = share_of(a, total);
-    const int cut = (int)min((int64_t)total, (int64_t)(blockIdx.x + 1) * share);
+    const int cut = total == kTooMany ? total : (int)min((int64_t)total, (int64_t)(blockIdx.x + 1) * share);
     locate<R, TP, kCombineWarps, 1>(a, cut, 0, before, own, &at);
     __syncthreads();
     int pieces = 0;
@@ -789,13 +810,14 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
                                           int64_t out_row_stride, int64_t out_head_stride, const int32_t* cu_tokens,
                                           int32_t max_new, int32_t max_len, int32_t window, float scale, void* workspace,
                                           int64_t workspace_bytes, int32_t* status, void* stream) {
-    if (!attention_shape_ok(cache, num_q_heads, max_new) || max_len < 1 || window < 0 || !std::isfinite(scale)) return TKV_EINVAL;
+    if (!attention_shape_ok(cache, num_q_heads, max_new) || max_len < 1 || window < 0 || !std::isfinite((float)((double)scale * kLog2E))) return TKV_EINVAL;
     if (dtype != TKV_BF16 && dtype != TKV_FP16) return TKV_EINVAL;
     if (cache->kv_type != TKV_INT4 && cache->kv_type != dtype) return TKV_EINVAL;
     if (rows < 0 || rows > 0x7FFFFFFF || !cu_tokens) return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     // row indices within a sequence (queries x heads of a group) are 32-bit
-    if (!q || !out || rows * (num_q_heads / cache->num_kv_heads) > 0x7FFF0000) return TKV_EINVAL;
+    if (!q || !out || q == out || rows * (num_q_heads / cache->num_kv_heads) > 0x7FFF0000) return TKV_EINVAL;
+    if (!aligned4(lse) || !aligned4(cu_tokens) || !aligned4(status)) return TKV_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || q_row_stride < 0 || q_head_stride < 0 || q_row_stride % 8 ||
         q_head_stride % 8 || out_row_stride % 8 || out_head_stride % 8)
         return TKV_EINVAL;
@@ -821,16 +843,18 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.group_mul = 0xFFFFFFFFu / (uint32_t)a.group;
     a.window = window;
     a.page_shift = __builtin_ctz((unsigned)cache->page_size);
-    a.whole_items = max_len <= kWholeItems;
+    const int64_t sight = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + max_new) : max_len;
     a.q_fp16 = dtype == TKV_FP16;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.scale_log2 = (float)((double)scale * kLog2E);
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = row_tiles(a.group, max_new);
-    // tiles are counted in 32 bits
-    const double tile_bound = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads *
-                              ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
-    if (tile_bound > 2.0e9) return TKV_EINVAL;
-    const cudaError_t e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, st) : launch_kind<128, 2>(a, st))
+    int ctas = 0, dev = 0;
+    cudaError_t e = device_ctas(1, &ctas, &dev);
+    const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
+    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= ctas);
+    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
+    if (tile_bound > kMostTiles) return TKV_EINVAL;
+    if (e == cudaSuccess) e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, st) : launch_kind<128, 2>(a, st))
                                                  : (nt == 1 ? launch_kind<64, 1>(a, st) : launch_kind<64, 2>(a, st));
     if (e != cudaSuccess) {
         (void)cudaGetLastError();

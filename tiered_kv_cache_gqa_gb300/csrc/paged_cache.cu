@@ -395,8 +395,8 @@ cudaError_t gather_type(const RowArgs& a, dim3 grid, cudaStream_t st) {
 
 // The checks that append and gather share.
 tkv_status row_args(const tkv_paged* c, const void* k, const void* v, int64_t rows, int64_t k_row, int64_t k_head,
-                    int64_t v_row, int64_t v_head, int element, const int32_t* cu, RowArgs* a) {
-    if (check_paged(c) != TKV_OK || rows < 0 || rows > 0x7FFFFFFF || !cu) return TKV_EINVAL;
+                    int64_t v_row, int64_t v_head, int element, const int32_t* cu, int32_t* status, RowArgs* a) {
+    if (check_paged(c) != TKV_OK || rows < 0 || rows > 0x7FFFFFFF || !cu || !aligned4(cu) || !aligned4(status)) return TKV_EINVAL;
     if (rows > 0 && (!k || !v)) return TKV_EINVAL;
     const int64_t E = 16 / element;   // blocks are moved in 16-byte pieces
     if (!aligned16(k) || !aligned16(v) || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0 || k_row % E || k_head % E ||
@@ -406,6 +406,7 @@ tkv_status row_args(const tkv_paged* c, const void* k, const void* v, int64_t ro
     a->k = k;
     a->v = v;
     a->cu = cu;
+    a->status = status;
     a->rows = rows;
     a->k_row = k_row;
     a->k_head = k_head;
@@ -426,7 +427,7 @@ tkv_status check_paged(const tkv_paged* c) {
     if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return TKV_EINVAL;
     if (c->batch < 1 || c->max_pages < 1 || c->num_kv_heads < 1 || c->num_pages < 1) return TKV_EINVAL;
     if ((int64_t)c->max_pages * c->page_size > (int64_t)1 << 30) return TKV_EINVAL;   // positions are int32
-    if (!aligned16(c->pages)) return TKV_EINVAL;
+    if (!aligned16(c->pages) || !aligned4(c->page_table) || !aligned4(c->lengths) || !aligned4(c->k_gain) || !aligned4(c->v_gain)) return TKV_EINVAL;
     return TKV_OK;
 }
 
@@ -438,7 +439,7 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
                                        int32_t* status, void* stream) {
     RowArgs a{};
     if (dtype != TKV_BF16 && dtype != TKV_FP16) return TKV_EINVAL;
-    if (row_args(cache, k, v, rows, k_row_stride, k_head_stride, v_row_stride, v_head_stride, 2, cu_tokens, &a) != TKV_OK)
+    if (row_args(cache, k, v, rows, k_row_stride, k_head_stride, v_row_stride, v_head_stride, 2, cu_tokens, status, &a) != TKV_OK)
         return TKV_EINVAL;
     if (cache->kv_type != TKV_INT4 && cache->kv_type != dtype) return TKV_EINVAL;
     int turn = kNone;
@@ -456,7 +457,6 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
         turn = !aligned16(rotary->table) ? kAny : a.interleaved ? (a.pairs % 4 == 0 ? kAdjacent : kAny) : (a.pairs % 16 == 0 ? kHalves : kAny);
     }
     if (rows == 0) return TKV_OK;
-    a.status = status;
     a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);
     const int rows_a_block = kThreads / a.units;
     cudaError_t e = spread_heads(a, rows * a.units);
@@ -478,13 +478,12 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
     RowArgs a{};
     if (!is_dtype(dtype)) return TKV_EINVAL;
     if (row_args(cache, k, v, rows, k_row_stride, k_head_stride, v_row_stride, v_head_stride, dtype_size(dtype), cu_tokens,
-                 &a) != TKV_OK)
+                 status, &a) != TKV_OK)
         return TKV_EINVAL;
     if (!strides_apart(rows, k_row_stride, cache->num_kv_heads, k_head_stride, cache->head_dim) ||
         !strides_apart(rows, v_row_stride, cache->num_kv_heads, v_head_stride, cache->head_dim) || (rows > 0 && k == v))
         return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
-    a.status = status;
     const int64_t threads = rows * (cache->head_dim * dtype_size(dtype) / 16);
     cudaError_t e = spread_heads(a, threads);
     if (e == cudaSuccess) {

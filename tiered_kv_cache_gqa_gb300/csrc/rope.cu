@@ -164,7 +164,7 @@ bool strides_apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head
 }
 
 tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions) {
-    if (!r || !r->table || (reinterpret_cast<uintptr_t>(r->table) & 7u)) return TKV_EINVAL;
+    if (!r || !r->table || (reinterpret_cast<uintptr_t>(r->table) & 7u) || !aligned4(r->positions)) return TKV_EINVAL;
     if (need_positions && !r->positions) return TKV_EINVAL;
     if (r->max_positions < 1 || r->pairs < 1 || r->pairs > 256 || 2 * r->pairs > head_dim) return TKV_EINVAL;
     if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->positions)) return TKV_EINVAL;
@@ -179,11 +179,11 @@ tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions) 
 extern "C" tkv_status tkv_rope(const tkv_rotary* rotary, const void* x, void* out, int32_t dtype, int64_t rows,
                                int32_t heads, int32_t head_dim, int64_t x_row_stride, int64_t x_head_stride,
                                int64_t out_row_stride, int64_t out_head_stride, int32_t* status, void* stream) {
-    if (!is_dtype(dtype) || rows < 0 || rows > (int64_t)1 << 31 || heads < 1 || head_dim < 2 || head_dim > 65536)
+    if (!is_dtype(dtype) || rows < 0 || rows > 0x7FFFFFFF || heads < 1 || head_dim < 2 || head_dim > 65536)
         return TKV_EINVAL;
     if (check_rotary(rotary, head_dim, true) != TKV_OK) return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
-    if (!x || !out || x_row_stride < 0 || x_head_stride < 0) return TKV_EINVAL;
+    if (!x || !out || x_row_stride < 0 || x_head_stride < 0 || !aligned4(status)) return TKV_EINVAL;
     const uintptr_t size = dtype_size(dtype);
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & (size - 1)) return TKV_EINVAL;
     if (!strides_apart(rows, out_row_stride, heads, out_head_stride, head_dim)) return TKV_EINVAL;
