@@ -642,3 +642,40 @@ def test_kernels_behind_other_work(max_len):
         out.zero_()
         graph.replay()
         assert torch.equal(out, want)
+
+
+def test_threads_and_graphs_side_by_side():
+    """Four threads, two of them on one stream, rotate and attend beside a graph that is replayed on a fifth stream."""
+    import threading
+    p = Pool("int4", [3000, 2000], [1, 1], d=128, page=16).fill()
+    rot, pos = tkv.Rotary(tkv.rope_table(4096, 128)), [ints([i, 3000 - i]) for i in range(5)]
+    q = [queries(p, 4, seed=s) for s in range(5)]
+    want = [p.cache.attend(tkv.rope(q[i], rot, pos[i], inverse=i % 2), p.cu_t) for i in range(5)]
+    shared, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    streams = [shared, shared, torch.cuda.Stream(), torch.cuda.Stream()]
+    with torch.cuda.graph(graph, stream=shared):
+        replayed = p.cache.attend(tkv.rope(q[4], rot, pos[4]), p.cu_t)
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in range(4)], []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(40):
+                    got[i].append(p.cache.attend(tkv.rope(q[i], rot, pos[i], inverse=i % 2), p.cu_t))
+        except Exception as e:   # noqa: BLE001 -- shown below
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    replays = []
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(40):
+            graph.replay()
+            replays.append(replayed.clone())
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    assert all(torch.equal(x, want[i]) for i in range(4) for x in got[i]) and all(torch.equal(x, want[4]) for x in replays)

@@ -1,6 +1,6 @@
 """The operators around a paged KV cache on torch tensors: rope, and PagedCache with append, attend, gather.
 
-Thin wrappers: they check the arguments, allocate outputs and workspace with torch's allocator on the current
+Thin wrappers: they check the arguments, allocate outputs and workspaces with torch's allocator on the current
 stream of the tensors' device, and call the C functions of the same names (include/tkv.h), which say what is computed
 and what a kernel does with positions, pages and lengths that make no sense.  Everything runs on torch's current
 stream; nothing synchronises, and every call can be captured into a CUDA graph.
@@ -14,23 +14,25 @@ stream; nothing synchronises, and every call can be captured into a CUDA graph.
     out = cache.attend(q, cu_tokens)
 """
 import math
+import threading
 
 from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_OK, PagedDesc, RotaryDesc, TkvError,
                load)
 
-_torch = _raw_stream = _current_device = _int32 = None
+_torch = _raw_stream = _current_device = _capturing = _int32 = None
 _DTYPES = {}
 
 
 def _types():
     """torch, imported at the first use (the package itself does not need it)."""
-    global _torch, _raw_stream, _current_device, _int32
+    global _torch, _raw_stream, _current_device, _capturing, _int32
     if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: TKV_BF16, torch.float16: TKV_FP16, torch.float32: TKV_FP32})
         _int32 = torch.int32
         # the handle of a device's current stream and the current device, without an object around them
         _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _capturing = torch._C._cuda_isCurrentStreamCapturing
         _torch = torch
     return _torch
 
@@ -41,7 +43,8 @@ def _refuse(where, why):
     raise e
 
 
-# The checks below run at every call, in front of kernels of a few microseconds: they build no text unless they refuse.
+# What follows runs at every call, in front of kernels of a few microseconds.  An entry point looks at all that matters in one
+# condition; where it does not hold, the checks below say what is wrong.
 def _on(x, where, what, dtype=None, dim=None, device=None):
     """x is a CUDA tensor, of that type and dimension, on that device."""
     if not isinstance(x, _torch.Tensor) or not x.is_cuda:
@@ -56,19 +59,20 @@ def _on(x, where, what, dtype=None, dim=None, device=None):
 
 def _is_int32(x, where, what, shape, device):
     """x is a contiguous int32 tensor of that shape."""
+    if isinstance(x, _torch.Tensor) and x.dtype is _int32 and x.shape == shape and x.is_cuda and x.get_device() == device.index and x.is_contiguous():
+        return
     _on(x, where, what, _int32, None, device)
     if x.shape != shape or not x.is_contiguous():
         _refuse(where, "%s has to be a contiguous int32 tensor %s, not %s" % (what, list(shape), list(x.shape)))
 
 
 def _call(fn, where, device, *args):
-    """The C call on the tensors' device, behind what its current stream holds."""
-    i = device.index
-    if _current_device() != i:
-        with _torch.cuda.device(i):
-            rc = fn(*args, _raw_stream(i) or CUDA_STREAM_LEGACY)
+    """The C call on the tensors' device (its index), behind what its current stream holds."""
+    if _current_device() != device:
+        with _torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(device) or CUDA_STREAM_LEGACY)
     else:
-        rc = fn(*args, _raw_stream(i) or CUDA_STREAM_LEGACY)
+        rc = fn(*args, _raw_stream(device) or CUDA_STREAM_LEGACY)
     if rc != TKV_OK:
         raise TkvError(rc, where)
 
@@ -116,30 +120,36 @@ class Rotary:
         if len(axes) != table.shape[1] or not all(0 <= x < 4 for x in axes):
             _refuse(w, "pair_axis has an axis 0 .. 3 for each pair")
         self.table, self.num_axes, self.pairs = table, max(axes) + 1, table.shape[1]
-        self.device = table.device
-        self._forward, self._inverse = RotaryDesc(), RotaryDesc()
-        for d, inverse in ((self._forward, 0), (self._inverse, 1)):
-            d.table, d.max_positions, d.pairs = table.data_ptr(), table.shape[0], table.shape[1]
-            d.num_axes, d.interleaved, d.inverse = self.num_axes, int(bool(interleaved)), inverse
-            d.pair_axis[:len(axes)] = axes
+        self.device, self._index = table.device, table.get_device()
+        d = self._first = RotaryDesc()
+        d.table, d.max_positions, d.pairs = table.data_ptr(), table.shape[0], table.shape[1]
+        d.num_axes, d.interleaved = self.num_axes, int(bool(interleaved))
+        d.pair_axis[:len(axes)] = axes
+        self._own = threading.local()
 
     def _desc(self, positions, rows, where, inverse=False):
-        """A descriptor with these positions (a copy: calls from several threads do not share one)."""
-        d = RotaryDesc.from_buffer_copy(self._inverse if inverse else self._forward)
+        """The calling thread's descriptor, with these positions: the C call has read it when it returns."""
+        try:
+            d = self._own.desc
+        except AttributeError:
+            d = self._own.desc = RotaryDesc.from_buffer_copy(self._first)
+        d.inverse = inverse
         if positions is None:
             if self.num_axes > 1:
                 _refuse(where, "positions are needed with %d axes" % self.num_axes)
+            d.positions = None
             return d
-        _on(positions, where, "positions", _int32, None, self.device)
+        if not (isinstance(positions, _torch.Tensor) and positions.dtype is _int32 and positions.is_cuda and positions.get_device() == self._index):
+            _on(positions, where, "positions", _int32, None, self.device)
         shape, strides = positions.shape, positions.stride()
         if len(shape) == 1:
-            ok, d.axis_stride = shape[0] == rows and self.num_axes == 1, rows
+            ok, axis_stride = shape[0] == rows and self.num_axes == 1, rows
         else:
             ok = len(shape) == 2 and shape[0] >= self.num_axes and shape[1] == rows
-            d.axis_stride = strides[0] if ok else 0
+            axis_stride = strides[0] if ok else 0
         if not ok or (rows > 1 and strides[-1] != 1):
             _refuse(where, "positions are int32 [%d, %d], rows next to one another, not %s" % (self.num_axes, rows, list(shape)))
-        d.positions = positions.data_ptr()
+        d.positions, d.axis_stride = positions.data_ptr(), axis_stride
         return d
 
 
@@ -154,7 +164,7 @@ def rope(x, rotary, positions, out=None, inverse=False, status=None):
     dt = _DTYPES.get(x.dtype)
     if dt is None:
         _refuse(w, "x is %s: bf16, fp16 or fp32" % x.dtype)
-    if not isinstance(rotary, Rotary) or rotary.device.index != x.get_device():
+    if not isinstance(rotary, Rotary) or rotary._index != x.get_device():
         _refuse(w, "rotary is not a Rotary on %s" % x.device)
     if positions is None:
         _refuse(w, "positions are needed")
@@ -171,7 +181,7 @@ def rope(x, rotary, positions, out=None, inverse=False, status=None):
         _refuse(w, "the channels of x and out have to be contiguous")
     desc = rotary._desc(positions, rows, w, inverse)
     if rows:
-        _call(load().tkv_rope, w, rotary.device, desc, x.data_ptr(), out.data_ptr(), dt, rows, heads, d, xs[0], xs[1], os_[0],
+        _call(load().tkv_rope, w, rotary._index, desc, x.data_ptr(), out.data_ptr(), dt, rows, heads, d, xs[0], xs[1], os_[0],
               os_[1], _status_ptr(status, w, rotary.device))
     return out
 
@@ -227,7 +237,8 @@ class PagedCache:
         self.device, self.num_kv_heads, self.head_dim, self.page_size = pages.device, c.num_kv_heads, c.head_dim, c.page_size
         self.batch, self.max_pages, self.is_int4 = c.batch, c.max_pages, c.kv_type == TKV_INT4
         # what each call reads of the descriptor, without a ctypes access
-        self._c, self._workspace, self._kv_type, self._cu_shape = c, {}, c.kv_type, (c.batch + 1,)
+        self._c, self._kv_type, self._cu_shape, self._index = c, c.kv_type, (c.batch + 1,), pages.get_device()
+        self._sizes, self._own = {}, threading.local()   # of workspaces; a thread's workspaces, by stream
 
     @classmethod
     def empty(cls, num_pages, page_table, lengths, *, num_kv_heads, head_dim, page_size, dtype="int4", k_gain=None, v_gain=None):
@@ -241,6 +252,12 @@ class PagedCache:
 
     def _rows(self, x, where, what, heads):
         """x [rows, heads, d] of a 16-bit type that fits the pages, 16-byte pieces; its element type."""
+        dt = _DTYPES.get(x.dtype) if isinstance(x, _torch.Tensor) else None
+        if dt == self._kv_type or (self.is_int4 and (dt == TKV_BF16 or dt == TKV_FP16)):
+            shape, s = x.shape, x.stride()
+            if (len(shape) == 3 and shape[2] == self.head_dim and (heads is None or shape[1] == heads) and s[2] == 1 and
+                    not (s[0] | s[1]) % 8 and not x.data_ptr() % 16 and x.get_device() == self._index and x.is_cuda):
+                return dt
         _on(x, where, what, None, 3, self.device)
         dt = _DTYPES.get(x.dtype)
         if dt == TKV_FP32 or dt is None or (not self.is_int4 and dt != self._kv_type):
@@ -255,6 +272,27 @@ class PagedCache:
         e = 16 // x.element_size()
         if s[2] != 1 or s[0] % e or s[1] % e or x.data_ptr() % 16:
             _refuse(where, "%s has to lie in 16-byte pieces: contiguous channels, aligned rows and heads" % what)
+
+    def _work(self, hq, max_new):
+        """A workspace for an attention that is enqueued next on the current stream.
+
+        A thread keeps one a stream: what it enqueues there runs in order.  Other threads' launches may come between the
+        two of a call, so they have their own; so has a call that is captured, which may run beside any other later."""
+        size = self._sizes.get((hq, max_new))
+        if size is None:
+            with _torch.cuda.device(self._index):
+                size = self._sizes[hq, max_new] = load().tkv_paged_attention_workspace(self._c, hq, max_new)
+        if _current_device() != self._index or _capturing():
+            return _torch.empty(size, dtype=_torch.uint8, device=self.device)
+        try:
+            kept = self._own.work
+        except AttributeError:
+            kept = self._own.work = {}
+        stream = _raw_stream(self._index)
+        work = kept.get(stream)
+        if work is None or work.numel() < size:
+            work = kept[stream] = _torch.empty(size, dtype=_torch.uint8, device=self.device)
+        return work
 
     def append(self, k, v, cu_tokens, rotary=None, positions=None, status=None):
         """Writes k, v [rows, Hkv, d] (bf16 or fp16) to their places, k rotated on the way if `rotary` is given:
@@ -276,7 +314,7 @@ class PagedCache:
             _refuse(w, "positions without rotary")
         if rows:
             ks, vs = k.stride(), v.stride()
-            _call(load().tkv_paged_append, w, self.device, self._c, desc, k.data_ptr(), v.data_ptr(), dt, rows, ks[0], ks[1],
+            _call(load().tkv_paged_append, w, self._index, self._c, desc, k.data_ptr(), v.data_ptr(), dt, rows, ks[0], ks[1],
                   vs[0], vs[1], cu_tokens.data_ptr(), _status_ptr(status, w, self.device))
 
     def gather(self, cu_tokens, rows, dtype=None, k=None, v=None, lengths=None, status=None):
@@ -309,7 +347,7 @@ class PagedCache:
             c.lengths = lengths.data_ptr()
         if rows:
             ks, vs = k.stride(), v.stride()
-            _call(load().tkv_paged_gather, w, self.device, c, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], rows, ks[0], ks[1],
+            _call(load().tkv_paged_gather, w, self._index, c, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], rows, ks[0], ks[1],
                   vs[0], vs[1], cu_tokens.data_ptr(), _status_ptr(status, w, self.device))
         return k, v
 
@@ -350,16 +388,9 @@ class PagedCache:
         elif return_lse:
             lse = torch.empty((rows, hq), dtype=torch.float32, device=self.device)
         if rows:
-            key = (hq, max_new)
-            size = self._workspace.get(key)
-            if size is None:
-                with torch.cuda.device(self.device):
-                    size = load().tkv_paged_attention_workspace(self._c, hq, max_new)
-                self._workspace[key] = size
-            # of torch's allocator, in stream order: calls on several streams, and captured graphs, get their own
-            work = torch.empty(size, dtype=torch.uint8, device=self.device)
+            work = self._work(hq, max_new)
             qs, os_ = q.stride(), out.stride()
-            _call(load().tkv_paged_attention, w, self.device, self._c, q.data_ptr(), out.data_ptr(),
+            _call(load().tkv_paged_attention, w, self._index, self._c, q.data_ptr(), out.data_ptr(),
                   None if lse is None else lse.data_ptr(), dt, rows, hq, qs[0], qs[1], os_[0], os_[1], cu_tokens.data_ptr(),
-                  max_new, max_len, window, scale, work.data_ptr(), size, _status_ptr(status, w, self.device))
+                  max_new, max_len, window, scale, work.data_ptr(), work.numel(), _status_ptr(status, w, self.device))
         return (out, lse) if return_lse else out
