@@ -18,6 +18,7 @@ using namespace tkv;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAppendCtas = 4, kGatherCtas = 8;   // on an SM at once, by their registers
 
 struct RowArgs {
     tkv_paged c;
@@ -140,52 +141,32 @@ __device__ __forceinline__ void turn_any(const RowArgs& a, const T* k, int64_t r
     if (bad) raise_status(a.status, TKV_EINVAL);
 }
 
-// Where a chunk of a row goes (4-bit pages: its codes and its block's scale), in the page of the first head, and its
-// partner; from head to head it moves by the size of a head's page.
-template <typename T, int D, bool INT4>
-struct Target {
-    uint8_t *to, *scale;
-    int partner, scale_partner;
-    __device__ __forceinline__ Target(uint8_t* page, int page_size, int off, int which, int chunk, int pair_chunks) {
-        using R = Record<D>;
-        if (INT4) {
-            const int r = off & 15;
-            uint8_t* rec = page + (off >> 4) * R::bytes;
-            to = rec + (which ? R::v_codes : R::k_codes) + r * (D / 2) + 4 * chunk;
-            scale = rec + (which ? R::v_scales + (chunk >> 1) * 16 + r : R::k_scales + r * (D / 16) + (chunk >> 1));
-            partner = 4 * pair_chunks;
-            scale_partner = (pair_chunks >> 1) * (which ? 16 : 1);
-        } else {
-            to = page + ((int64_t)which * page_size + off) * (2 * D) + 16 * chunk;
-            scale = nullptr;
-            partner = 16 * pair_chunks;
-            scale_partner = 0;
+// x (8 values), and y if there is a partner, to their places: 4-bit pages, codes and the byte of the block's scale, `scale`
+// bytes behind them; the partner's lie `partner` and `scale_partner` further on.
+template <typename T, bool INT4>
+__device__ __forceinline__ void put(float (&x)[8], float (&y)[8], bool two, uint8_t* to, int scale, int partner, int scale_partner, bool writes_scale, float gain) {
+    if (INT4) {
+        const float inv_7_gain = __frcp_rn(__fmul_rn(7.0f, gain));
+        const float x_max = block_max(x), y_max = block_max(y);
+        uint8_t s;
+        *reinterpret_cast<uint32_t*>(to) = quantise_half(x, x_max, gain, inv_7_gain, &s);
+        if (writes_scale) to[scale] = s;
+        if (two) {
+            *reinterpret_cast<uint32_t*>(to + partner) = quantise_half(y, y_max, gain, inv_7_gain, &s);
+            if (writes_scale) to[scale + scale_partner] = s;
         }
+    } else {
+        *reinterpret_cast<uint4*>(to) = pack<T>(x);
+        if (two) *reinterpret_cast<uint4*>(to + partner) = pack<T>(y);
     }
-    // x, and y to the partner's place if there is one
-    __device__ __forceinline__ void put(float (&x)[8], float (&y)[8], bool two, int chunk, float gain) {
-        if (INT4) {
-            const float inv_7_gain = __frcp_rn(__fmul_rn(7.0f, gain));
-            const float x_max = block_max(x), y_max = block_max(y);
-            uint8_t s;
-            *reinterpret_cast<uint32_t*>(to) = quantise_half(x, x_max, gain, inv_7_gain, &s);
-            if (!(chunk & 1)) *scale = s;
-            if (two) {
-                *reinterpret_cast<uint32_t*>(to + partner) = quantise_half(y, y_max, gain, inv_7_gain, &s);
-                if (!(chunk & 1)) scale[scale_partner] = s;
-            }
-        } else {
-            *reinterpret_cast<uint4*>(to) = pack<T>(x);
-            if (two) *reinterpret_cast<uint4*>(to + partner) = pack<T>(y);
-        }
-    }
-};
+}
 
-// blockIdx.y: the first head.  The threads of a row are an even number, so neighbours share its place.
-// 18,432 rows of 8 heads of 128 into 4-bit pages: 33 us (97 MB, 2.9 TB/s; 27 us without the rotation).  What bounds it there
-// is instructions, about 80 for 8 values; three CTAs an SM were faster than two (36 us) and than four (36 us, spills).
+// blockIdx.y: the first head.  The threads of a row are an even number, so neighbours share its place.  K and V of a head
+// one after the other, the next head's values on their way meanwhile: 64 registers, so four CTAs an SM, which cost a
+// few spills and were worth it (18,432 rows of 8 heads of 128 into 4-bit pages: 28.5 us, 97 MB, 3.4 TB/s; three CTAs 34.5;
+// both at once with three CTAs 32.4).  What bounds it there is instructions, about 75 for 8 values, issued in half the cycles.
 template <typename T, int D, bool INT4, int TURN>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __grid_constant__ RowArgs a) {
     let_next_start();
     wait_for_previous();
     const int rows_here = kThreads / a.units;
@@ -202,19 +183,15 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     const T* v_at = reinterpret_cast<const T*>(a.v) + row * a.v_row + blockIdx.y * a.v_head + 8 * chunk;
     // The next head's values are read while the last one's are worked on, the first one's and the positions before the row's
     // place is looked for: what a thread waits for is memory, several times in a row.
-    uint4 raw[4] = {};
-    auto read = [&](int h) {
+    uint4 k_raw[2] = {}, v_raw[2] = {};
+    auto read = [&](uint4 (&raw)[2], const T*& at, int64_t stride, int h) {
         if (h >= a.c.num_kv_heads) return;
-        raw[0] = __ldg(reinterpret_cast<const uint4*>(k_at));
-        raw[2] = __ldg(reinterpret_cast<const uint4*>(v_at));
-        if (two) {
-            raw[1] = __ldg(reinterpret_cast<const uint4*>(k_at + a.pairs));
-            raw[3] = __ldg(reinterpret_cast<const uint4*>(v_at + a.pairs));
-        }
-        k_at += a.lanes * a.k_head;
-        v_at += a.lanes * a.v_head;
+        raw[0] = __ldg(reinterpret_cast<const uint4*>(at));
+        if (two) raw[1] = __ldg(reinterpret_cast<const uint4*>(at + a.pairs));
+        at += a.lanes * stride;
     };
-    read(blockIdx.y);
+    read(k_raw, k_at, a.k_head, blockIdx.y);
+    read(v_raw, v_at, a.v_head, blockIdx.y);
     int p[4] = {0, 0, 0, 0};
     if (turned && a.positions) {
 #pragma unroll
@@ -233,18 +210,22 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         if (!a.positions) p[0] = position;
         load_angles<NCS>(a, p, NCS * chunk, cs);
     }
-    const int64_t head_bytes = INT4 ? (int64_t)(a.c.page_size >> 4) * Record<D>::bytes : (int64_t)a.c.page_size * (4 * D);
-    uint8_t* head = reinterpret_cast<uint8_t*>(a.c.pages) + (page * a.c.num_kv_heads + blockIdx.y) * head_bytes;
-    Target<T, D, INT4> kt(head, a.c.page_size, off, 0, chunk, pair_chunks), vt(head, a.c.page_size, off, 1, chunk, pair_chunks);
+    using R = Record<D>;
+    const int64_t head_bytes = INT4 ? (int64_t)(a.c.page_size >> 4) * R::bytes : (int64_t)a.c.page_size * (4 * D);
+    // in a head's page: K's place; how far behind it V's lies, and behind each its scale
+    const int r = off & 15, block = chunk >> 1;
+    uint8_t* to = reinterpret_cast<uint8_t*>(a.c.pages) + (page * a.c.num_kv_heads + blockIdx.y) * head_bytes +
+                  (INT4 ? (off >> 4) * R::bytes + r * (D / 2) + 4 * chunk : off * (2 * D) + 16 * chunk);
+    const int to_v = INT4 ? R::v_codes : a.c.page_size * (2 * D), partner = (INT4 ? 4 : 16) * pair_chunks;
+    const int k_scale = R::k_scales + r * (D / 16) + block - (r * (D / 2) + 4 * chunk);
+    const int v_scale = R::v_scales - R::v_codes + block * 16 + r - (r * (D / 2) + 4 * chunk);
     const int64_t next = a.lanes * head_bytes;
 #pragma unroll 1
     for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes) {
-        float x[8], y[8], vx[8], vy[8];
-        unpack<T>(raw[0], x);
-        unpack<T>(raw[2], vx);
-        unpack<T>(raw[1], y);
-        unpack<T>(raw[3], vy);
-        read(h + a.lanes);
+        float x[8], y[8];
+        unpack<T>(k_raw[0], x);
+        unpack<T>(k_raw[1], y);
+        read(k_raw, k_at, a.k_head, h + a.lanes);
         if (TURN == kHalves && turned) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -262,14 +243,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         } else if (TURN == kAny && turned) {
             turn_any(a, k + h * a.k_head, row, position, chunk, x);
         }
-        kt.put(x, y, two, chunk, INT4 && a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f);
-        vt.put(vx, vy, two, chunk, INT4 && a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f);
-        kt.to += next;
-        vt.to += next;
-        if (INT4) {
-            kt.scale += next;
-            vt.scale += next;
-        }
+        put<T, INT4>(x, y, two, to, k_scale, partner, pair_chunks >> 1, !(chunk & 1), INT4 && a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f);
+        unpack<T>(v_raw[0], x);
+        unpack<T>(v_raw[1], y);
+        read(v_raw, v_at, a.v_head, h + a.lanes);
+        put<T, INT4>(x, y, two, to + to_v, v_scale, partner, (pair_chunks >> 1) * 16, !(chunk & 1), INT4 && a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f);
+        to += next;
     }
 }
 
@@ -294,8 +273,9 @@ __device__ __forceinline__ void expand(uint32_t word, uint8_t scale_byte, float 
 }
 
 // TO: element type of the outputs; T: of 16-bit pages.  blockIdx.y: the first head.
+// 18,432 rows of 8 heads of 128 out of 4-bit pages: 19.9 us (97 MB, 4.9 TB/s); with 40 registers, six CTAs an SM, 23.5.
 template <typename TO, typename T, int D, bool INT4>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const __grid_constant__ RowArgs a) {
     let_next_start();
     wait_for_previous();
     constexpr int N = 16 / sizeof(TO), NC = D / N;   // values of a thread, threads of a row
@@ -351,16 +331,24 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     }
 }
 
-// How many heads the threads of a row take at once: a thread walks over up to 8 of them as long as 1,024 threads an SM
-// are left (the angles and the row's place are then read once for them).
-cudaError_t spread_heads(RowArgs& a, int64_t threads_a_head) {
+// How many heads the threads of a row take at once.  A thread that walks over several finds its row's place and angles once
+// for them, which costs as much as kFixed heads; a call takes as long as its waves of CTAs (`per_sm` of them at once), and
+// the last one is rarely full.
+constexpr int kFixed = 1;
+cudaError_t spread_heads(RowArgs& a, int64_t blocks, int per_sm) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int hkv = a.c.num_kv_heads;
-    const int per_thread = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads_a_head * hkv / ((int64_t)sms * 1024)));
-    a.lanes = std::min(65535, (hkv + per_thread - 1) / per_thread);
+    const int64_t at_once = (int64_t)sms * per_sm, hkv = a.c.num_kv_heads;
+    int64_t best = 0;
+    for (int per_thread = 8; per_thread >= 1; --per_thread) {
+        const int64_t lanes = std::min<int64_t>(65535, (hkv + per_thread - 1) / per_thread), heads = (hkv + lanes - 1) / lanes;
+        const int64_t cost = (blocks * lanes + at_once - 1) / at_once * (heads + kFixed);
+        if (best && cost >= best) continue;
+        best = cost;
+        a.lanes = (int)lanes;
+    }
     return cudaSuccess;
 }
 
@@ -459,7 +447,7 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
     if (rows == 0) return TKV_OK;
     a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);
     const int rows_a_block = kThreads / a.units;
-    cudaError_t e = spread_heads(a, rows * a.units);
+    cudaError_t e = spread_heads(a, (rows + rows_a_block - 1) / rows_a_block, kAppendCtas);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((rows + rows_a_block - 1) / rows_a_block), a.lanes);
         e = dtype == TKV_BF16 ? append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream)
@@ -485,7 +473,7 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
         return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     const int64_t threads = rows * (cache->head_dim * dtype_size(dtype) / 16);
-    cudaError_t e = spread_heads(a, threads);
+    cudaError_t e = spread_heads(a, (threads + kThreads - 1) / kThreads, kGatherCtas);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), a.lanes);
         cudaStream_t st = (cudaStream_t)stream;
