@@ -331,25 +331,12 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const __g
     }
 }
 
-// How many heads the threads of a row take at once.  A thread that walks over several finds its row's place and angles once
-// for them, which costs as much as kFixed heads; a call takes as long as its waves of CTAs (`per_sm` of them at once), and
-// the last one is rarely full.
-constexpr int kFixed = 1;
-cudaError_t spread_heads(RowArgs& a, int64_t blocks, int per_sm) {
+cudaError_t spread(RowArgs& a, int64_t blocks, int ctas) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int64_t at_once = (int64_t)sms * per_sm, hkv = a.c.num_kv_heads;
-    int64_t best = 0;
-    for (int per_thread = 8; per_thread >= 1; --per_thread) {
-        const int64_t lanes = std::min<int64_t>(65535, (hkv + per_thread - 1) / per_thread), heads = (hkv + lanes - 1) / lanes;
-        const int64_t cost = (blocks * lanes + at_once - 1) / at_once * (heads + kFixed);
-        if (best && cost >= best) continue;
-        best = cost;
-        a.lanes = (int)lanes;
-    }
-    return cudaSuccess;
+    if (e == cudaSuccess) a.lanes = spread_heads(blocks, a.c.num_kv_heads, (int64_t)sms * ctas, 8);
+    return e;
 }
 
 template <typename T, int D, bool INT4>
@@ -447,7 +434,7 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
     if (rows == 0) return TKV_OK;
     a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);
     const int rows_a_block = kThreads / a.units;
-    cudaError_t e = spread_heads(a, (rows + rows_a_block - 1) / rows_a_block, kAppendCtas);
+    cudaError_t e = spread(a, (rows + rows_a_block - 1) / rows_a_block, kAppendCtas);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((rows + rows_a_block - 1) / rows_a_block), a.lanes);
         e = dtype == TKV_BF16 ? append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream)
@@ -473,7 +460,7 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
         return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     const int64_t threads = rows * (cache->head_dim * dtype_size(dtype) / 16);
-    cudaError_t e = spread_heads(a, (threads + kThreads - 1) / kThreads, kGatherCtas);
+    cudaError_t e = spread(a, (threads + kThreads - 1) / kThreads, kGatherCtas);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), a.lanes);
         cudaStream_t st = (cudaStream_t)stream;

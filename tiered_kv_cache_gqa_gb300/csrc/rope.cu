@@ -17,6 +17,13 @@ using namespace tkv;
 namespace {
 
 constexpr int kThreads = 256;
+// CTAs on an SM at once, by their registers.  4,096 rows of 32 heads of 128 in bf16, halves: 13.4 us with five, 14.0 with four,
+// 14.6 with six (spills); adjacent pairs, which need half the angles, 16,384 rows of 64 heads: 85 us with eight, 92 with
+// six; fp32, 5,003 rows of 13 heads of 80: 8.9 us with six, 9.3 with five, 10.0 with eight.
+template <typename T, bool INTERLEAVED>
+constexpr int ctas_of() {
+    return sizeof(T) == 4 ? 6 : INTERLEAVED ? 8 : 5;
+}
 
 struct RopeArgs {
     const void* x;
@@ -35,9 +42,9 @@ struct RopeArgs {
 // Whole 16-byte pieces: E = 16 / sizeof(T) elements.  Pieces of a head: with halves, piece i takes channels [i E, i E + E) and
 // their partners `pairs` further on; with adjacent pairs, its own E / 2 pairs.  Behind the rotated pieces come the copied
 // ones.  A block holds kThreads / pieces rows; blockIdx.y is the first head.
-// 16,384 rows of 64 heads of 128 in bf16, three axes: 94 us (545 MB, 5.8 TB/s).
+// 16,384 rows of 64 heads of 128 in bf16, three axes: 90 us (545 MB, 6.0 TB/s).
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_of<T, INTERLEAVED>()) rope_kernel(const __grid_constant__ RopeArgs a) {
     let_next_start();
     wait_for_previous();
     constexpr int E = 16 / sizeof(T);
@@ -134,19 +141,16 @@ cudaError_t launch(RopeArgs& a, bool whole, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int64_t full = (int64_t)sms * 2048;   // threads that run at once
     if (!whole) {
         const int64_t total = a.rows * a.heads * (a.pairs + (a.copy_rest ? a.head_dim - 2 * a.pairs : 0));
         const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)sms * 64);
         return launch_behind(rope_pairs_kernel<T>, dim3(grid), kThreads, 0, st, a);
     }
     const int pieces = pieces_of<T>(a);
-    // A thread takes up to 8 heads of its row, which reads the table once for them, as long as two
-    // waves of threads are left; a short call takes one head a thread.
-    const int per_thread = (int)std::min<int64_t>(8, std::max<int64_t>(1, a.rows * a.heads * pieces / (2 * full)));
-    a.lanes = std::min(65535, (a.heads + per_thread - 1) / per_thread);
     const int rows_here = kThreads / pieces;
-    const dim3 grid((unsigned)((a.rows + rows_here - 1) / rows_here), a.lanes);
+    const int64_t blocks = (a.rows + rows_here - 1) / rows_here;
+    a.lanes = spread_heads(blocks, a.heads, (int64_t)sms * (a.interleaved ? ctas_of<T, true>() : ctas_of<T, false>()), 16);
+    const dim3 grid((unsigned)blocks, a.lanes);
     return a.interleaved ? launch_behind(rope_kernel<T, true>, grid, kThreads, 0, st, a)
                          : launch_behind(rope_kernel<T, false>, grid, kThreads, 0, st, a);
 }
