@@ -458,8 +458,8 @@ typedef struct {
 /* Rotates x into out, which may be x itself (same strides).
  * x, out: device [rows][heads][head_dim] of dtype (TKV_BF16, TKV_FP16 or
  * TKV_FP32), rows up to 2^31 - 1, any strides that keep out's elements apart; channels behind the
- * rotated ones are copied.  Computed in fp32, rounded once.  Fast where
- * everything starts on 16-byte boundaries.  A position outside the table turns
+ * rotated ones are copied.  Computed in fp32, rounded once.  Fastest
+ * where everything starts on 16-byte boundaries.  A position outside the table turns
  * its pairs into NaN and raises status to TKV_EINVAL.
  * Errors: TKV_EINVAL, TKV_ECUDA. */
 tkv_status tkv_rope(const tkv_rotary* rotary, const void* x, void* out, int32_t dtype, int64_t rows,

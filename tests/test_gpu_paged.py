@@ -679,3 +679,21 @@ def test_threads_and_graphs_side_by_side():
     torch.cuda.synchronize()
     assert not failed
     assert all(torch.equal(x, want[i]) for i in range(4) for x in got[i]) and all(torch.equal(x, want[4]) for x in replays)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d,pairs,interleaved", [(64, 32, False), (64, 32, True), (76, 38, False), (76, 34, True), (74, 37, False), (70, 20, True),
+                                                (600, 4, False), (600, 4, True)])
+def test_rope_pieces_of_every_size(dtype, d, pairs, interleaved):
+    """Rows that start 0 .. 8 elements behind a 16-byte boundary, into rows that start elsewhere: the same bits, the rest as it was."""
+    rows, heads = 13, 5
+    rot = tkv.Rotary(tkv.rope_table(100, 2 * pairs), [j % 3 for j in range(pairs)], interleaved)
+    pos = torch.randint(0, 100, (3, rows), device="cuda", dtype=torch.int32)
+    base = torch.randn(rows, heads, d + 16, device="cuda").to(dtype)
+    for shift, to in ((0, 0), (8, 0), (4, 4), (2, 4), (1, 0), (0, 3), (6, 2)):
+        x = base[:, :, shift:shift + d]
+        into = torch.full((rows, heads, d + 24), 7.0, device="cuda", dtype=dtype)
+        y = into[:, :, to:to + d]
+        tkv.rope(x, rot, pos, out=y)
+        check_rotation(y, x, rot.table, pos.cpu().numpy(), [j % 3 for j in range(pairs)], interleaved, False)
+        assert torch.equal(y, tkv.rope(x.contiguous(), rot, pos)) and (into[:, :, :to] == 7).all() and (into[:, :, to + d:] == 7).all()

@@ -97,11 +97,11 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicMax(status, code);
 }
 
-// cs[i] = (cos, sin) of pair j0 + i at a row's positions p, one an axis; table, rows of it and j0 lie on 16 bytes.
+// cs[i] = (cos, sin) of pair j0 + i at a row's positions p, one an axis; j0 is a multiple of N.
 template <int N, typename Args>
 __device__ __forceinline__ void load_angles(const Args& a, const int (&p)[4], int j0, float2 (&cs)[N]) {
     bool bad = false;
-    if (a.num_axes == 1) {
+    if (N > 1 && a.num_axes == 1 && a.table_16) {
         const bool in = (uint32_t)p[0] < (uint32_t)a.max_positions;
         const float4* at = reinterpret_cast<const float4*>(a.table + (int64_t)(in ? p[0] : 0) * a.pairs + j0);
         const float nan = __int_as_float(0x7FC00000);

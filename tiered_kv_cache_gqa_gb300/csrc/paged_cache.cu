@@ -30,6 +30,7 @@ struct RowArgs {
     int32_t* status;
     int64_t rows, axis_stride, k_row, k_head, v_row, v_head;
     int pairs, max_positions, num_axes, interleaved;
+    bool table_16;             // two pairs of the table lie on 16 bytes
     int lanes;                 // heads that the threads of a row take at once
     int page_shift;
     float sign;
@@ -427,9 +428,10 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
         a.max_positions = rotary->max_positions;
         a.num_axes = rotary->num_axes;
         a.interleaved = rotary->interleaved != 0;
+        a.table_16 = aligned16(rotary->table) && a.pairs % 2 == 0;
         a.sign = rotary->inverse ? -1.0f : 1.0f;
         for (int j = 0; j < 256; ++j) a.pair_axis[j] = j < rotary->pairs ? rotary->pair_axis[j] : 0;
-        turn = !aligned16(rotary->table) ? kAny : a.interleaved ? (a.pairs % 4 == 0 ? kAdjacent : kAny) : (a.pairs % 16 == 0 ? kHalves : kAny);
+        turn = a.interleaved ? (a.pairs % 4 == 0 ? kAdjacent : kAny) : (a.pairs % 16 == 0 ? kHalves : kAny);
     }
     if (rows == 0) return TKV_OK;
     a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);

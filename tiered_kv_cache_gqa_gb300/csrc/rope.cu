@@ -6,7 +6,7 @@
 // gradient is the rotation by the negated angle: the same kernel with the sine's sign turned.
 //
 // What bounds it is memory: every value is read and written once and costs three operations.  A thread
-// keeps the cosines and sines of its 16 bytes of a head in registers and walks over heads of its
+// keeps the cosines and sines of its piece of a head in registers and walks over heads of its
 // row, so the table (8 bytes a pair, fp32) is read once a row and not once a head.
 #include <algorithm>
 
@@ -17,13 +17,20 @@ using namespace tkv;
 namespace {
 
 constexpr int kThreads = 256;
-// CTAs on an SM at once, by their registers.  4,096 rows of 32 heads of 128 in bf16, halves: 13.4 us with five, 14.0 with four,
-// 14.6 with six (spills); adjacent pairs, which need half the angles, 16,384 rows of 64 heads: 85 us with eight, 92 with
-// six; fp32, 5,003 rows of 13 heads of 80: 8.9 us with six, 9.3 with five, 10.0 with eight.
-template <typename T, bool INTERLEAVED>
+
+// CTAs on an SM at once, by their registers.  16-byte pieces, 4,096 rows of 32 heads of 128 in bf16, halves: 13.4 us with five,
+// 14.0 with four, 14.6 with six (spills); adjacent pairs, which need half the angles, 16,384 rows of 64 heads: 84 us with
+// eight, 92 with six; fp32, 5,003 rows of 13 heads of 80: 8.9 us with six, 9.3 with five, 10.0 with eight.
+template <typename T, int BYTES, bool INTERLEAVED>
 constexpr int ctas_of() {
-    return sizeof(T) == 4 ? 6 : INTERLEAVED ? 8 : 5;
+    return BYTES < 16 || sizeof(T) == 4 ? 6 : INTERLEAVED ? 8 : 5;
 }
+
+template <int BYTES> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
 
 struct RopeArgs {
     const void* x;
@@ -35,20 +42,27 @@ struct RopeArgs {
     int heads, head_dim, pairs, max_positions, num_axes, interleaved;
     int lanes;       // heads that the threads of a row take at once
     bool copy_rest;  // channels behind the rotated ones are copied (out is not x)
+    bool table_16;   // two pairs of the table lie on 16 bytes
     float sign;
     uint8_t pair_axis[256];
 };
 
-// Whole 16-byte pieces: E = 16 / sizeof(T) elements.  Pieces of a head: with halves, piece i takes channels [i E, i E + E) and
-// their partners `pairs` further on; with adjacent pairs, its own E / 2 pairs.  Behind the rotated pieces come the copied
-// ones.  A block holds kThreads / pieces rows; blockIdx.y is the first head.
-// 16,384 rows of 64 heads of 128 in bf16, three axes: 90 us (545 MB, 6.0 TB/s).
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, ctas_of<T, INTERLEAVED>()) rope_kernel(const __grid_constant__ RopeArgs a) {
+// Pieces of BYTES bytes, E elements: 16 bytes where everything allows it, fewer where alignments or numbers of pairs do not
+// (16,000 rows of 16 heads of 74 in bf16, pairs 37 apart, in 2-byte pieces: 20 us, 76 MB; one head at a time 31, a pair a
+// thread 74).  Pieces of a head: with halves, piece i takes channels [i E, i E + E) and their partners `pairs` further on;
+// with adjacent pairs, its own E / 2 pairs.  Behind the rotated pieces come the copied ones.  A block holds kThreads /
+// pieces rows; blockIdx.y is the first head.  16,384 rows of 64 heads of 128 in bf16, three axes: 89 us (545 MB, 6.1 TB/s).
+template <typename T, int BYTES, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, ctas_of<T, BYTES, INTERLEAVED>()) rope_kernel(const __grid_constant__ RopeArgs a) {
     let_next_start();
     wait_for_previous();
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = BYTES / sizeof(T);
     constexpr int NP = INTERLEAVED ? E / 2 : E;   // pairs of a piece
+    using W = typename Word<BYTES>::type;
+    union Piece {
+        W u;
+        T e[E];
+    };
     const int rotated = a.pairs / NP;
     const int pieces = rotated + (a.copy_rest ? (a.head_dim - 2 * a.pairs) / E : 0);
     const int rows_here = kThreads / pieces;
@@ -60,14 +74,18 @@ __global__ void __launch_bounds__(kThreads, ctas_of<T, INTERLEAVED>()) rope_kern
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row + blockIdx.y * a.x_head + first;
     T* out = reinterpret_cast<T*>(a.out) + row * a.out_row + blockIdx.y * a.out_head + first;
     const bool two = !INTERLEAVED && turned;
-    // the next head's values are read while the last one's are turned, the first one's before the angles
-    Vec16<T> lo, hi, next_lo, next_hi;
-    next_hi.u = make_uint4(0, 0, 0, 0);
+    // The next heads' values are read while the last ones' are turned, the first ones' before the angles; of small pieces
+    // several heads at once, so that as many bytes are on their way.
+    constexpr int U = BYTES == 16 ? 1 : BYTES == 8 ? 2 : 4;
+    Piece lo[U], hi[U], next_lo[U], next_hi[U];
     auto read = [&](int h) {
-        if (h >= a.heads) return;
-        next_lo.u = *reinterpret_cast<const uint4*>(x);
-        if (two) next_hi.u = *reinterpret_cast<const uint4*>(x + a.pairs);
-        x += a.lanes * a.x_head;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (h + u * a.lanes >= a.heads) break;
+            next_lo[u].u = *reinterpret_cast<const W*>(x);
+            next_hi[u].u = two ? *reinterpret_cast<const W*>(x + a.pairs) : W();
+            x += a.lanes * a.x_head;
+        }
     };
     read(blockIdx.y);
     float2 cs[NP];
@@ -78,27 +96,35 @@ __global__ void __launch_bounds__(kThreads, ctas_of<T, INTERLEAVED>()) rope_kern
             if (i < a.num_axes) p[i] = __ldg(a.positions + i * a.axis_stride + row);
         load_angles<NP>(a, p, piece * NP, cs);
     }
-    for (int h = blockIdx.y; h < a.heads; h += a.lanes) {
-        lo = next_lo;
-        hi = next_hi;
-        read(h + a.lanes);
-        if (turned) {
+    for (int h = blockIdx.y; h < a.heads; h += U * a.lanes) {
 #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                T& e0 = INTERLEAVED ? lo.e[(2 * k) % E] : lo.e[k];
-                T& e1 = INTERLEAVED ? lo.e[(2 * k + 1) % E] : hi.e[k];
-                const float2 y = rotate_pair(to_float(e0), to_float(e1), cs[k]);
-                e0 = from_float<T>(y.x);
-                e1 = from_float<T>(y.y);
-            }
+        for (int u = 0; u < U; ++u) {
+            lo[u] = next_lo[u];
+            hi[u] = next_hi[u];
         }
-        *reinterpret_cast<uint4*>(out) = lo.u;
-        if (two) *reinterpret_cast<uint4*>(out + a.pairs) = hi.u;
-        out += a.lanes * a.out_head;
+        read(h + U * a.lanes);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (h + u * a.lanes >= a.heads) break;
+            if (turned) {
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    T& e0 = INTERLEAVED ? lo[u].e[(2 * k) % E] : lo[u].e[k];
+                    T& e1 = INTERLEAVED ? lo[u].e[(2 * k + 1) % E] : hi[u].e[k];
+                    const float2 y = rotate_pair(to_float(e0), to_float(e1), cs[k]);
+                    e0 = from_float<T>(y.x);
+                    e1 = from_float<T>(y.y);
+                }
+            }
+            *reinterpret_cast<W*>(out) = lo[u].u;
+            if (two) *reinterpret_cast<W*>(out + a.pairs) = hi[u].u;
+            out += a.lanes * a.out_head;
+        }
     }
 }
 
-// Any alignment and any number of pairs: a thread takes one pair (or one copied channel) of a head.
+// What no piece fits (adjacent pairs that are not aligned to a pair, heads of more pieces than a block has threads): a thread
+// takes one pair (or one copied channel) of a head.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs a) {
     let_next_start();
@@ -128,31 +154,40 @@ __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_const
     }
 }
 
-template <typename T>
-int pieces_of(const RopeArgs& a) {
-    constexpr int E = 16 / sizeof(T);
-    return a.pairs / (a.interleaved ? E / 2 : E) + (a.copy_rest ? (a.head_dim - 2 * a.pairs) / E : 0);
+template <typename T, int BYTES, bool INTERLEAVED>
+cudaError_t launch_pieces(RopeArgs& a, int pieces, int sms, cudaStream_t st) {
+    const int rows_here = kThreads / pieces;
+    const int64_t blocks = (a.rows + rows_here - 1) / rows_here;
+    a.lanes = spread_heads(blocks, a.heads, (int64_t)sms * ctas_of<T, BYTES, INTERLEAVED>(), 16);
+    return launch_behind(rope_kernel<T, BYTES, INTERLEAVED>, dim3((unsigned)blocks, a.lanes), kThreads, 0, st, a);
 }
 
+// `grain`: the bytes that every address and stride of x and out is a multiple of, as a power of two.
 template <typename T>
-cudaError_t launch(RopeArgs& a, bool whole, cudaStream_t st) {
-    whole = whole && pieces_of<T>(a) <= kThreads;
+cudaError_t launch(RopeArgs& a, int grain, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (!whole) {
-        const int64_t total = a.rows * a.heads * (a.pairs + (a.copy_rest ? a.head_dim - 2 * a.pairs : 0));
-        const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)sms * 64);
-        return launch_behind(rope_pairs_kernel<T>, dim3(grid), kThreads, 0, st, a);
+    const int rest = a.copy_rest ? a.head_dim - 2 * a.pairs : 0, least = a.interleaved ? 2 : 1;
+    for (int bytes = std::min(16, grain); bytes >= least * (int)sizeof(T); bytes /= 2) {
+        const int E = bytes / (int)sizeof(T), np = E / least;
+        if (a.pairs % np || rest % E) continue;
+        const int pieces = a.pairs / np + rest / E;
+        if (pieces > kThreads) break;
+        if (a.interleaved) {
+            if (bytes == 16) return launch_pieces<T, 16, true>(a, pieces, sms, st);
+            if (bytes == 8) return launch_pieces<T, 8, true>(a, pieces, sms, st);
+            if constexpr (sizeof(T) == 2) return launch_pieces<T, 4, true>(a, pieces, sms, st);
+        }
+        if (bytes == 16) return launch_pieces<T, 16, false>(a, pieces, sms, st);
+        if (bytes == 8) return launch_pieces<T, 8, false>(a, pieces, sms, st);
+        if (bytes == 4) return launch_pieces<T, 4, false>(a, pieces, sms, st);
+        if constexpr (sizeof(T) == 2) return launch_pieces<T, 2, false>(a, pieces, sms, st);
     }
-    const int pieces = pieces_of<T>(a);
-    const int rows_here = kThreads / pieces;
-    const int64_t blocks = (a.rows + rows_here - 1) / rows_here;
-    a.lanes = spread_heads(blocks, a.heads, (int64_t)sms * (a.interleaved ? ctas_of<T, true>() : ctas_of<T, false>()), 16);
-    const dim3 grid((unsigned)blocks, a.lanes);
-    return a.interleaved ? launch_behind(rope_kernel<T, true>, grid, kThreads, 0, st, a)
-                         : launch_behind(rope_kernel<T, false>, grid, kThreads, 0, st, a);
+    const int64_t total = a.rows * a.heads * (a.pairs + rest);
+    const int grid = (int)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)sms * 64);
+    return launch_behind(rope_pairs_kernel<T>, dim3(grid), kThreads, 0, st, a);
 }
 
 }  // namespace
@@ -213,17 +248,15 @@ extern "C" tkv_status tkv_rope(const tkv_rotary* rotary, const void* x, void* ou
     a.num_axes = rotary->num_axes;
     a.interleaved = rotary->interleaved != 0;
     a.copy_rest = !in_place && head_dim > 2 * rotary->pairs;
+    a.table_16 = aligned16(rotary->table) && a.pairs % 2 == 0;
     a.sign = rotary->inverse ? -1.0f : 1.0f;
     for (int j = 0; j < 256; ++j) a.pair_axis[j] = j < rotary->pairs ? rotary->pair_axis[j] : 0;
-    // 16-byte pieces: every piece, of the tensors and of the table, starts on a 16-byte boundary and holds whole pairs
-    const int64_t E = 16 / size;
-    const bool whole = aligned16(x) && aligned16(out) && aligned16(rotary->table) && a.pairs % 2 == 0 && x_row_stride % E == 0 && x_head_stride % E == 0 &&
-                       out_row_stride % E == 0 && out_head_stride % E == 0 &&
-                       a.pairs % (a.interleaved ? E / 2 : E) == 0 && (!a.copy_rest || (head_dim - 2 * a.pairs) % E == 0);
+    const uint64_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) | size * (uint64_t)(x_row_stride | x_head_stride | out_row_stride | out_head_stride) | 16;
+    const int grain = (int)(all & (0 - all));
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = dtype == TKV_BF16   ? launch<__nv_bfloat16>(a, whole, st)
-                          : dtype == TKV_FP16 ? launch<__half>(a, whole, st)
-                                              : launch<float>(a, whole, st);
+    const cudaError_t e = dtype == TKV_BF16   ? launch<__nv_bfloat16>(a, grain, st)
+                          : dtype == TKV_FP16 ? launch<__half>(a, grain, st)
+                                              : launch<float>(a, grain, st);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return TKV_ECUDA;
