@@ -755,24 +755,25 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
 // expanded once for twice the rows.
 int row_tiles(int group, int max_new) { return (int64_t)group * max_new > 8 ? 2 : 1; }
 
-cudaError_t device_ctas(int ctas, int* grid, int* dev) {
-    int sms = 0;
-    cudaError_t e = cudaGetDevice(dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, *dev);
-    *grid = ctas * sms;
-    return e;
+cudaError_t device_sms(int* sms, int* dev) {
+    const cudaError_t e = cudaGetDevice(dev);
+    return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) : e;
+}
+
+int64_t workspace_bytes_of(const tkv_paged* c, int32_t hq, int32_t max_new, int sms) {   // two CTAs an SM: the most that any variant uses
+    return (int64_t)2 * sms * (2 + kWarps) * 8 * row_tiles(hq / c->num_kv_heads, max_new) * (c->head_dim + 4) * 4;
 }
 
 template <int D, int NT, int KIND>
-cudaError_t launch(PagedAttnArgs& a, cudaStream_t st) {
+cudaError_t launch(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
     using C = Config<D, NT, KIND>;
     constexpr int smem = sizeof(Shared<D, NT, KIND>);
     static_assert(C::ctas * (smem + 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
-    int dev = 0;
-    cudaError_t e = device_ctas(C::ctas, &a.grid, &dev);
+    cudaError_t e = cudaSuccess;
+    a.grid = C::ctas * sms;
     // the kernel's shared-memory limit, once a device
     static std::atomic<uint64_t> ready{0};
-    if (e == cudaSuccess && !(dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1))) {
+    if (!(dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1))) {
         e = cudaFuncSetAttribute(paged_attention_kernel<D, NT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_release);
     }
@@ -783,10 +784,10 @@ cudaError_t launch(PagedAttnArgs& a, cudaStream_t st) {
 }
 
 template <int D, int NT>
-cudaError_t launch_kind(PagedAttnArgs& a, cudaStream_t st) {
-    return a.c.kv_type == TKV_INT4   ? launch<D, NT, kInt4>(a, st)
-           : a.c.kv_type == TKV_BF16 ? launch<D, NT, kBf16>(a, st)
-                                     : launch<D, NT, kFp16>(a, st);
+cudaError_t launch_kind(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
+    return a.c.kv_type == TKV_INT4   ? launch<D, NT, kInt4>(a, sms, dev, st)
+           : a.c.kv_type == TKV_BF16 ? launch<D, NT, kBf16>(a, sms, dev, st)
+                                     : launch<D, NT, kFp16>(a, sms, dev, st);
 }
 
 bool attention_shape_ok(const tkv_paged* c, int32_t hq, int32_t max_new) {
@@ -797,12 +798,12 @@ bool attention_shape_ok(const tkv_paged* c, int32_t hq, int32_t max_new) {
 
 extern "C" int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_heads, int32_t max_new) {
     if (!attention_shape_ok(cache, num_q_heads, max_new)) return 0;
-    int grid = 0, dev = 0;
-    if (device_ctas(2, &grid, &dev) != cudaSuccess) {   // the most that any variant uses
+    int sms = 0, dev = 0;
+    if (device_sms(&sms, &dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
-    return (int64_t)grid * (2 + kWarps) * 8 * row_tiles(num_q_heads / cache->num_kv_heads, max_new) * (cache->head_dim + 4) * 4;
+    return workspace_bytes_of(cache, num_q_heads, max_new, sms);
 }
 
 extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q, void* out, float* lse, int32_t dtype,
@@ -822,9 +823,13 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
         q_head_stride % 8 || out_row_stride % 8 || out_head_stride % 8)
         return TKV_EINVAL;
     if (!strides_apart(rows, out_row_stride, num_q_heads, out_head_stride, cache->head_dim)) return TKV_EINVAL;
-    const int64_t need = tkv_paged_attention_workspace(cache, num_q_heads, max_new);
-    if (need == 0) return TKV_ECUDA;
-    if (!workspace || workspace_bytes < need) return TKV_ECAPACITY;
+    int sms = 0, dev = 0;
+    cudaError_t e = device_sms(&sms, &dev);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TKV_ECUDA;
+    }
+    if (!workspace || workspace_bytes < workspace_bytes_of(cache, num_q_heads, max_new, sms)) return TKV_ECAPACITY;
     PagedAttnArgs a{};
     a.c = *cache;
     a.q = q;
@@ -848,14 +853,12 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.scale_log2 = (float)((double)scale * kLog2E);
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = row_tiles(a.group, max_new);
-    int ctas = 0, dev = 0;
-    cudaError_t e = device_ctas(1, &ctas, &dev);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
-    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= ctas);
+    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms);
     const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
-    if (e == cudaSuccess) e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, st) : launch_kind<128, 2>(a, st))
-                                                 : (nt == 1 ? launch_kind<64, 1>(a, st) : launch_kind<64, 2>(a, st));
+    e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, sms, dev, st) : launch_kind<128, 2>(a, sms, dev, st))
+                                                 : (nt == 1 ? launch_kind<64, 1>(a, sms, dev, st) : launch_kind<64, 2>(a, sms, dev, st));
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return TKV_ECUDA;
