@@ -697,3 +697,42 @@ def test_rope_pieces_of_every_size(dtype, d, pairs, interleaved):
         tkv.rope(x, rot, pos, out=y)
         check_rotation(y, x, rot.table, pos.cpu().numpy(), [j % 3 for j in range(pairs)], interleaved, False)
         assert torch.equal(y, tkv.rope(x.contiguous(), rot, pos)) and (into[:, :, :to] == 7).all() and (into[:, :, to + d:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths,n,G,page,window", [
+    ([3000], [6], 5, 16, 0), ([700, 0, 33, 1290, 20], [6, 2, 33, 0, 20], 3, 32, 0), ([300, 2100], [40, 3], 8, 16, 0),
+    ([1200, 90], [9, 9], 2, 64, 100), ([520, 3], [30, 5], 1, 16, 1), ([64], [64], 4, 16, 0)])
+def test_tiles_of_32_rows(dtype, d, lengths, n, G, page, window):
+    """What the host expects to be long (the hint says so) is taken 32 rows at a time; the same steps said to be short are not."""
+    p = Pool("int4", lengths, n, d=d, page=page).fill()
+    q = queries(p, G, dtype=dtype)
+    want = p.oracle(q, window=window)
+    for ln in (1 << 30, 1):
+        out = torch.full((q.shape[0] + 2, q.shape[1], d), 5.0, device="cuda", dtype=dtype)
+        padded = torch.cat([q, q[:1], q[:1]])
+        _, lse = p.cache.attend(padded, p.cu_t, max_new=max(n), max_len=ln, window=(1 << 30 if window == 0 else window), out=out, return_lse=True)
+        close(p, out[:-2], lse[:-2], want, dtype)
+        assert (out[-2:] == 5.0).all()
+
+
+def test_bad_values_in_tiles_of_32_rows():
+    """A NaN, an infinity and a bad page where only some of 32 rows look."""
+    p = Pool("int4", [400, 130], [10, 7], page=16).fill()
+    k, v = (torch.randn(4, 2, 64, device="cuda") for _ in range(2))
+    v[0, 0, 3], v[1, 1, 9], k[2, 0, 1], v[3, 0, 40] = float("nan"), float("inf"), float("nan"), -float("inf")
+    p.cache.append(k.to(BF16), v.to(BF16), ints([0, 2, 4]))        # the last two positions of both
+    p.sync_back()
+    p.pt[0, 3] = p.num_pages + 5
+    p.table.copy_(torch.tensor(p.pt))
+    q = queries(p, 4)
+    status = ints([0])
+    out = f32(p.cache.attend(q, p.cu_t, max_new=10, max_len=1 << 30, status=status))
+    assert status.item() == tkv.TKV_ECAPACITY
+    with np.errstate(all="ignore"):
+        want = p.oracle(q)[0]
+    some = np.isfinite(want)
+    assert np.array_equal(np.isfinite(out), some) and some.any() and not some.all()
+    # p's rounding 2^-11 and the sums' 2^-14 of at most max |V| < 6, the result's 2^-8: below 2^-7 (1 + |o|)
+    assert np.all(np.abs(out[some] - want[some]) <= 2.0 ** -7 * (1 + np.abs(want[some])))

@@ -192,9 +192,10 @@ template <int D, int NT, int KIND>
 struct Config {
     static constexpr int R = 8 * NT;
     static constexpr int ctas = (KIND == kInt4 && NT == 1) ? 2 : 1;
-    static constexpr int stages = KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : 6) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
+    static constexpr int stages = KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
     static constexpr int queue = stages <= 6 ? 8 : 16;   // pieces: the one computed, one a stage, one not yet copied
     static constexpr int warp_ring = stages * TileOf<D, KIND>::bytes;
+    static constexpr int at_once = NT == 4 ? 1 : TileOf<D, KIND>::groups;   // groups of positions, by the registers
 };
 
 // A warp's part of an item.
@@ -218,6 +219,7 @@ struct Shared {
     Where where[kWarps], ends[2];
     int flags[kWarps], last[kWarps];    // of each warp's last piece, and its place in the queue
     uint8_t bad[kWarps][C::stages][2];  // records of a stage that have no page
+    uint2 q[kWarps][Query<D, NT>::words];
 };
 
 // ------------------------------------------------------------------ out
@@ -503,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             ++taken;
             const int all_from = piece.rows.all_from, all_until = piece.rows.all_until, tiles = piece.tiles;
             Query<D, NT> q;
+            q.s = sh.q[warp] + lane;
             load_query<D, NT, KIND>(reinterpret_cast<const uint16_t*>(a.q), a.q_row, a.q_head, a.q_fp16, a.group, a.group_mul, a.scale_log2,
                                     KIND == kInt4 && a.c.k_gain ? __ldg(a.c.k_gain + piece.rows.h) : 1.0f, lane, piece.rows, q);
             sums.clear();
@@ -514,9 +517,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 const uint8_t* at = sh.ring[warp] + stage * TB;
                 const uint32_t at_s = smem_u32(at);
                 const uint32_t bad = sh.bad[warp][stage][0] | (KIND == kInt4 ? sh.bad[warp][stage][1] << 1 : 0);
-                if (!bad && p0 + TP <= all_until && p0 >= all_from)
-                    attend_tile<D, NT, KIND, T::groups, true>(at, at_s, lane, p0, false, piece.rows, a.group, a.group_mul, a.window, q, sums);
-                else {
+                if (!bad && p0 + TP <= all_until && p0 >= all_from) {
+#pragma unroll 1
+                    for (int g = 0; g < T::groups; g += C::at_once)
+                        attend_tile<D, NT, KIND, C::at_once, true>(at + g * Record<D>::bytes, at_s, lane, p0 + 16 * g, false, piece.rows, a.group,
+                                                                   a.group_mul, a.window, q, sums);
+                } else {
 #pragma unroll 1
                     for (int g = 0; g < T::groups; ++g)
                         attend_tile<D, NT, KIND, 1, false>(at + g * Record<D>::bytes, at_s, lane, p0 + 16 * g, (bad >> g) & 1, piece.rows, a.group,
@@ -686,7 +692,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     float4 x[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) x[k] = make_float4(0, 0, 0, 0);
-    float4 ml = make_float4(kLowest, 0.0f, kLowest, 0.0f);   // of warp w's two rows, w < 4 NT
+    constexpr int TWOS = (4 * NT + kCombineWarps - 1) / kCombineWarps;   // a warp takes two rows, or twice two
+    float4 ml_of[TWOS];
+#pragma unroll
+    for (int k = 0; k < TWOS; ++k) ml_of[k] = make_float4(kLowest, 0.0f, kLowest, 0.0f);
     for (int i0 = 0; i0 < pieces; i0 += 32) {
         const int n = min(32, pieces - i0);
         float4 y[PER][8];   // eight loads in flight, the first of them while the weights are worked out
@@ -697,9 +706,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
                 for (int q = 0; q < 8; ++q) y[k][q] = record(i0 + min(p + q, n - 1))[min(tid + k * kCombineWarps * 32, SLOTS - 1)];
         };
         read(0);
-        if (warp < 4 * NT) {
+#pragma unroll
+        for (int k = 0; k < TWOS; ++k) {
+            const int two = warp + k * kCombineWarps;
+            if (two >= 4 * NT) break;
+            float4& ml = ml_of[k];
             float4 v = make_float4(kLowest, 0.0f, kLowest, 0.0f);
-            if (lane < n) v = record(i0 + lane)[SLOTS + warp];
+            if (lane < n) v = record(i0 + lane)[SLOTS + two];
             float m0 = v.x, m1 = v.z;
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
@@ -716,10 +729,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
                 l1 += __shfl_xor_sync(0xffffffffu, l1, o);
             }
             ml = make_float4(m0, ml.y * f0 + l0, m1, ml.w * f1 + l1);
-            weight_of[lane][warp] = make_float2(w0, w1);
+            weight_of[lane][two] = make_float2(w0, w1);
             if (lane == 0) {
-                scale_ml[warp] = make_float4(f0, f1, 0.0f, 0.0f);
-                total_ml[warp] = ml;
+                scale_ml[two] = make_float4(f0, f1, 0.0f, 0.0f);
+                total_ml[two] = ml;
             }
         }
         __syncthreads();
@@ -751,16 +764,27 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
 }
 
 // ------------------------------------------------------------------ launch
-// Row tiles are 8 rows, or 16 where a step brings more than 8 rows a KV head: the cache is then read and
-// expanded once for twice the rows.
+// Row tiles are 8 rows, or 16 where a step brings more than 8 rows a KV head: the cache is then read and expanded once for
+// twice the rows.
 int row_tiles(int group, int max_new) { return (int64_t)group * max_new > 8 ? 2 : 1; }
+
+// Tiles of 32 rows of 4-bit pages do that once more, but the code is long and the joining heavy: worth it from so many tiles a
+// computing warp on, by the host's estimate.  30 rows a KV head, 8 x 8 heads of 64: 36.3 us with 16 rows and 37.3 with 32 at
+// 8,192 positions (15 tiles a warp), 65.7 and 58.4 at 16,384, 244 and 170 at 65,536; of 128: 90.0 and 93.1 at 16,384 (31
+// tiles), 163.5 and 156.2 at 32,768, 307 and 276 at 65,536.
+bool rows_of_32(const PagedAttnArgs& a, int max_new, int64_t sight, int sms) {
+    const int64_t rows = (int64_t)a.group * max_new;
+    if (a.c.kv_type != TKV_INT4 || rows <= 16) return false;
+    const double tiles = (double)a.c.batch * a.c.num_kv_heads * ((rows + 31) / 32) * ((sight + 31) / 32);
+    return tiles >= (a.c.head_dim == 64 ? 18.0 : 45.0) * kWarps * sms;
+}
 
 cudaError_t device_sms(int* sms, int* dev) {
     const cudaError_t e = cudaGetDevice(dev);
     return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) : e;
 }
 
-int64_t workspace_bytes_of(const tkv_paged* c, int32_t hq, int32_t max_new, int sms) {   // two CTAs an SM: the most that any variant uses
+int64_t workspace_bytes_of(const tkv_paged* c, int32_t hq, int32_t max_new, int sms) {   // the most that any variant uses: two CTAs an SM, or one with twice the rows
     return (int64_t)2 * sms * (2 + kWarps) * 8 * row_tiles(hq / c->num_kv_heads, max_new) * (c->head_dim + 4) * 4;
 }
 
@@ -788,6 +812,11 @@ cudaError_t launch_kind(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
     return a.c.kv_type == TKV_INT4   ? launch<D, NT, kInt4>(a, sms, dev, st)
            : a.c.kv_type == TKV_BF16 ? launch<D, NT, kBf16>(a, sms, dev, st)
                                      : launch<D, NT, kFp16>(a, sms, dev, st);
+}
+
+template <int D>
+cudaError_t launch_rows(PagedAttnArgs& a, int nt, int sms, int dev, cudaStream_t st) {
+    return nt == 1 ? launch_kind<D, 1>(a, sms, dev, st) : nt == 2 ? launch_kind<D, 2>(a, sms, dev, st) : launch<D, 4, kInt4>(a, sms, dev, st);
 }
 
 bool attention_shape_ok(const tkv_paged* c, int32_t hq, int32_t max_new) {
@@ -852,13 +881,12 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.q_fp16 = dtype == TKV_FP16;
     a.scale_log2 = (float)((double)scale * kLog2E);
     cudaStream_t st = (cudaStream_t)stream;
-    const int nt = row_tiles(a.group, max_new);
+    const int nt = rows_of_32(a, max_new, sight, sms) ? 4 : row_tiles(a.group, max_new);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
     a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms);
     const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
-    e = cache->head_dim == 128 ? (nt == 1 ? launch_kind<128, 1>(a, sms, dev, st) : launch_kind<128, 2>(a, sms, dev, st))
-                                                 : (nt == 1 ? launch_kind<64, 1>(a, sms, dev, st) : launch_kind<64, 2>(a, sms, dev, st));
+    e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return TKV_ECUDA;

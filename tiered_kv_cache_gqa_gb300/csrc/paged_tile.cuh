@@ -123,10 +123,26 @@ struct Sums {
 };
 
 // Fragments of q^T: column r of row tile nt.  4 bits: channels in the order of the codes' pairs.
+// Where they would take 64 registers the lane keeps them in shared memory, every 32nd uint2 of its own.
 template <int D, int NT>
 struct Query {
-    uint32_t f[NT][D / 16][2];
+    static constexpr bool kShared = D * NT > 256;
+    static constexpr int words = kShared ? NT * (D / 16) * 32 : 1;   // uint2s of a warp
+    uint32_t f[kShared ? 1 : NT][kShared ? 1 : D / 16][2];
+    uint2* s;
     float z0[NT], z1[NT];      // S -> z, columns 2 cq and 2 cq + 1
+    __device__ __forceinline__ uint2 get(int nt, int i) const {
+        if constexpr (kShared) return s[(nt * (D / 16) + i) * 32];
+        else return make_uint2(f[nt][i][0], f[nt][i][1]);
+    }
+    __device__ __forceinline__ void set(int nt, int i, uint32_t a, uint32_t b) {
+        if constexpr (kShared) {
+            s[(nt * (D / 16) + i) * 32] = make_uint2(a, b);
+        } else {
+            f[nt][i][0] = a;
+            f[nt][i][1] = b;
+        }
+    }
 };
 
 // The position, within a group of 16, that row i of a fragment stands for.  4 bits: 0 1 3 2 4 5 7 6 8 .., so that the
@@ -186,7 +202,10 @@ __device__ __forceinline__ void scores_int4(const uint8_t* rec, int r, int cq, c
                 const uint32_t f0 = expand_low(x, sa[k], a1032), f2 = expand_high(x, sa[k], a72);
                 const uint32_t f1 = expand_low(y, sb[k], b1032), f3 = expand_high(y, sb[k], b72);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(z[nt], f0, f1, f2, f3, q.f[nt][2 * w + i][0], q.f[nt][2 * w + i][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint2 b = q.get(nt, 2 * w + i);
+                    mma_f16(z[nt], f0, f1, f2, f3, b.x, b.y);
+                }
             }
     }
 }
@@ -201,8 +220,9 @@ __device__ __forceinline__ void scores_16(uint32_t k_at, int lane, const Query<D
         ldmatrix4(f, k_at + row * TileOf<D, KIND>::row + (2 * i + (lane >> 4)) * 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (KIND == kBf16) mma_bf16(z[nt], f[0], f[1], f[2], f[3], q.f[nt][i][0], q.f[nt][i][1]);
-            else mma_f16(z[nt], f[0], f[1], f[2], f[3], q.f[nt][i][0], q.f[nt][i][1]);
+            const uint2 b = q.get(nt, i);
+            if (KIND == kBf16) mma_bf16(z[nt], f[0], f[1], f[2], f[3], b.x, b.y);
+            else mma_f16(z[nt], f[0], f[1], f[2], f[3], b.x, b.y);
         }
     }
 }
@@ -500,8 +520,8 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
                 const int w = i >> 1, c = (i & 1) * 2;
-                q.f[nt][i][0] = half2_bits(__floats2half2_rn(x[8 * w + c] * up, x[8 * w + c + 4] * up));
-                q.f[nt][i][1] = half2_bits(__floats2half2_rn(x[8 * w + c + 1] * up, x[8 * w + c + 5] * up));
+                q.set(nt, i, half2_bits(__floats2half2_rn(x[8 * w + c] * up, x[8 * w + c + 4] * up)),
+                      half2_bits(__floats2half2_rn(x[8 * w + c + 1] * up, x[8 * w + c + 5] * up)));
             }
             const float z = scale_log2 * gain * 16.0f / up;
             q.z0[nt] = __shfl_sync(0xffffffffu, z, 8 * cq);
@@ -509,8 +529,8 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
         } else {
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
-                q.f[nt][i][0] = is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq)) : 0u;
-                q.f[nt][i][1] = is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq + 8)) : 0u;
+                q.set(nt, i, is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq)) : 0u,
+                      is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq + 8)) : 0u);
             }
             q.z0[nt] = q.z1[nt] = scale_log2;
         }
