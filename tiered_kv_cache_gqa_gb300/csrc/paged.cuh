@@ -87,7 +87,7 @@ __device__ __forceinline__ float2 table_at(const float2* table, int pairs, int m
         *bad = true;
         return make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
     }
-    float2 cs = __ldg(table + (int64_t)p * pairs + j);
+    float2 cs = table[(int64_t)p * pairs + j];
     cs.y *= sign;
     return cs;
 }
@@ -107,7 +107,7 @@ __device__ __forceinline__ void load_angles(const Args& a, const int (&p)[4], in
         const float nan = __int_as_float(0x7FC00000);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const float4 v = __ldg(at + i);
+            const float4 v = at[i];
             cs[2 * i] = in ? make_float2(v.x, v.y * a.sign) : make_float2(nan, nan);
             cs[2 * i + 1] = in ? make_float2(v.z, v.w * a.sign) : make_float2(nan, nan);
         }
@@ -124,11 +124,11 @@ __device__ __forceinline__ void load_angles(const Args& a, const int (&p)[4], in
 
 // The sequence that row `row` of a step belongs to: cu[b] <= row < cu[b + 1]; -1 behind the last.
 __device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int row) {
-    if (row < __ldg(cu) || row >= __ldg(cu + batch)) return -1;
+    if (row < cu[0] || row >= cu[batch]) return -1;
     int lo = 0, hi = batch;   // cu[lo] <= row < cu[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= row) lo = mid; else hi = mid;
+        if (cu[mid] <= row) lo = mid; else hi = mid;
     }
     return lo;
 }
@@ -137,6 +137,9 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int
 // memory only behind wait_for_previous, which lasts until the kernel before it is done and its writes can be seen.  A
 // kernel that calls let_next_start first lets its successor start although its predecessor still runs: the successor
 // then may not read anything before its own wait.
+// Every load is an ordinary one.  The read-only path (__ldg, ld.global.nc) is for memory that nothing writes while the kernel
+// exists, and these kernels exist before what precedes them has finished: the wait does not hold such a load back, nor does
+// it renew a line that the SM read through that path for a kernel still running when this one came.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

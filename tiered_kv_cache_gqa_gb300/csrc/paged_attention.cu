@@ -100,8 +100,8 @@ struct Seq {
 template <int R, int TP>
 __device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
     Seq s;
-    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    s.full = max(0, __ldg(a.c.lengths + b));
+    const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    s.full = max(0, a.c.lengths[b]);
     s.first_row = c0;
     s.n = (c0 < 0 || c1 < c0 || c1 > a.rows) ? -1 : c1 - c0;
     s.len = min(s.full, a.c.max_pages << a.page_shift);
@@ -324,7 +324,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     bool first = true;   // the ring's first round: nothing to wait for
     auto look_up = [&]() {   // a 4-bit tile has two records, which may lie in two pages
         const int p = pos + (KIND == kInt4 ? (k & 1) * 16 : 0);
-        page = p < end ? __ldg(table + (p >> a.page_shift)) : -2;
+        page = p < end ? table[p >> a.page_shift] : -2;
     };
     while (__any_sync(0xffffffffu, left + tiles > 0 && spins < kSpinLimit)) {
         bool moved = false;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     int taken = 0;                       // pieces of this warp
     Sums<D, NT> sums;
     const bool fp16 = KIND == kFp16 || (KIND == kInt4 && a.q_fp16);
-    auto gain_of = [&](int h) { return KIND == kInt4 ? 16.0f * (a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f) : 1.0f; };
+    auto gain_of = [&](int h) { return KIND == kInt4 ? 16.0f * (a.c.v_gain ? a.c.v_gain[h] : 1.0f) : 1.0f; };
     if (warp == kWarps) {
         const int w = min(lane >> 2, kWarps - 1);
         copy_tiles<D, NT, KIND>(a, sh, lane, w, sh.where[w], lane >> 2 < kWarps ? tiles_of(w) : 0);
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             Query<D, NT> q;
             q.s = sh.q[warp] + lane;
             load_query<D, NT, KIND>(reinterpret_cast<const uint16_t*>(a.q), a.q_row, a.q_head, a.q_fp16, a.group, a.group_mul, a.scale_log2,
-                                    KIND == kInt4 && a.c.k_gain ? __ldg(a.c.k_gain + piece.rows.h) : 1.0f, lane, piece.rows, q);
+                                    KIND == kInt4 && a.c.k_gain ? a.c.k_gain[piece.rows.h] : 1.0f, lane, piece.rows, q);
             sums.clear();
             failed = __any_sync(0xffffffffu, !mbar_wait(full0 + 8 * stage, parity));
             if (failed) break;
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     wait_for_previous();
     if (pieces == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? __ldg(a.c.v_gain + rows.h) : 1.0f) : 1.0f;
+    const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? a.c.v_gain[rows.h] : 1.0f) : 1.0f;
     const float4* first = a.part + (int64_t)2 * blockIdx.x * SIZE;
     auto record = [&](int i) { return first + (i ? 2 * i * SIZE : SIZE); };
     float4 x[PER];

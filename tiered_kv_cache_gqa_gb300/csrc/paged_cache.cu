@@ -44,11 +44,11 @@ __device__ __forceinline__ bool place_of_row(const RowArgs& a, int64_t row, int6
     const int b = sequence_of_row(a.cu, a.c.batch, (int)row);
     *page = -2;
     if (b < 0) return false;
-    const int pos = __ldg(a.c.lengths + b) - (__ldg(a.cu + b + 1) - (int)row);
+    const int pos = a.c.lengths[b] - (a.cu[b + 1] - (int)row);
     *page = -1;
     *position = pos;
     if (pos < 0 || (pos >> a.page_shift) >= a.c.max_pages) return false;
-    const int p = __ldg(a.c.page_table + (int64_t)b * a.c.max_pages + (pos >> a.page_shift));
+    const int p = a.c.page_table[(int64_t)b * a.c.max_pages + (pos >> a.page_shift)];
     if (p < 0 || p >= a.c.num_pages) return false;
     *page = p;
     *off = pos & (a.c.page_size - 1);
@@ -132,7 +132,7 @@ __device__ __forceinline__ void turn_any(const RowArgs& a, const T* k, int64_t r
         if (ch >= 2 * a.pairs) break;
         const bool first = a.interleaved ? !(ch & 1) : ch < a.pairs;
         const int j = a.interleaved ? ch >> 1 : first ? ch : ch - a.pairs;
-        const int p = a.positions ? __ldg(a.positions + a.pair_axis[j] * a.axis_stride + row) : own_position;
+        const int p = a.positions ? a.positions[a.pair_axis[j] * a.axis_stride + row] : own_position;
         const float2 cs = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
         const float own = to_float(k[ch]), other = to_float(k[a.interleaved ? ch ^ 1 : first ? ch + a.pairs : ch - a.pairs]);
         const float y = first ? rotate_pair(own, other, cs).x : rotate_pair(other, own, cs).y;
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __g
     uint4 k_raw[2] = {}, v_raw[2] = {};
     auto read = [&](uint4 (&raw)[2], const T*& at, int64_t stride, int h) {
         if (h >= a.c.num_kv_heads) return;
-        raw[0] = __ldg(reinterpret_cast<const uint4*>(at));
-        if (two) raw[1] = __ldg(reinterpret_cast<const uint4*>(at + a.pairs));
+        raw[0] = *reinterpret_cast<const uint4*>(at);
+        if (two) raw[1] = *reinterpret_cast<const uint4*>(at + a.pairs);
         at += a.lanes * stride;
     };
     read(k_raw, k_at, a.k_head, blockIdx.y);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __g
     if (turned && a.positions) {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            if (x < a.num_axes) p[x] = __ldg(a.positions + x * a.axis_stride + row);
+            if (x < a.num_axes) p[x] = a.positions[x * a.axis_stride + row];
     }
     int64_t page;
     int off, position;
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __g
     const int64_t next = a.lanes * head_bytes;
 #pragma unroll 1
     for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes) {
+        const float k_gain = INT4 && a.c.k_gain ? a.c.k_gain[h] : 1.0f, v_gain = INT4 && a.c.v_gain ? a.c.v_gain[h] : 1.0f;
         float x[8], y[8];
         unpack<T>(k_raw[0], x);
         unpack<T>(k_raw[1], y);
@@ -244,11 +245,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __g
         } else if (TURN == kAny && turned) {
             turn_any(a, k + h * a.k_head, row, position, chunk, x);
         }
-        put<T, INT4>(x, y, two, to, k_scale, partner, pair_chunks >> 1, !(chunk & 1), INT4 && a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f);
+        put<T, INT4>(x, y, two, to, k_scale, partner, pair_chunks >> 1, !(chunk & 1), k_gain);
         unpack<T>(v_raw[0], x);
         unpack<T>(v_raw[1], y);
         read(v_raw, v_at, a.v_head, h + a.lanes);
-        put<T, INT4>(x, y, two, to + to_v, v_scale, partner, (pair_chunks >> 1) * 16, !(chunk & 1), INT4 && a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f);
+        put<T, INT4>(x, y, two, to + to_v, v_scale, partner, (pair_chunks >> 1) * 16, !(chunk & 1), v_gain);
         to += next;
     }
 }
@@ -274,7 +275,7 @@ __device__ __forceinline__ void expand(uint32_t word, uint8_t scale_byte, float 
 }
 
 // TO: element type of the outputs; T: of 16-bit pages.  blockIdx.y: the first head.
-// 18,432 rows of 8 heads of 128 out of 4-bit pages: 19.9 us (97 MB, 4.9 TB/s); with 40 registers, six CTAs an SM, 23.5.
+// 18,432 rows of 8 heads of 128 out of 4-bit pages: 20.1 us (97 MB, 4.8 TB/s); with 40 registers, six CTAs an SM, 23.5.
 template <typename TO, typename T, int D, bool INT4>
 __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const __grid_constant__ RowArgs a) {
     let_next_start();
@@ -297,38 +298,57 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const __g
     const int64_t head_bytes = INT4 ? (int64_t)(a.c.page_size >> 4) * R::bytes : (int64_t)a.c.page_size * (4 * D);
     const uint8_t* from = reinterpret_cast<const uint8_t*>(a.c.pages) + ((good ? page : 0) * a.c.num_kv_heads + lane) * head_bytes +
                           (INT4 ? (off >> 4) * R::bytes : off * (2 * D));
-#pragma unroll 4   // the pages are read-only here: four heads' loads go out before the first is stored
-    for (int h = lane; h < a.c.num_kv_heads; h += a.lanes) {
-        float x[N], y[N];
-        if (!good) {
+    using Raw = typename std::conditional<INT4, typename std::conditional<N == 8, uint32_t, uint16_t>::type,
+                                          typename std::conditional<N == 8, uint4, uint2>::type>::type;
+    // Heads whose loads go out before the first is stored.  6,139 rows of 4 heads of 128 out of 4-bit and 16-bit pages: as fp32,
+    // half as many values a thread, 8.1 and 8.4 us with two, 8.6 and 9.2 with one; as bf16 5.9 and 12.2 (spills) against 5.7 and 6.7.
+    constexpr int U = sizeof(TO) == 4 ? 2 : 1;
+    const int k_at = INT4 ? R::k_codes + r * (D / 2) : 0, v_at = INT4 ? R::v_codes + r * (D / 2) : a.c.page_size * (2 * D);
+    const int64_t next = a.lanes * head_bytes, next_k = a.lanes * a.k_head, next_v = a.lanes * a.v_head;
+    for (int h = lane; h < a.c.num_kv_heads; h += U * a.lanes) {
+        Raw kr[U], vr[U];
+        uint8_t ks[U], vs[U];
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = y[j] = __int_as_float(0x7FC00000);
-        } else if (INT4) {
-            using Codes = typename std::conditional<N == 8, uint32_t, uint16_t>::type;
-            const Codes kc = __ldg(reinterpret_cast<const Codes*>(from + R::k_codes + r * (D / 2)) + chunk);
-            const Codes vc = __ldg(reinterpret_cast<const Codes*>(from + R::v_codes + r * (D / 2)) + chunk);
-            const uint8_t ks = __ldg(from + R::k_scales + r * (D / 16) + block), vs = __ldg(from + R::v_scales + block * 16 + r);
-            expand<N>(kc, ks, a.c.k_gain ? __ldg(a.c.k_gain + h) : 1.0f, x);
-            expand<N>(vc, vs, a.c.v_gain ? __ldg(a.c.v_gain + h) : 1.0f, y);
-        } else {
-            using Raw = typename std::conditional<N == 8, uint4, uint2>::type;
-            union {
-                Raw u;
-                T e[N];
-            } kr, vr;
-            kr.u = __ldg(reinterpret_cast<const Raw*>(from) + chunk);
-            vr.u = __ldg(reinterpret_cast<const Raw*>(from + (int64_t)a.c.page_size * (2 * D)) + chunk);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                x[j] = to_float(kr.e[j]);
-                y[j] = to_float(vr.e[j]);
+        for (int u = 0; u < U; ++u) {
+            if (!good || h + u * a.lanes >= a.c.num_kv_heads) break;
+            const uint8_t* at = from + u * next;
+            kr[u] = reinterpret_cast<const Raw*>(at + k_at)[chunk];
+            vr[u] = reinterpret_cast<const Raw*>(at + v_at)[chunk];
+            if (INT4) {
+                ks[u] = at[R::k_scales + r * (D / 16) + block];
+                vs[u] = at[R::v_scales + block * 16 + r];
             }
         }
-        *reinterpret_cast<uint4*>(k) = pack<TO>(x);
-        *reinterpret_cast<uint4*>(v) = pack<TO>(y);
-        from += a.lanes * head_bytes;
-        k += a.lanes * a.k_head;
-        v += a.lanes * a.v_head;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hu = h + u * a.lanes;
+            if (hu >= a.c.num_kv_heads) break;
+            float x[N], y[N];
+            if (!good) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) x[j] = y[j] = __int_as_float(0x7FC00000);
+            } else if constexpr (INT4) {
+                expand<N>(kr[u], ks[u], a.c.k_gain ? a.c.k_gain[hu] : 1.0f, x);
+                expand<N>(vr[u], vs[u], a.c.v_gain ? a.c.v_gain[hu] : 1.0f, y);
+            } else {
+                union {
+                    Raw u;
+                    T e[N];
+                } ke, ve;
+                ke.u = kr[u];
+                ve.u = vr[u];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    x[j] = to_float(ke.e[j]);
+                    y[j] = to_float(ve.e[j]);
+                }
+            }
+            *reinterpret_cast<uint4*>(k) = pack<TO>(x);
+            *reinterpret_cast<uint4*>(v) = pack<TO>(y);
+            k += next_k;
+            v += next_v;
+        }
+        from += U * next;
     }
 }
 

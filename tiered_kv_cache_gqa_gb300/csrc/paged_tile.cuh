@@ -502,7 +502,7 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (is_row) v = __ldg(reinterpret_cast<const uint4*>(x16 + (D / 4) * cq + 8 * w));
+                if (is_row) v = *reinterpret_cast<const uint4*>(x16 + (D / 4) * cq + 8 * w);
                 const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -529,8 +529,8 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
         } else {
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
-                q.set(nt, i, is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq)) : 0u,
-                      is_row ? __ldg(reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq + 8)) : 0u);
+                q.set(nt, i, is_row ? *reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq) : 0u,
+                      is_row ? *reinterpret_cast<const uint32_t*>(x16 + 16 * i + 2 * cq + 8) : 0u);
             }
             q.z0[nt] = q.z1[nt] = scale_log2;
         }

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<T, BYTES, INTERLEAVED>()) ro
         int p[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < a.num_axes) p[i] = __ldg(a.positions + i * a.axis_stride + row);
+            if (i < a.num_axes) p[i] = a.positions[i * a.axis_stride + row];
         load_angles<NP>(a, p, piece * NP, cs);
     }
     for (int h = blockIdx.y; h < a.heads; h += U * a.lanes) {
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_const
             continue;
         }
         bool bad = false;
-        const int p = __ldg(a.positions + (a.num_axes > 1 ? a.pair_axis[j] : 0) * a.axis_stride + row);
+        const int p = a.positions[(a.num_axes > 1 ? a.pair_axis[j] : 0) * a.axis_stride + row];
         const float2 cs = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
         if (bad) raise_status(a.status, TKV_EINVAL);
         const int i0 = a.interleaved ? 2 * j : j, i1 = a.interleaved ? 2 * j + 1 : j + a.pairs;
