@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import tiered_kv_cache_gqa_gb300 as tkv
-from test_gpu_paged import BF16, FP16, Pool, ints
+from test_gpu_paged import BF16, FP16, Pool, close, ints, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,21 @@ def test_steps_that_rewrite_what_the_last_ones_read(kind, dtype, lengths, max_le
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     lens = ints(lengths)
     assert torch.equal(p.lens, lens)
+
+
+@pytest.mark.parametrize("kind,dtype", [("bf16", BF16), ("fp16", FP16), ("int4", BF16)])
+@pytest.mark.parametrize("max_len", [256, 4000])
+def test_pages_that_are_missing_in_turn(kind, dtype, max_len):
+    """Every other page is none, where the ring's slots hold other tiles from before: each tile goes by its own flag."""
+    p = Pool(kind, [4000, 1500, 300], [1, 1, 2], d=64, page=16).fill()
+    p.pt[:, 1::2] = -1
+    p.pt[0, 40:44], p.pt[0, 101] = -1, p.num_pages
+    p.table.copy_(torch.tensor(p.pt))
+    q, status = queries(p, 4, dtype=dtype), ints([0])
+    want = p.oracle(q)
+    first = p.cache.attend(q, p.cu_t, max_len=max_len, return_lse=True, status=status)
+    assert status.item() == tkv.TKV_ECAPACITY
+    close(p, *first, want, dtype)
+    for _ in range(30):
+        got = p.cache.attend(q, p.cu_t, max_len=max_len, return_lse=True)
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])

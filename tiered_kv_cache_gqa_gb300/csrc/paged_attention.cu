@@ -393,7 +393,10 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                         }
                     }
                 } else {
-                    if (k == 0) sh.bad[w][st][0] = !ok;
+                    if (k == 0) {
+                        sh.bad[w][st][0] = !ok;
+                        mbar_arrive(bar);   // with this word: the arrivals behind the copies order nothing but the copies
+                    }
                     tile_to = to;
                     tile_bar = bar;
                     tile_rows = ok ? min(16, end - pos) : 0;      // those behind the end are not needed
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kWarps && lane < kWarps) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&sh.full[lane][s]), KIND == kInt4 ? 2 : 32);   // the lanes that bring a tile
+            mbar_init(smem_u32(&sh.full[lane][s]), KIND == kInt4 ? 2 : 33);   // the lanes that bring a tile; 16 bits: and the one that says if there is a page
             mbar_init(smem_u32(&sh.empty[lane][s]), 1);
         }
         for (int s = 0; s < C::queue; ++s) mbar_init(smem_u32(&sh.known[lane][s]), 1);
