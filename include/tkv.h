@@ -392,7 +392,8 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  *     is position lengths[b] - n_b + i, n_b = cu_tokens[b + 1] - cu_tokens[b].
  *     `rows` is the extent of the tensors; rows behind cu_tokens[batch] are
  *     left as they were (a captured step can be padded).  lengths counts the
- *     step's own tokens, so one array serves append and attention.
+ *     step's own tokens, so one array serves append and attention.  Both launches
+ *     of an attention read lengths and cu_tokens.
  *   - Strides count elements; the channels of a head are contiguous.  Inputs
  *     may be broadcast (stride 0); the elements of an output may not overlap.
  *   - The device arrays (positions, page table, lengths, cu_tokens) cannot be

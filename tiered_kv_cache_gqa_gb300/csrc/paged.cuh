@@ -136,7 +136,8 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* cu, int batch, int
 // The operators' kernels start while the kernel before them in the stream ends (programmatic launches): each reads and writes
 // memory only behind wait_for_previous, which lasts until the kernel before it is done and its writes can be seen.  A
 // kernel that calls let_next_start first lets its successor start although its predecessor still runs: the successor
-// then may not read anything before its own wait.
+// then may not read anything before its own wait.  One kernel does: the one that joins an attention's pieces reads lengths and
+// cu_tokens early, so the attention's main kernel lets it start only behind its own wait.
 // Every load is an ordinary one.  The read-only path (__ldg, ld.global.nc) is for memory that nothing writes while the kernel
 // exists, and these kernels exist before what precedes them has finished: the wait does not hold such a load back, nor does
 // it renew a line that the SM read through that path for a kernel still running when this one came.
