@@ -97,6 +97,12 @@ struct Seq {
     int first_row, n, len, full, lo, units, tiles;
 };
 
+// The first position that a query at `position` sees.  In 64 bits: the position may be negative (more queries than positions)
+// and the window as large as an int.
+__device__ __forceinline__ int window_begin(const PagedAttnArgs& a, int position) {
+    return a.window > 0 ? (int)max((int64_t)0, (int64_t)position - a.window + 1) : 0;
+}
+
 // EARLY: in the joining kernel, before its wait.  What precedes the main kernel in the stream is done by then (the main kernel
 // lets the joining one start behind its own wait), and reads from L2 find what it wrote there.
 template <int R, int TP, bool EARLY = false>
@@ -108,7 +114,7 @@ __device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
     s.n = (c0 < 0 || c1 < c0 || c1 > a.rows) ? -1 : c1 - c0;
     s.len = min(s.full, a.c.max_pages << a.page_shift);
     s.lo = 0;
-    if (a.window > 0) s.lo = max(0, min(s.len, s.full - s.n - a.window + 1)) & ~31;
+    if (a.window > 0) s.lo = min(s.len, window_begin(a, s.full - s.n)) & ~31;
     s.units = max(1, (s.len - s.lo + TP - 1) / TP);   // a row that sees nothing is written too
     s.tiles = s.n > 0 ? (int)(((int64_t)s.n * a.group + R - 1) / R) : 0;
     return s;
@@ -351,8 +357,8 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 const int t_hi = query_of(min(p.rows.seq_rows, p.rows.row0 + R) - 1, a.group, a.group_mul);
                 p.rows.all_until = min(s.len, p.rows.last0 + t_lo + 1);
                 p.rows.any_until = min(s.len, p.rows.last0 + t_hi + 1);
-                p.rows.all_from = a.window > 0 ? p.rows.last0 + t_hi - a.window + 1 : 0;
-                p.rows.any_from = a.window > 0 ? p.rows.last0 + t_lo - a.window + 1 : 0;
+                p.rows.all_from = window_begin(a, p.rows.last0 + t_hi);
+                p.rows.any_from = window_begin(a, p.rows.last0 + t_lo);
                 p.begin = s.lo + unit * TP;
                 p.tiles = min(s.units - unit, left);
                 p.flags = kValid | (unit ? kContinues : 0) | (unit + p.tiles == s.units ? kEnds : 0);

@@ -385,10 +385,11 @@ __device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int to = rows.last0 + query_of(rows.row0 + nt * 8 + 2 * cq + c, group, mul);   // the last position that this row sees
+                    const int before = to >= 0 ? to - window : 0;   // and the one before its window (with to < 0 it sees nothing)
 #pragma unroll
                     for (int e = c; e < 4; e += 2) {
                         const int p = p0 + 16 * g + slot_position<KIND>(r) + (e >> 1) * 8;
-                        if (!here || p >= rows.len || p > to || (window > 0 && p <= to - window)) z[g][nt][e] = -INFINITY;
+                        if (!here || p >= rows.len || p > to || (window > 0 && p <= before)) z[g][nt][e] = -INFINITY;
                     }
                 }
             // the others may hold anything: their V is taken as 0
