@@ -402,7 +402,9 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  *     reported in `status`: a device int32 that the caller clears (or NULL),
  *     raised to TKV_EINVAL (a position outside the rotary table; in the attention
  *     a sequence whose cu_tokens descend or leave the rows), TKV_ECAPACITY
- *     (a page or a position outside the cache) or TKV_ETIMEOUT, the largest. */
+ *     (a page or a position outside the cache) or TKV_ETIMEOUT (in the attention a
+ *     wait for a copy of the kernel's own ran out: the rows that it was for are NaN),
+ *     the largest.  With NULL none of them is reported. */
 
 /* Element types.  TKV_INT4 is a type of pages only. */
 enum { TKV_BF16 = 0, TKV_FP16 = 1, TKV_FP32 = 2, TKV_INT4 = 3 };

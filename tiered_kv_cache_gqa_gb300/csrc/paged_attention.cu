@@ -14,6 +14,8 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <type_traits>
 
 #include "paged_tile.cuh"
@@ -31,7 +33,7 @@ constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, 
 // 64, 512 positions 19.1 and 16.0, 1,024 positions 27.0 and 25.5, 4,096 positions 65.0 and 68.9; d 64, batch 67 with a
 // window of 700 positions, 16.2 and 20.3.
 constexpr int kWholeShort = 256, kWholeMany = 512;
-constexpr int kSpinLimit = 1 << 18;     // tries of a wait
+constexpr int kSpinLimit = 1 << 18;     // tries of a wait; 1.5 us each where nothing comes, so 0.4 s
 constexpr double kLog2E = 1.4426950408889634;
 
 struct PagedAttnArgs {
@@ -45,6 +47,7 @@ struct PagedAttnArgs {
     int64_t rows, q_row, q_head, out_row, out_head;
     int hq, group, window, page_shift, grid, whole_items, q_fp16;
     uint32_t group_mul;                  // floor((2^32 - 1) / group)
+    int give_up;                         // this computing warp of the grid behaves as if its first wait had run out; -1: none
     float scale_log2;
 };
 
@@ -211,7 +214,8 @@ struct Piece {
     Rows rows;
     int begin, tiles, flags;
 };
-enum { kContinues = 1, kEnds = 2, kValid = 4, kHead = 8 };   // begins within the item; reaches its end; exists; there was an earlier, cut one
+// begins within the item; reaches its end; exists; there was an earlier, cut one; a wait ran out
+enum { kContinues = 1, kEnds = 2, kValid = 4, kHead = 8, kFailed = 16 };
 
 template <int D, int NT, int KIND>
 struct Shared {
@@ -226,6 +230,7 @@ struct Shared {
     int sums[kWarps + 1];
     Where where[kWarps], ends[2];
     int flags[kWarps], last[kWarps];    // of each warp's last piece, and its place in the queue
+    int stopped[kWarps], issued[kWarps];   // the warp takes no more tiles; tiles that were brought for it
     uint8_t bad[kWarps][C::stages][2];  // records of a stage that have no page
     uint2 q[kWarps][Query<D, NT>::words];
 };
@@ -328,7 +333,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     int tiles = 0, pos = 0, end = 0, pieces = 0, page = -2;
     const int32_t* table = nullptr;
     const uint8_t* pages = nullptr;
-    int st = 0, parity = 0, spins = 0;
+    int st = 0, parity = 0, spins = 0, issued = 0;
     bool first = true;   // the ring's first round: nothing to wait for
     auto look_up = [&]() {   // a 4-bit tile has two records, which may lie in two pages
         const int p = pos + (KIND == kInt4 ? (k & 1) * 16 : 0);
@@ -386,6 +391,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
             }
             if (first || mbar_test(empty0 + 8 * st, parity)) {
                 moved = true;
+                ++issued;
                 const bool ok = page >= 0 && page < a.c.num_pages;
                 const uint32_t bar = full0 + 8 * st, to = ring + st * T::bytes;
                 if (!ok && page != -2) raise_status(a.status, TKV_ECAPACITY);
@@ -419,6 +425,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 if (--tiles > 0) look_up();
             }
             spins = moved ? 0 : spins + 1;
+            if (!moved && *(volatile int*)&sh.stopped[w]) left = tiles = 0;
         }
         uint32_t groups = __ballot_sync(0xffffffffu, moved);
         if (groups == 0) __nanosleep(32);
@@ -444,6 +451,46 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
         }
     }
     if (spins >= kSpinLimit) raise_status(a.status, TKV_ETIMEOUT);
+    issued = max(issued, __shfl_xor_sync(0xffffffffu, issued, 1));   // of both lanes that bring records
+    if (k == 0 && lane >> 2 < kWarps) sh.issued[w] = issued;
+}
+
+// ------------------------------------------------------------------ a wait that ran out
+// Every row that this CTA (tiles u0 .. u1 of the deal) has a part in becomes NaN: items that lie in it whole at once, those cut
+// at its begin or end through its two records, which the joining kernel reads whatever happened here.
+template <int D, int NT, int KIND>
+__device__ __forceinline__ void fail_rows(const PagedAttnArgs& a, const Where& from, int u0, int u1) {
+    constexpr int R = 8 * NT, TP = TileOf<D, KIND>::positions;
+    const int tid = threadIdx.x;
+    if (tid < 8 * NT)
+        a.part[((int64_t)blockIdx.x * 2 + tid / (4 * NT)) * Rec4<D, NT>::size + Rec4<D, NT>::sums + tid % (4 * NT)] = make_float4(kLowest, NAN, kLowest, NAN);
+    int b = from.b, in_seq = from.in_seq;
+    Seq s = sequence<R, TP>(a, b);
+#pragma unroll 1
+    for (int u = u0; u < u1;) {
+        const int item = in_seq / s.units, c = in_seq - item * s.units, rest = s.units - c;
+        if (c == 0 && u + rest <= u1) {
+            Rows rows{};
+            rows.h = item / s.tiles;
+            rows.row0 = (item - rows.h * s.tiles) * R;
+            rows.first_row = s.first_row;
+            rows.seq_rows = s.n * a.group;
+#pragma unroll 1
+            for (int i = tid; i < R * (D / 8); i += kThreads) {
+                float* lse;
+                uint16_t* to = out_row(a, rows, i / (D / 8), &lse);
+                if (!to) continue;
+                reinterpret_cast<uint4*>(to)[i % (D / 8)] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);   // in both types
+                if (lse) *lse = NAN;
+            }
+        }
+        u += rest;
+        in_seq += rest;
+        if (in_seq == weight(a, s)) {
+            in_seq = 0;
+            while (u < u1 && (s = sequence<R, TP>(a, ++b)).tiles == 0) {}   // below u1 there is a next one
+        }
+    }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -461,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             mbar_init(smem_u32(&sh.empty[lane][s]), 1);
         }
         for (int s = 0; s < C::queue; ++s) mbar_init(smem_u32(&sh.known[lane][s]), 1);
+        sh.stopped[lane] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
@@ -510,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 #pragma unroll 1
         while (left > 0 && !failed) {
             const int place = taken & (C::queue - 1);
-            failed = __any_sync(0xffffffffu, !mbar_wait(smem_u32(&sh.known[warp][place]), (taken / C::queue) & 1));
+            failed = __any_sync(0xffffffffu, (int)blockIdx.x * kWarps + warp == a.give_up || !mbar_wait(smem_u32(&sh.known[warp][place]), (taken / C::queue) & 1));
             if (failed) break;
             const Piece& piece = sh.queue[warp][place];   // stays where it is: its place is taken again much later
             ++taken;
@@ -598,15 +646,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 }
             }
         }
-        if (failed) {
-            // A copy did not come in time: the status says so, the piece's rows are NaN and what follows stays unwritten;
-            // what may still be in flight is given as long again.
-            if (lane == 0) raise_status(a.status, TKV_ETIMEOUT);
-            for (int s = 0; s < S; ++s) mbar_wait(full0 + 8 * (stage + s < S ? stage + s : stage + s - S), parity ^ (stage + s >= S));
-            sums.clear();
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sums.l[nt][0] = sums.l[nt][1] = NAN;
-            flags |= taken ? sh.queue[warp][(taken - 1) & (C::queue - 1)].flags : 0;
+        if (failed) {   // a copy did not come in time
+            flags = kFailed;
+            if (lane == 0) {
+                *(volatile int*)&sh.stopped[warp] = 1;
+                raise_status(a.status, TKV_ETIMEOUT);
+            }
         }
         if (lane == 0) {
             sh.flags[warp] = flags;
@@ -616,6 +661,15 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 
     // -------------------------------------------------------- join the warps' last pieces
     __syncthreads();   // every warp is done with its ring
+    const int f = lane < kWarps ? sh.flags[lane] : 0;
+    if (__any_sync(0xffffffffu, f & kFailed)) {
+        // no copy may be under way when the CTA ends; the ring's last round, of which each warp's tiles have come or will
+        if (warp < kWarps)
+            for (int i = max(0, sh.issued[warp] - S); i < sh.issued[warp]; ++i) mbar_wait(smem_u32(&sh.full[warp][i % S]), (i / S) & 1);
+        __syncthreads();
+        fail_rows<D, NT, KIND>(a, sh.where[0], u0, u1);
+        return;
+    }
     if (taken) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -629,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     __syncthreads();
     // A warp's piece that is the first of its item here leads; the warps behind it that hold nothing else follow, and the
     // record of the one in which the item ended.
-    const int f = lane < kWarps ? sh.flags[lane] : 0;
     const uint32_t valid = __ballot_sync(0xffffffffu, f & kValid), continues = __ballot_sync(0xffffffffu, f & kContinues);
     const uint32_t ends = __ballot_sync(0xffffffffu, f & kEnds), heads = __ballot_sync(0xffffffffu, f & kHead);
     const uint32_t leads = valid & ~(continues & ~1u);
@@ -791,6 +844,14 @@ bool rows_of_32(const PagedAttnArgs& a, int max_new, int64_t sight, int sms) {
     return tiles >= (a.c.head_dim == 64 ? 18.0 : 45.0) * kWarps * sms;
 }
 
+// TKV_FAULT_INJECT=wait:N: computing warp N of every attention's grid gives up at its first wait, as if a copy had not come.
+// A process that starts without the variable never looks at it again.
+int warp_that_gives_up() {
+    static const bool injects = std::getenv("TKV_FAULT_INJECT") != nullptr;
+    const char* what = injects ? std::getenv("TKV_FAULT_INJECT") : nullptr;
+    return what && !std::strncmp(what, "wait:", 5) ? std::atoi(what + 5) : -1;
+}
+
 cudaError_t device_sms(int* sms, int* dev) {
     const cudaError_t e = cudaGetDevice(dev);
     return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) : e;
@@ -887,6 +948,7 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     a.hq = num_q_heads;
     a.group = num_q_heads / cache->num_kv_heads;
     a.group_mul = 0xFFFFFFFFu / (uint32_t)a.group;
+    a.give_up = warp_that_gives_up();
     a.window = window;
     a.page_shift = __builtin_ctz((unsigned)cache->page_size);
     const int64_t sight = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + max_new) : max_len;

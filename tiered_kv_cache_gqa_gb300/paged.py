@@ -195,7 +195,8 @@ class PagedCache:
     k_gain, v_gain  fp32 [Hkv] > 0, 4 bits only: a value is code * scale * gain (1 if None)
 
     A step is ragged: rows cu_tokens[b] .. cu_tokens[b + 1] of k, v, q are the last positions of sequence b (cu_tokens
-    int32 [batch + 1]).  `status` (an int32 tensor that the caller clears) is raised where a row or page has no place."""
+    int32 [batch + 1]).  `status` (an int32 tensor that the caller clears) is raised where a row or page has no place, or a
+    kernel's wait ran out; without it nothing reports what the device finds wrong."""
 
     def __init__(self, pages, page_table, lengths, k_gain=None, v_gain=None):
         torch, w = _types(), "PagedCache"
