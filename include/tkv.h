@@ -458,7 +458,7 @@ typedef struct {
     int32_t max_pages;          /* pages a sequence; max_pages * page_size <= 2^30 */
 } tkv_paged;
 
-/* Rotates x into out, which may be x itself (same strides).
+/* Rotates x into out, which may be x itself (same strides) and may not overlap it otherwise.
  * x, out: device [rows][heads][head_dim] of dtype (TKV_BF16, TKV_FP16 or
  * TKV_FP32), rows up to 2^31 - 1, any strides that keep out's elements apart; channels behind the
  * rotated ones are copied.  Computed in fp32, rounded once.  Fastest

@@ -19,13 +19,13 @@ import threading
 from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_OK, PagedDesc, RotaryDesc, TkvError,
                load)
 
-_torch = _raw_stream = _current_device = _capturing = _int32 = None
+_torch = _raw_stream = _current_device = _capturing = _int32 = _grad_enabled = _written = _turn = None
 _DTYPES = {}
 
 
 def _types():
     """torch, imported at the first use (the package itself does not need it)."""
-    global _torch, _raw_stream, _current_device, _capturing, _int32
+    global _torch, _raw_stream, _current_device, _capturing, _int32, _grad_enabled, _written, _turn
     if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: TKV_BF16, torch.float16: TKV_FP16, torch.float32: TKV_FP32})
@@ -33,6 +33,30 @@ def _types():
         # the handle of a device's current stream and the current device, without an object around them
         _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         _capturing = torch._C._cuda_isCurrentStreamCapturing
+        # of tensors that a kernel writes for the caller: autograd notices if it had kept them for a backward pass
+        _grad_enabled, _written = torch.is_grad_enabled, torch.autograd.graph.increment_version
+
+        class Turn(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, out, in_place, rotary, positions, inverse, status):
+                y = _rope(x, rotary, positions, x if in_place else out, inverse, status)
+                ctx.rotary, ctx.inverse = rotary, inverse
+                ctx.save_for_backward(positions, rotary.table)   # a change of either before the backward pass is an error
+                if in_place or out is not None:
+                    ctx.mark_dirty(y)
+                return y
+
+            @staticmethod
+            def backward(ctx, grad):
+                positions, _ = ctx.saved_tensors
+                if ctx.needs_input_grad[0]:
+                    grad = grad if grad.shape[2] <= 1 or grad.stride(2) == 1 else grad.contiguous()
+                    grad = rope(grad, ctx.rotary, positions, inverse=not ctx.inverse)
+                else:
+                    grad = None
+                return grad, None, None, None, None, None, None   # what out held before does not matter
+
+        _turn = Turn.apply
         _torch = torch
     return _torch
 
@@ -156,10 +180,21 @@ class Rotary:
 def rope(x, rotary, positions, out=None, inverse=False, status=None):
     """x [rows, heads, head_dim] (bf16, fp16 or fp32, channels contiguous) with its first 2 * pairs channels rotated.
 
-    positions: int32 [rows] or [axes, rows].  out: a tensor like x, or x itself; a new one if None.
-    inverse=True turns back: the gradient with respect to x of a call is rope(grad, ..., inverse=True)."""
-    w = "rope"
-    torch = _types()
+    positions: int32 [rows] or [axes, rows].  out: a tensor like x that does not overlap it, or x itself; a new one if None.
+    inverse=True turns back.  Autograd differentiates the call, with respect to x and any number of times: the gradient is
+    rope(grad, ..., inverse=not inverse).  As with torch's own operators, a backward pass that is captured into a CUDA graph
+    wants its forward pass captured with it, and leaves of which no eager graph is alive."""
+    _types()
+    if _grad_enabled() and (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)):
+        return _turn(x, None if out is x else out, out is x, rotary, positions, inverse, status)
+    y = _rope(x, rotary, positions, out, inverse, status)
+    if out is not None:
+        _written(out)
+    return y
+
+
+def _rope(x, rotary, positions, out, inverse, status):
+    w, torch = "rope", _torch
     _on(x, w, "x", None, 3)
     dt = _DTYPES.get(x.dtype)
     if dt is None:
@@ -177,7 +212,7 @@ def rope(x, rotary, positions, out=None, inverse=False, status=None):
         if out.shape != shape:
             _refuse(w, "out is %s, x is %s" % (list(out.shape), list(shape)))
     os_ = out.stride()
-    if d > 1 and (xs[2] != 1 or os_[2] != 1):
+    if rows and d > 1 and (xs[2] != 1 or os_[2] != 1):
         _refuse(w, "the channels of x and out have to be contiguous")
     desc = rotary._desc(positions, rows, w, inverse)
     if rows:
