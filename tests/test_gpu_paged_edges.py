@@ -38,3 +38,18 @@ def test_windows_of_a_sequence_that_counts_more_positions_than_its_table(window)
             want = p.oracle(q[row:row + 1], 48 - first, cu=[0, 1, 1] if b == 0 else [0, 0, 1])
             p.lens.fill_(far)
             close(p, out[row:row + 1], lse[row:row + 1], want, BF16)
+
+
+def test_tensors_to_write_to_are_not_overwritten_unnoticed():
+    """out, lse, k and v that autograd keeps for a backward pass: the pass says that they have changed."""
+    p = Pool("int4", [40], [2], page=16).fill()
+    q = queries(p, 2)
+    out, lse = torch.randn_like(q), torch.randn(q.shape[:2], device="cuda")
+    k, v = (torch.randn(2, 2, 64, device="cuda") for _ in range(2))
+    for kept, call in ((out, lambda: p.cache.attend(q, p.cu_t, out=out)), (lse, lambda: p.cache.attend(q, p.cu_t, lse=lse)),
+                       (k, lambda: p.cache.gather(p.cu_t, 2, k=k, v=v)), (v, lambda: p.cache.gather(p.cu_t, 2, k=k, v=v))):
+        leaf = torch.ones_like(kept).requires_grad_()
+        y = (leaf * kept).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()

@@ -231,7 +231,8 @@ class PagedCache:
 
     A step is ragged: rows cu_tokens[b] .. cu_tokens[b + 1] of k, v, q are the last positions of sequence b (cu_tokens
     int32 [batch + 1]).  `status` (an int32 tensor that the caller clears) is raised where a row or page has no place, or a
-    kernel's wait ran out; without it nothing reports what the device finds wrong."""
+    kernel's wait ran out; without it nothing reports what the device finds wrong.  The calls have no gradients: their results
+    are not part of autograd's graphs, whatever k, v and q are."""
 
     def __init__(self, pages, page_table, lengths, k_gain=None, v_gain=None):
         torch, w = _types(), "PagedCache"
@@ -376,6 +377,7 @@ class PagedCache:
                 if x.shape != shape or x.dtype not in _DTYPES:
                     _refuse(w, "%s is not bf16, fp16 or fp32 %s" % (name, list(shape)))
                 self._pieces(x, w, name)
+            _written((k, v))
         c = self._c
         if lengths is not None:
             _is_int32(lengths, w, "lengths", (self.batch,), self.device)
@@ -417,10 +419,12 @@ class PagedCache:
             if out.shape != shape:
                 _refuse(w, "out is %s, q is %s" % (list(out.shape), list(shape)))
             self._pieces(out, w, "out")
+            _written(out)
         if lse is not None:
             _on(lse, w, "lse", torch.float32, 2, self.device)
             if lse.shape != (rows, hq) or not lse.is_contiguous():
                 _refuse(w, "lse is a contiguous [%d, %d]" % (rows, hq))
+            _written(lse)
         elif return_lse:
             lse = torch.empty((rows, hq), dtype=torch.float32, device=self.device)
         if rows:
