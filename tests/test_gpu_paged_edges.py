@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import tiered_kv_cache_gqa_gb300 as tkv
 from test_gpu_paged import BF16, FP16, Pool, close, queries
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,21 @@ def test_tensors_to_write_to_are_not_overwritten_unnoticed():
         call()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward()
+
+
+def test_caches_share_a_workspace():
+    """The layers of a model, one after the other on a stream: one workspace for all, as large as the largest call wants it."""
+    pools = [Pool("int4", [300 + 7 * i], [1 + i % 3], d=128, page=16, seed=i).fill() for i in range(8)]
+    q = [queries(p, 2 + i % 5, seed=i) for i, p in enumerate(pools)]
+    outs = [torch.empty_like(x) for x in q]
+    size = pools[0].cache._c
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        for p, x, o in zip(pools, q, outs):
+            p.cache.attend(x, p.cu_t, out=o, max_new=p.n[0])
+        kept = torch.cuda.memory_allocated() - before
+        torch.cuda.synchronize()
+    assert kept <= tkv.tkv_paged_attention_workspace(size, 12, 3) + (2 << 20)
+    for p, x, o in zip(pools, q, outs):
+        close(p, o, None, p.oracle(x), BF16)

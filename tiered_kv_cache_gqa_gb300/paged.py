@@ -1,9 +1,10 @@
 """The operators around a paged KV cache on torch tensors: rope, and PagedCache with append, attend, gather.
 
-Thin wrappers: they check the arguments, allocate outputs and workspaces with torch's allocator on the current
-stream of the tensors' device, and call the C functions of the same names (include/tkv.h), which say what is computed
-and what a kernel does with positions, pages and lengths that make no sense.  Everything runs on torch's current
-stream; nothing synchronises, and every call can be captured into a CUDA graph.
+Thin wrappers: they check the arguments, allocate outputs with torch's allocator on the current stream of the tensors'
+device, and call the C functions of the same names (include/tkv.h), which say what is computed and what a kernel does
+with positions, pages and lengths that make no sense.  An attention's workspace (12 to 23 MB at d 128) is kept by the
+thread for its next attentions on that stream.  Everything runs on torch's current stream; nothing synchronises, and
+every call can be captured into a CUDA graph.
 
     table  = rope_table(max_positions, 128)
     rotary = Rotary(table)
@@ -21,6 +22,7 @@ from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV
 
 _torch = _raw_stream = _current_device = _capturing = _int32 = _grad_enabled = _written = _turn = None
 _DTYPES = {}
+_own = threading.local()   # .work: the thread's workspaces of the attention, by device and stream
 
 
 def _types():
@@ -275,7 +277,7 @@ class PagedCache:
         self.batch, self.max_pages, self.is_int4 = c.batch, c.max_pages, c.kv_type == TKV_INT4
         # what each call reads of the descriptor, without a ctypes access
         self._c, self._kv_type, self._cu_shape, self._index = c, c.kv_type, (c.batch + 1,), pages.get_device()
-        self._sizes, self._own = {}, threading.local()   # of workspaces; a thread's workspaces, by stream
+        self._sizes = {}   # of workspaces
 
     @classmethod
     def empty(cls, num_pages, page_table, lengths, *, num_kv_heads, head_dim, page_size, dtype="int4", k_gain=None, v_gain=None):
@@ -313,8 +315,9 @@ class PagedCache:
     def _work(self, hq, max_new):
         """A workspace for an attention that is enqueued next on the current stream.
 
-        A thread keeps one a stream: what it enqueues there runs in order.  Other threads' launches may come between the
-        two of a call, so they have their own; so has a call that is captured, which may run beside any other later."""
+        A thread keeps one a stream, for all its caches: what it enqueues there runs in order.  Other threads' launches may
+        come between the two of a call, so they have their own; so has a call that is captured, which may run beside any
+        other later."""
         size = self._sizes.get((hq, max_new))
         if size is None:
             with _torch.cuda.device(self._index):
@@ -322,13 +325,13 @@ class PagedCache:
         if _current_device() != self._index or _capturing():
             return _torch.empty(size, dtype=_torch.uint8, device=self.device)
         try:
-            kept = self._own.work
+            kept = _own.work
         except AttributeError:
-            kept = self._own.work = {}
-        stream = _raw_stream(self._index)
-        work = kept.get(stream)
+            kept = _own.work = {}
+        key = self._index, _raw_stream(self._index)
+        work = kept.get(key)
         if work is None or work.numel() < size:
-            work = kept[stream] = _torch.empty(size, dtype=_torch.uint8, device=self.device)
+            work = kept[key] = _torch.empty(size, dtype=_torch.uint8, device=self.device)
         return work
 
     def append(self, k, v, cu_tokens, rotary=None, positions=None, status=None):
