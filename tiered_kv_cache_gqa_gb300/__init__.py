@@ -169,12 +169,15 @@ def _check(rc, where):
 
 
 def _ptr(x):
-    """Device pointer of a torch tensor, or an int address; None is NULL."""
-    if x is None:
-        return None
+    """Device pointer of a torch tensor, or an int address."""
     if hasattr(x, "data_ptr"):
         return ctypes.c_void_p(x.data_ptr())
     return ctypes.c_void_p(int(x))
+
+
+def _opt_ptr(x):
+    """_ptr of what the C call lets be NULL: None."""
+    return None if x is None else _ptr(x)
 
 
 # ------------------------------------------------------------ C-named calls
@@ -279,20 +282,20 @@ def tkv_measure_host_link(device, nbytes):
 
 def tkv_rope(rotary, x, out, dtype, rows, heads, head_dim, x_strides, out_strides, status=None, stream=None):
     """Rotary positions (see include/tkv.h): rotary a RotaryDesc, strides (row, head); returns the status."""
-    return load().tkv_rope(rotary, _ptr(x), _ptr(out), dtype, rows, heads, head_dim, *x_strides, *out_strides,
-                           _ptr(status), torch_stream_handle() if stream is None else stream)
+    return load().tkv_rope(rotary, _opt_ptr(x), _opt_ptr(out), dtype, rows, heads, head_dim, *x_strides, *out_strides,
+                           _opt_ptr(status), torch_stream_handle() if stream is None else stream)
 
 
 def tkv_paged_append(cache, rotary, k, v, dtype, rows, k_strides, v_strides, cu_tokens, status=None, stream=None):
     """Rows into a paged cache (see include/tkv.h): cache a PagedDesc, rotary a RotaryDesc or None; returns the status."""
-    return load().tkv_paged_append(cache, rotary, _ptr(k), _ptr(v), dtype, rows, *k_strides, *v_strides, _ptr(cu_tokens),
-                                   _ptr(status), torch_stream_handle() if stream is None else stream)
+    return load().tkv_paged_append(cache, rotary, _opt_ptr(k), _opt_ptr(v), dtype, rows, *k_strides, *v_strides, _opt_ptr(cu_tokens),
+                                   _opt_ptr(status), torch_stream_handle() if stream is None else stream)
 
 
 def tkv_paged_gather(cache, k, v, dtype, rows, k_strides, v_strides, cu_tokens, status=None, stream=None):
     """Rows out of a paged cache (see include/tkv.h); returns the status."""
-    return load().tkv_paged_gather(cache, _ptr(k), _ptr(v), dtype, rows, *k_strides, *v_strides, _ptr(cu_tokens),
-                                   _ptr(status), torch_stream_handle() if stream is None else stream)
+    return load().tkv_paged_gather(cache, _opt_ptr(k), _opt_ptr(v), dtype, rows, *k_strides, *v_strides, _opt_ptr(cu_tokens),
+                                   _opt_ptr(status), torch_stream_handle() if stream is None else stream)
 
 
 def tkv_paged_attention_workspace(cache, num_q_heads, max_new):
@@ -303,9 +306,9 @@ def tkv_paged_attention_workspace(cache, num_q_heads, max_new):
 def tkv_paged_attention(cache, q, out, lse, dtype, rows, num_q_heads, q_strides, out_strides, cu_tokens, max_new,
                         max_len, window, scale, workspace, workspace_bytes, status=None, stream=None):
     """Attention over a paged cache (see include/tkv.h); returns the status."""
-    return load().tkv_paged_attention(cache, _ptr(q), _ptr(out), _ptr(lse), dtype, rows, num_q_heads, *q_strides,
-                                      *out_strides, _ptr(cu_tokens), max_new, max_len, window, scale, _ptr(workspace),
-                                      workspace_bytes, _ptr(status), torch_stream_handle() if stream is None else stream)
+    return load().tkv_paged_attention(cache, _opt_ptr(q), _opt_ptr(out), _opt_ptr(lse), dtype, rows, num_q_heads, *q_strides,
+                                      *out_strides, _opt_ptr(cu_tokens), max_new, max_len, window, scale, _opt_ptr(workspace),
+                                      workspace_bytes, _opt_ptr(status), torch_stream_handle() if stream is None else stream)
 
 
 def tkv_sync(ctx):
