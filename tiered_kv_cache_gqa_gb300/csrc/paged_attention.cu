@@ -28,10 +28,14 @@ constexpr int kWarps = 7, kThreads = (kWarps + 1) * 32;   // warps that compute,
 constexpr int kCombineWarps = 8;
 constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, joining costs more than it brings
 // Up to these numbers of positions in sight a CTA takes whole items, and nothing is left to join: always; where the items
-// may be as many as the SMs.  One launch instead of two, but uneven shares.  Cut against whole, 8 KV heads of
-// d 128 in 4 bits: batch 1, 256 positions 8.3 and 7.3 us, 512 positions 8.3 and 9.0, 1,024 positions 8.5 and 11.0; batch
-// 64, 512 positions 19.1 and 16.0, 1,024 positions 27.0 and 25.5, 4,096 positions 65.0 and 68.9; d 64, batch 67 with a
-// window of 700 positions, 16.2 and 20.3.
+// may be as many as the SMs and the pages are of 4 bits.  One launch instead of two, but uneven shares.  Whole and cut, us, 8 KV
+// heads, groups of 4:
+//   4 bits, d 128: batch 1, 256 positions 6.9 and 8.1, 512 positions 8.7 and 8.3; batch 8, 512 positions 10.5 and 9.9; batch 64,
+//     256 positions 11.8 and 13.7, 512 positions 16.7 and 19.7, 1,024 positions 25.2 and 26.5
+//   4 bits, d 64: batch 1, 256 positions 6.2 and 7.1; batch 64, 512 positions 11.7 and 13.5, 1,024 positions 18.1 and 18.9; but
+//     batch 67 of mixed lengths with a window of 700 positions 20.3 and 16.2, so not beyond 512
+//   bf16, d 128: batch 1, 64 positions 5.5 and 9.0, 256 positions 7.6 and 7.6; batch 64, 256 positions 20.0 and 20.4, 512 positions
+//     33.1 and 32.3; d 64: batch 64, 256 positions 15.8 and 16.0, 512 positions 24.6 and 23.7
 constexpr int kWholeShort = 256, kWholeMany = 512;
 constexpr int kSpinLimit = 1 << 18;     // tries of a wait; 1.5 us each where nothing comes, so 0.4 s
 constexpr double kLog2E = 1.4426950408889634;
@@ -959,7 +963,7 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = rows_of_32(a, max_new, sight, sms) ? 4 : row_tiles(a.group, max_new);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
-    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms);
+    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && cache->kv_type == TKV_INT4);
     const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
     e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
