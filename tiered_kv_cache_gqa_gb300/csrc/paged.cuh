@@ -24,8 +24,6 @@
 
 namespace tkv {
 
-constexpr int kGroup = 16;   // positions of a record, channels of a block
-
 template <int D>
 struct Record {
     static constexpr int k_codes = 0, k_scales = 8 * D, v_codes = 9 * D, v_scales = 17 * D, bytes = 18 * D;
