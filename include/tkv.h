@@ -485,7 +485,8 @@ tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary* rotary, co
 /* The reverse: reads positions out of the pages into k and v, addressed like an
  * append (lengths[b] = the end of the range, n_b its extent).
  * k, v: device [rows][Hkv][d] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, 16-byte
- * aligned, strides multiples of 16 bytes; the values are rounded once.  A row
+ * aligned, strides multiples of 16 bytes; a 4-bit value is rounded to fp32, and
+ * every value from there to dtype.  A row
  * without a place (see the append) reads as NaN and raises status.
  * Errors: TKV_EINVAL, TKV_ECUDA. */
 tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dtype, int64_t rows,

@@ -842,7 +842,8 @@ int row_tiles(int group, int max_new) { return (int64_t)group * max_new > 8 ? 2 
 // Tiles of 32 rows of 4-bit pages do that once more, but the code is long and the joining heavy: worth it from so many tiles a
 // computing warp on, by the host's estimate.  30 rows a KV head, 8 x 8 heads of 64: 36.3 us with 16 rows and 37.3 with 32 at
 // 8,192 positions (15 tiles a warp), 65.7 and 58.4 at 16,384, 244 and 170 at 65,536; of 128: 90.0 and 93.1 at 16,384 (31
-// tiles), 163.5 and 156.2 at 32,768, 307 and 276 at 65,536.
+// tiles), 163.5 and 156.2 at 32,768, 307 and 276 at 65,536.  Measured on sequences of one length; the rule takes every
+// sequence to have max_new queries, so a ragged step may get the longer code for less than it is worth.
 bool rows_of_32(const PagedAttnArgs& a, int max_new, int64_t sight, int sms) {
     const int64_t rows = (int64_t)a.group * max_new;
     if (a.c.kv_type != TKV_INT4 || rows <= 16) return false;

@@ -164,8 +164,9 @@ __device__ __forceinline__ void put(float (&x)[8], float (&y)[8], bool two, uint
 
 // blockIdx.y: the first head.  The threads of a row are an even number, so neighbours share its place.  K and V of a head
 // one after the other, the next head's values on their way meanwhile: 64 registers, so four CTAs an SM, which cost a
-// few spills and were worth it (18,432 rows of 8 heads of 128 into 4-bit pages: 28.5 us, 97 MB, 3.4 TB/s; three CTAs 34.5;
-// both at once with three CTAs 32.4).  What bounds it there is instructions, about 75 for 8 values, issued in half the cycles.
+// few spills and were worth it (18,432 rows of 8 heads of 128 into 4-bit pages: 27.3 us, 97 MB, 3.6 TB/s; three CTAs 34.5;
+// both at once with three CTAs 32.4).  No unit is at its limit there: about 75 instructions for 8 values are issued in 64 % of
+// the cycles, DRAM is busy for 36 %, 42 % of the warps there could be are there, and they wait for memory and for one another.
 template <typename T, int D, bool INT4, int TURN>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(const __grid_constant__ RowArgs a) {
     let_next_start();

@@ -8,7 +8,8 @@
 // number that the maximum has not passed by more than kTop (in powers of two): p stays within fp16's range, the
 // common tile needs no exchange between lanes, and O is rescaled only where that room is used up.
 // Transposed like this, a group of 8 heads fills the 8 columns of mma.m16n8k16 with nothing wasted; the operation is
-// bound by memory (at 8 heads and 4 bits, 28 operations a byte), so mma.sync is enough for it.
+// bound by memory there (at 8 heads and 4 bits, 28 operations a byte), so mma.sync is enough for it.  With more rows it is not:
+// the tiles of 16 or 32 rows are held up by expanding the codes again for each and by O in registers.
 //
 // 4 bits to fp16, exactly.  (w & 0x000F000F) | 0x64006400 is the pair (1024 + n, 1024 + n') of two codes n = q + 8, and
 // (w & 0x00F000F0) | 0x54005400 the pair (64 + n, 64 + n'); one fused multiply-add with s = scale / 16 gives

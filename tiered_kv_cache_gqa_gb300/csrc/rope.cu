@@ -48,8 +48,8 @@ struct RopeArgs {
 };
 
 // Pieces of BYTES bytes, E elements: 16 bytes where everything allows it, fewer where alignments or numbers of pairs do not
-// (16,000 rows of 16 heads of 74 in bf16, pairs 37 apart, in 2-byte pieces: 20 us, 76 MB; one head at a time 31, a pair a
-// thread 74).  Pieces of a head: with halves, piece i takes channels [i E, i E + E) and their partners `pairs` further on;
+// (16,000 rows of 16 heads of 74 in bf16, pairs 37 apart, in 2-byte pieces: 20 us, 76 MB, 3.8 TB/s, eight times the loads and
+// stores of 16-byte pieces; one head at a time 31, a pair a thread 74).  Pieces of a head: with halves, piece i takes channels [i E, i E + E) and their partners `pairs` further on;
 // with adjacent pairs, its own E / 2 pairs.  Behind the rotated pieces come the copied ones.  A block holds kThreads /
 // pieces rows; blockIdx.y is the first head.  16,384 rows of 64 heads of 128 in bf16, three axes: 89 us (545 MB, 6.1 TB/s).
 template <typename T, int BYTES, bool INTERLEAVED>
