@@ -89,6 +89,32 @@ def test_in_place_and_into_a_tensor():
     assert y is into and y.requires_grad
     y.backward(w)
     assert torch.equal(leaf.grad, tkv.rope(w, rot, pos, inverse=True))
+    leaf = x.clone().requires_grad_()
+    behind = x.clone().requires_grad_()
+    wide = torch.cat([behind[:, :1], behind, behind[:, :1]], dim=1)   # a part of a larger tensor, which autograd then follows
+    tkv.rope(leaf, rot, pos, out=wide[:, 1:-1])
+    u = torch.randn_like(wide)
+    (wide * 3.0).backward(u)
+    assert torch.equal(leaf.grad, tkv.rope(u[:, 1:-1] * 3.0, rot, pos, inverse=True))
+    want = torch.zeros_like(x)                                  # what lay in that part before has no gradient
+    want[:, 0] = (u[:, 0] + u[:, -1]) * 3.0
+    assert torch.allclose(behind.grad, want, rtol=0, atol=6 * 8 * 2.0 ** -23)
+    leaf = x.clone().requires_grad_()
+    wide = torch.cat([leaf[:, :1], leaf * 2.0], dim=1)
+    part = wide[:, 1:]
+    assert tkv.rope(part, rot, pos, out=part) is part           # a part in place
+    u = torch.randn_like(wide)
+    wide.backward(u)
+    want = tkv.rope(u[:, 1:].contiguous(), rot, pos, inverse=True) * 2.0
+    want[:, 0] += u[:, 0]
+    assert torch.allclose(leaf.grad, want, rtol=0, atol=3 * 16 * 2.0 ** -23)
+    leaf = x.clone().requires_grad_()
+    both = leaf * 2.0
+    tkv.rope(both[:, :3], rot, pos, out=both[:, :3])            # two views of the same part
+    both.backward(w)
+    want = torch.cat([tkv.rope(w[:, :3].contiguous(), rot, pos, inverse=True), w[:, 3:]], dim=1) * 2.0
+    assert torch.equal(leaf.grad, want)
+    leaf = x.clone().requires_grad_()
     with pytest.raises(RuntimeError):                           # a leaf cannot be overwritten
         tkv.rope(leaf, rot, pos, out=leaf)
     with torch.no_grad():                                       # the user's own business here
@@ -129,7 +155,8 @@ def test_refusals_under_autograd():
     x, _, rot, pos, _ = case(FP32)
     x.requires_grad_()
     for call in (lambda: tkv.rope(x, rot, None), lambda: tkv.rope(x, rot, pos[:1]), lambda: tkv.rope(x.transpose(1, 2), rot, pos),
-                 lambda: tkv.rope(x, rot, pos, out=torch.empty(1, device="cuda")), lambda: tkv.rope(x.double(), rot, pos), lambda: tkv.rope(x.cpu(), rot, pos)):
+                 lambda: tkv.rope(x, rot, pos, out=torch.empty(1, device="cuda")), lambda: tkv.rope(x.double(), rot, pos), lambda: tkv.rope(x.cpu(), rot, pos),
+                 lambda: tkv.rope(None, rot, pos, out=x)):
         with pytest.raises(tkv.TkvError) as e:
             call()
         assert e.value.status == tkv.TKV_EINVAL

@@ -40,23 +40,29 @@ def _types():
 
         class Turn(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, out, in_place, rotary, positions, inverse, status):
-                y = _rope(x, rotary, positions, x if in_place else out, inverse, status)
-                ctx.rotary, ctx.inverse = rotary, inverse
+            def forward(ctx, to, x, rotary, positions, inverse, status):
+                """Turns x into `to` (a new tensor if None), or `to` in place if x is None.  What is written comes first:
+                where it is a view, autograd takes the first gradient for what the view held before."""
+                y = _rope(to if x is None else x, rotary, positions, to, inverse, status)
+                ctx.rotary, ctx.inverse, ctx.in_place = rotary, inverse, x is None
                 ctx.save_for_backward(positions, rotary.table)   # a change of either before the backward pass is an error
-                if in_place or out is not None:
+                if to is not None:
                     ctx.mark_dirty(y)
                 return y
 
             @staticmethod
             def backward(ctx, grad):
                 positions, _ = ctx.saved_tensors
-                if ctx.needs_input_grad[0]:
+                before = None
+                if not ctx.in_place and ctx.needs_input_grad[0]:
+                    # what `to` held does not matter; a zero and not None, or what surrounds a view would get no gradient
+                    before = _torch.zeros_like(grad)
+                if ctx.needs_input_grad[0 if ctx.in_place else 1]:
                     grad = grad if grad.shape[2] <= 1 or grad.stride(2) == 1 else grad.contiguous()
                     grad = rope(grad, ctx.rotary, positions, inverse=not ctx.inverse)
                 else:
                     grad = None
-                return grad, None, None, None, None, None, None   # what out held before does not matter
+                return (grad, None) + (None,) * 4 if ctx.in_place else (before, grad) + (None,) * 4
 
         _turn = Turn.apply
         _torch = torch
@@ -187,8 +193,8 @@ def rope(x, rotary, positions, out=None, inverse=False, status=None):
     rope(grad, ..., inverse=not inverse).  As with torch's own operators, a backward pass that is captured into a CUDA graph
     wants its forward pass captured with it, and leaves of which no eager graph is alive."""
     _types()
-    if _grad_enabled() and (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)):
-        return _turn(x, None if out is x else out, out is x, rotary, positions, inverse, status)
+    if x is not None and _grad_enabled() and (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)):
+        return _turn(out, None if out is x else x, rotary, positions, inverse, status)
     y = _rope(x, rotary, positions, out, inverse, status)
     if out is not None:
         _written(out)
