@@ -331,7 +331,7 @@ def _handles(s):
         s["rotary"] = tkv.Rotary(s["table"], pair_axis=s["pair_axis"])
     if "cache" not in s and "pages" in s:
         if s["case"]["op"] == "reorder":
-            s["cache"] = [tkv.PagedCache(p, s["page_table"], s["lengths"]) for p in s["pages"]]
+            s["cache"] = tkv.PagedLayers([tkv.PagedCache(p, s["page_table"], s["lengths"]) for p in s["pages"]])
         else:
             s["cache"] = tkv.PagedCache(s["pages"], s["page_table"], s["lengths"])
     return tkv
@@ -342,7 +342,7 @@ def _run_own(s):
     if c["op"] == "select":
         return tkv.beam_select(s["logits"], s["scores"], count=c["count"], finished=s["finished"], eos=s["eos"])
     if c["op"] == "reorder":
-        tkv.reorder_beams(s["cache"], s["parents"])
+        s["cache"].reorder(s["parents"])
         return s["page_table"], s["pages"]
     if c["op"] == "append":
         s["cache"].append(s["k"], s["v"], s["cu"], rotary=s["rotary"], positions=s["positions"])
