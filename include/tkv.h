@@ -378,9 +378,11 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  * The pages have no counterpart for these calls: they are what a decode layer
  * around the attention needs when its cache is not a tiered context -- the
  * rotation of positions, rows into a paged cache with the rotation of k on the
- * way, attention over that cache held in 4 bits or in 16, and rows back out.
+ * way, attention over that cache held in 4 bits, in 8 or in 16, rows back out,
+ * and beam search: the choice of the beams' continuations, and caches that follow
+ * the beams that were chosen.
  *
- * Conventions of the five calls, beyond those at the top of this file:
+ * Conventions of these calls, beyond those at the top of this file:
  *   - They have no context and keep nothing: the caller owns every buffer, they
  *     allocate nothing, never synchronise, can be captured into a CUDA graph, and
  *     may be called from several host threads.  Their work is enqueued on
@@ -406,8 +408,8 @@ tkv_status tkv_measure_host_link(int32_t device, int64_t bytes, double* h2d_ce_g
  *     wait for a copy of the kernel's own ran out: the rows that it was for are NaN),
  *     the largest.  With NULL none of them is reported. */
 
-/* Element types.  TKV_INT4 is a type of pages only. */
-enum { TKV_BF16 = 0, TKV_FP16 = 1, TKV_FP32 = 2, TKV_INT4 = 3 };
+/* Element types.  TKV_INT4 and TKV_E4M3 are types of pages only. */
+enum { TKV_BF16 = 0, TKV_FP16 = 1, TKV_FP32 = 2, TKV_INT4 = 3, TKV_E4M3 = 4 };
 
 /* A rotation of positions.  Of a head's channels the first 2 * pairs are
  * turned in pairs, (j, j + pairs) or, if interleaved, (2j, 2j + 1):
@@ -442,7 +444,20 @@ typedef struct {
  *       NaN reads as NaN.  A quotient within 2^-22 of a tie may go to either side
  *       where gain is not a power of two.  Choose gain so that amax / (7 gain) falls in E4M3's
  *       normal range, 2^-6 .. 448: amax / 1024 of what the head is expected to
- *       hold leaves room on both sides. */
+ *       hold leaves room on both sides.
+ *   TKV_E4M3            [num_pages][Hkv][page_size / 16][32 d + 16] bytes: records of
+ *       16 positions, K codes [d/64][16][64] | V codes [2][d/8][4][8][2] | int32 e_k,
+ *       e_v | 8 unused bytes.  K: 64 channels of 16 positions at a time; V: half of the
+ *       positions, channel / 8, pair of positions, channel, position of the pair.  The
+ *       value is E4M3(code) * 2^e, with one e for the 16 positions of a block and
+ *       head, of K and of V (e outside -32 .. 31 counts as the nearer of these).
+ *       The append finds the least e in that range with amax <= 448 * 2^e, amax the largest
+ *       finite magnitude of the block's new rows; where rows of the block precede
+ *       them, e never falls, and if it grows their codes are rounded anew: only what falls below
+ *       2^-6 of the new scale can change.  A code is x 2^-e to nearest even, saturating (at
+ *       448 * 2^31); an infinity or a NaN is stored as NaN, and the block's other values stay
+ *       what they are.  The rows of a block that come after the step's are as good as free:
+ *       sequences that share a block's page may not append to it. */
 typedef struct {
     void* pages;                /* device, 16-byte aligned */
     const int32_t* page_table;  /* device int32 [batch][max_pages] */
@@ -450,7 +465,7 @@ typedef struct {
     const float* k_gain;        /* device fp32 [Hkv], > 0; TKV_INT4 only; NULL = 1 */
     const float* v_gain;
     int64_t num_pages;
-    int32_t kv_type;            /* TKV_BF16, TKV_FP16 or TKV_INT4 */
+    int32_t kv_type;            /* TKV_BF16, TKV_FP16, TKV_INT4 or TKV_E4M3 */
     int32_t num_kv_heads;       /* Hkv >= 1 */
     int32_t head_dim;           /* d: 64 or 128 */
     int32_t page_size;          /* a power of two, 16 .. 65536 */
@@ -485,8 +500,8 @@ tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary* rotary, co
 /* The reverse: reads positions out of the pages into k and v, addressed like an
  * append (lengths[b] = the end of the range, n_b its extent).
  * k, v: device [rows][Hkv][d] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, 16-byte
- * aligned, strides multiples of 16 bytes; a 4-bit value is rounded to fp32, and
- * every value from there to dtype.  A row
+ * aligned, strides multiples of 16 bytes; a 4-bit or 8-bit value is rounded to fp32,
+ * and every value from there to dtype.  A row
  * without a place (see the append) reads as NaN and raises status.
  * Errors: TKV_EINVAL, TKV_ECUDA. */
 tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dtype, int64_t rows,
@@ -507,7 +522,7 @@ tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dt
  * device fp32 [rows][num_q_heads], contiguous.
  * A step's size is limited: (rows * num_q_heads / Hkv / 8 + batch) * Hkv *
  * (max_pages * page_size / 32) tiles (half as many positions a tile with 16-bit
- * pages) are at most 2 * 10^9; a longer prompt enters in parts.
+ * pages, and with 8-bit pages of d 128) are at most 2 * 10^9; a longer prompt enters in parts.
  * max_new and max_len are the host's estimates of the largest n_b and the largest
  * length.  They choose how the work is split, not what is computed: any
  * values >= 1 give right results, better ones faster.
@@ -530,6 +545,51 @@ tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q, void* out,
  * this cache, num_q_heads and max_new (0 if the arguments are refused).  Does
  * not depend on lengths. */
 int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_heads, int32_t max_new);
+
+/* Beam search: the best continuations of each sequence's beams.
+ *   total[b][w][v] = scores[b][w] + logits[b][w][v] - log sum_v exp(logits[b][w][v])
+ * and the outputs are the `count` largest over (w, v), in descending order, ties to the
+ * lowest w * vocab + v: the total (rounded from 64 bits), the beam w and the token v.
+ * Within a beam the order is that of the logits.
+ * finished (device uint8 [batch][beams], or NULL): a beam where it is not 0 offers
+ * one candidate, token eos with the beam's own score; its logits are not read.
+ * A beam with a score that is not finite, or with a NaN or +infinity among its logits, offers
+ * none, and no candidate has a total of -infinity.  Places that are left over get
+ * score -infinity, beam -1 and token -1.
+ * logits: device [batch][beams][vocab] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, the
+ * vocabulary contiguous, strides in elements (any alignment); scores: device fp32
+ * [batch][beams]; out_scores, out_beams, out_tokens: device [batch][count].
+ * Limits: beams and count 1 .. 64, beams * vocab < 2^31 - 256.
+ * workspace: tkv_beam_select_workspace(...) bytes on the current device, 16-byte aligned,
+ * contents irrelevant; calls that may run at the same time need one each.
+ * Errors: TKV_EINVAL (eos outside the vocabulary with `finished` among them), TKV_ECAPACITY
+ * (workspace too small), TKV_ECUDA. */
+tkv_status tkv_beam_select(const void* logits, int32_t dtype, int64_t batch, int32_t beams, int32_t vocab, int64_t batch_stride,
+                           int64_t beam_stride, const float* scores, const uint8_t* finished, int32_t eos, int32_t count,
+                           float* out_scores, int32_t* out_beams, int32_t* out_tokens, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/* Bytes of workspace of tkv_beam_select on the current device (0 if the arguments are refused, or batch is 0). */
+int64_t tkv_beam_select_workspace(int32_t dtype, int64_t batch, int32_t beams, int32_t vocab, int32_t count);
+
+/* The caches of a model's layers follow the chosen beams: sequence g * beams + w goes on
+ * from sequence g * beams + parents[g * beams + w].
+ * caches: host array of num_caches descriptors that share page_table, lengths, batch,
+ * max_pages and page_size; pages, types, heads and head_dim may differ.  parents:
+ * device int32 [batch]; a negative one means that the sequence keeps what it has.
+ * The columns of the page table before a sequence's current page (lengths / page_size) become
+ * its parent's, so beams share pages that are full; what the current, partly filled
+ * page holds (whole records of 4-bit and 8-bit pages) is copied, in every cache, from the parent's page into
+ * the sequence's own.  The table's columns from the current one on stay as they are, and the pages
+ * in them have to be each sequence's own.  So a prompt that one sequence has appended is given to its
+ * group by parents of that sequence; a child that keeps its parent costs nothing.
+ * What is wrong is reported in status, and left as it was: a parent >= beams (TKV_EINVAL, as if
+ * negative), a group whose sequences differ in length (TKV_EINVAL), lengths outside the table and pages
+ * outside [0, num_pages) (TKV_ECAPACITY; the table's columns are exchanged all the same in the
+ * latter case).  The page table is written, although the descriptor's pointer is const.
+ * Limits: beams 1 .. 32, page_size * Hkv < 2^26.  Errors: TKV_EINVAL, TKV_ECUDA. */
+tkv_status tkv_paged_reorder(const tkv_paged* caches, int32_t num_caches, const int32_t* parents, int32_t beams, int32_t* status,
+                             void* stream);
 
 /* Waits for all enqueued work and reports any device-side status word. */
 tkv_status tkv_sync(tkv_ctx* ctx);

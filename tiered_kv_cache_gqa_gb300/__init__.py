@@ -22,7 +22,7 @@ TKV_OK, TKV_EINVAL, TKV_ENOMEM, TKV_ECUDA, TKV_ECAPACITY, TKV_ETIMEOUT, TKV_ESTA
 TKV_T1_COPY_ENGINE, TKV_T1_SM_COPY, TKV_T1_SPLIT, TKV_T1_MULTI_CE, TKV_T1_RESIDENT = range(5)
 TKV_T2_HBM, TKV_T2_HOST = range(2)
 TKV_HOST_AUTO, TKV_HOST_PINNED_ALLOC, TKV_HOST_HUGE_ARENA = range(3)
-TKV_BF16, TKV_FP16, TKV_FP32, TKV_INT4 = range(4)
+TKV_BF16, TKV_FP16, TKV_FP32, TKV_INT4, TKV_E4M3 = range(5)
 
 # Every function the C ABI exports (include/tkv.h).
 EXPORTS = ("tkv_create", "tkv_destroy", "tkv_append", "tkv_prefetch", "tkv_decode_step",
@@ -30,7 +30,8 @@ EXPORTS = ("tkv_create", "tkv_destroy", "tkv_append", "tkv_prefetch", "tkv_decod
            "tkv_get_row", "tkv_profile_begin", "tkv_profile_end", "tkv_sync", "tkv_get_stats",
            "tkv_status_string", "tkv_decode_dense_noalloc", "tkv_capture_begin", "tkv_capture_end",
            "tkv_replay", "tkv_measure_host_link", "tkv_rope", "tkv_paged_append", "tkv_paged_gather",
-           "tkv_paged_attention", "tkv_paged_attention_workspace")
+           "tkv_paged_attention", "tkv_paged_attention_workspace", "tkv_beam_select",
+           "tkv_beam_select_workspace", "tkv_paged_reorder")
 
 
 class TkvUnavailable(RuntimeError):
@@ -148,6 +149,9 @@ def load():
     lib.tkv_paged_attention.argtypes = [pag, vp, vp, vp, i32, i64, i32, i64, i64, i64, i64, vp, i32, i32, i32,
                                         ctypes.c_float, vp, i64, vp, vp]
     lib.tkv_paged_attention_workspace.argtypes = [pag, i32, i32]
+    lib.tkv_beam_select.argtypes = [vp, i32, i64, i32, i32, i64, i64, vp, vp, i32, i32, vp, vp, vp, vp, i64, vp]
+    lib.tkv_beam_select_workspace.argtypes = [i32, i64, i32, i32, i32]
+    lib.tkv_paged_reorder.argtypes = [pag, i32, vp, i32, vp, vp]
     lib.tkv_get_stats.argtypes = [vp, ctypes.POINTER(Stats)]
     lib.tkv_status_string.argtypes = [st]
     lib.tkv_status_string.restype = ctypes.c_char_p
@@ -155,6 +159,7 @@ def load():
         if name not in ("tkv_destroy", "tkv_status_string"):
             getattr(lib, name).restype = st
     lib.tkv_paged_attention_workspace.restype = i64
+    lib.tkv_beam_select_workspace.restype = i64
     _lib = lib
     return lib
 
@@ -311,6 +316,25 @@ def tkv_paged_attention(cache, q, out, lse, dtype, rows, num_q_heads, q_strides,
                                       workspace_bytes, _opt_ptr(status), torch_stream_handle() if stream is None else stream)
 
 
+def tkv_beam_select_workspace(dtype, batch, beams, vocab, count):
+    """Bytes of workspace of tkv_beam_select on the current device; 0: the arguments are refused."""
+    return load().tkv_beam_select_workspace(dtype, batch, beams, vocab, count)
+
+
+def tkv_beam_select(logits, dtype, batch, beams, vocab, strides, scores, finished, eos, count, out_scores, out_beams, out_tokens,
+                    workspace, workspace_bytes, stream=None):
+    """The best continuations of beams (see include/tkv.h): strides (batch, beam); returns the status."""
+    return load().tkv_beam_select(_opt_ptr(logits), dtype, batch, beams, vocab, *strides, _opt_ptr(scores), _opt_ptr(finished), eos, count,
+                                  _opt_ptr(out_scores), _opt_ptr(out_beams), _opt_ptr(out_tokens), _opt_ptr(workspace), workspace_bytes,
+                                  torch_stream_handle() if stream is None else stream)
+
+
+def tkv_paged_reorder(caches, num_caches, parents, beams, status=None, stream=None):
+    """Caches that follow the chosen beams (see include/tkv.h): caches a ctypes array of PagedDesc; returns the status."""
+    return load().tkv_paged_reorder(caches, num_caches, _opt_ptr(parents), beams, _opt_ptr(status),
+                                    torch_stream_handle() if stream is None else stream)
+
+
 def tkv_sync(ctx):
     return load().tkv_sync(ctx)
 
@@ -464,4 +488,4 @@ class TieredKV:
 
 
 # ------------------------------------------------- operators over a paged cache
-from .paged import PagedCache, Rotary, rope, rope_table  # noqa: E402,F401
+from .paged import PagedCache, PagedLayers, Rotary, beam_select, rope, rope_table  # noqa: E402,F401

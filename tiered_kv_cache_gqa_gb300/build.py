@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libtkv.so")
 SOURCES = ["tkv_api.cu", "attention.cu", "retier.cu", "noalloc.cu", "rope.cu", "paged_cache.cu",
-           "paged_attention.cu"]
+           "paged_cache8.cu", "paged_attention.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

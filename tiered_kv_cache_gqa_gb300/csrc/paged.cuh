@@ -12,6 +12,14 @@
 // The value is q * scale * gain: scale an E4M3 number >= 0 of a block of 16 channels, gain a power of
 // two or any other positive fp32 number of the KV head.  Uniform codes and not E2M1: they expand to
 // fp16, times their scale, with one logic and one fused multiply-add instruction a pair, exactly.
+//
+// 8-bit pages.  Records of 16 positions too, with one exponent for K and one for V:
+//   K codes [d/64][16][64] | V codes [2][d/8][4][8][2] | int32 e_k, e_v | 8 bytes of zeros
+// 32 d + 16 bytes: 4,112 at d = 128, 2,064 at d = 64.  A code is an E4M3 number and the value code * 2^e, e in -32 .. 31.  The scale is a
+// power of two, so that a block whose scale has to grow for a later token loses only what becomes subnormal, and so that
+// it enters the softmax's exponents as a whole number.  V's places are (half of the positions, channels / 8, pair of positions, channel,
+// position of the pair): the two positions that a matrix instruction wants in one register are neighbours, and so are
+// the 16-byte pieces that the lanes of a quarter warp read, of K and of V: no two of them in one bank.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,6 +36,12 @@ template <int D>
 struct Record {
     static constexpr int k_codes = 0, k_scales = 8 * D, v_codes = 9 * D, v_scales = 17 * D, bytes = 18 * D;
 };
+
+template <int D>
+struct Record8 {
+    static constexpr int k_codes = 0, v_codes = 16 * D, exponents = 32 * D, bytes = 32 * D + 16;
+};
+constexpr int kLowestExponent = -32, kHighestExponent = 31;   // of a block of 8-bit pages
 
 template <typename T> __device__ __forceinline__ float to_float(T x);
 template <> __device__ __forceinline__ float to_float<float>(float x) { return x; }
@@ -89,6 +103,11 @@ __device__ __forceinline__ float2 table_at(const float2* table, int pairs, int m
     cs.y *= sign;
     return cs;
 }
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
+// An exponent of a record, whatever its bytes are
+__device__ __forceinline__ int block_exponent(int e) { return min(max(e, kLowestExponent), kHighestExponent); }
 
 // The status word holds the largest code that a kernel met.
 __device__ __forceinline__ void raise_status(int32_t* status, int code) {
@@ -180,6 +199,7 @@ tkv_status check_rotary(const tkv_rotary* r, int head_dim, bool need_positions);
 tkv_status check_paged(const tkv_paged* c);
 // element (row, head, channel) -> memory: rows and heads do not overlap, strides >= 0
 bool strides_apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t width);
+inline bool has_records(int kv_type) { return kv_type == TKV_INT4 || kv_type == TKV_E4M3; }   // pages that take rows of either 16-bit type
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int dtype_size(int t) { return t == TKV_FP32 ? 4 : 2; }

@@ -207,8 +207,8 @@ __device__ __forceinline__ int share_of(const PagedAttnArgs& a, int total) {
 template <int D, int NT, int KIND>
 struct Config {
     static constexpr int R = 8 * NT;
-    static constexpr int ctas = (KIND == kInt4 && NT == 1) ? 2 : 1;
-    static constexpr int stages = KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
+    static constexpr int ctas = (in_records(KIND) && NT == 1) ? 2 : 1;
+    static constexpr int stages = KIND == kE4m3 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
     static constexpr int queue = stages <= 6 ? 8 : 16;   // pieces: the one computed, one a stage, one not yet copied
     static constexpr int warp_ring = stages * TileOf<D, KIND>::bytes;
     static constexpr int at_once = NT == 4 ? 1 : TileOf<D, KIND>::groups;   // groups of positions, by the registers
@@ -252,7 +252,7 @@ struct Rec4 {
 
 // The channels of component c of float4 j: row 2 cq + (c & 1).
 template <int D, int KIND>
-__device__ __forceinline__ int channel_of(int r, int j, int c) { return KIND == kInt4 ? (D / 8) * r + 2 * j + (c >> 1) : 16 * j + r + 8 * (c >> 1); }
+__device__ __forceinline__ int channel_of(int r, int j, int c) { return KIND == kE4m3 ? 8 * (r + 8 * (j >> 2)) + 2 * (j & 3) + (c >> 1) : KIND == kInt4 ? (D / 8) * r + 2 * j + (c >> 1) : 16 * j + r + 8 * (c >> 1); }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {
     return fp16 ? half2_bits(__floats2half2_rn(a, b)) : bf162_bits(__floats2bfloat162_rn(a, b));
@@ -280,7 +280,7 @@ __device__ __forceinline__ void emit4(const PagedAttnArgs& a, const Rows& rows, 
         if (!to) continue;
         const float m = e ? ml.z : ml.x, l = e ? ml.w : ml.y, inv = inverse(l, gain);
         const uint32_t w = pack16((e ? x.y : x.x) * inv, (e ? x.w : x.z) * inv, fp16);
-        if (KIND == kInt4) {
+        if (in_records(KIND)) {
             *reinterpret_cast<uint32_t*>(to + channel_of<D, KIND>(r, j, 0)) = w;
         } else {
             to[channel_of<D, KIND>(r, j, 0)] = (uint16_t)w;
@@ -320,7 +320,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     using T = TileOf<D, KIND>;
     constexpr int R = C::R, S = C::stages, TP = T::positions;
     const int k = lane & 3;
-    const int64_t head_bytes = KIND == kInt4 ? (int64_t)(a.c.page_size >> 4) * Record<D>::bytes : (int64_t)a.c.page_size * (4 * D);
+    const int64_t head_bytes = in_records(KIND) ? (int64_t)(a.c.page_size >> 4) * T::record : (int64_t)a.c.page_size * (4 * D);
     const int64_t page_bytes = head_bytes * a.c.num_kv_heads;
     const int in_page = a.c.page_size - 1;
     const uint32_t full0 = smem_u32(sh.full[w]), empty0 = smem_u32(sh.empty[w]), ring = smem_u32(sh.ring[w]);
@@ -340,8 +340,8 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     const uint8_t* pages = nullptr;
     int st = 0, parity = 0, spins = 0, issued = 0;
     bool first = true;   // the ring's first round: nothing to wait for
-    auto look_up = [&]() {   // a 4-bit tile has two records, which may lie in two pages
-        const int p = pos + (KIND == kInt4 ? (k & 1) * 16 : 0);
+    auto look_up = [&]() {   // a tile may have two records, which may lie in two pages
+        const int p = pos + (T::groups == 2 ? (k & 1) * 16 : 0);
         page = p < end ? table[p >> a.page_shift] : -2;
     };
     while (__any_sync(0xffffffffu, left + tiles > 0 && spins < kSpinLimit)) {
@@ -400,13 +400,12 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 const bool ok = page >= 0 && page < a.c.num_pages;
                 const uint32_t bar = full0 + 8 * st, to = ring + st * T::bytes;
                 if (!ok && page != -2) raise_status(a.status, TKV_ECAPACITY);
-                if (KIND == kInt4) {
-                    if (k < 2) {
+                if (in_records(KIND)) {
+                    if (k < T::groups) {
                         sh.bad[w][st][k] = !ok;
                         if (ok) {
-                            mbar_arrive_expect(bar, Record<D>::bytes);
-                            bulk_copy(to + k * Record<D>::bytes, pages + page * page_bytes + (((pos + k * 16) & in_page) >> 4) * Record<D>::bytes,
-                                      Record<D>::bytes, bar);
+                            mbar_arrive_expect(bar, T::record);
+                            bulk_copy(to + k * T::record, pages + page * page_bytes + (((pos + k * 16) & in_page) >> 4) * T::record, T::record, bar);
                         } else {
                             mbar_arrive(bar);
                         }
@@ -434,7 +433,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
         }
         uint32_t groups = __ballot_sync(0xffffffffu, moved);
         if (groups == 0) __nanosleep(32);
-        if (KIND != kInt4) {
+        if (!in_records(KIND)) {
             // the whole warp copies the tile of each of its lane groups in turn
             constexpr int CH = D / 8;   // 16-byte pieces of a row
             for (groups &= 0x11111111u; groups; groups &= groups - 1) {
@@ -510,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kWarps && lane < kWarps) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&sh.full[lane][s]), KIND == kInt4 ? 2 : 33);   // the lanes that bring a tile; 16 bits: and the one that says if there is a page
+            mbar_init(smem_u32(&sh.full[lane][s]), in_records(KIND) ? T::groups : 33);   // the lanes that bring a tile; 16 bits: and the one that says if there is a page
             mbar_init(smem_u32(&sh.empty[lane][s]), 1);
         }
         for (int s = 0; s < C::queue; ++s) mbar_init(smem_u32(&sh.known[lane][s]), 1);
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 
     int taken = 0;                       // pieces of this warp
     Sums<D, NT> sums;
-    const bool fp16 = KIND == kFp16 || (KIND == kInt4 && a.q_fp16);
+    const bool fp16 = KIND == kFp16 || (in_records(KIND) && a.q_fp16);
     auto gain_of = [&](int h) { return KIND == kInt4 ? 16.0f * (a.c.v_gain ? a.c.v_gain[h] : 1.0f) : 1.0f; };
     if (warp == kWarps) {
         const int w = min(lane >> 2, kWarps - 1);
@@ -581,16 +580,16 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             for (int t = 1;; ++t, p0 += TP) {
                 const uint8_t* at = sh.ring[warp] + stage * TB;
                 const uint32_t at_s = smem_u32(at);
-                const uint32_t bad = sh.bad[warp][stage][0] | (KIND == kInt4 ? sh.bad[warp][stage][1] << 1 : 0);
+                const uint32_t bad = sh.bad[warp][stage][0] | (T::groups == 2 ? sh.bad[warp][stage][1] << 1 : 0);
                 if (!bad && p0 + TP <= all_until && p0 >= all_from) {
 #pragma unroll 1
                     for (int g = 0; g < T::groups; g += C::at_once)
-                        attend_tile<D, NT, KIND, C::at_once, true>(at + g * Record<D>::bytes, at_s, lane, p0 + 16 * g, false, piece.rows, a.group,
+                        attend_tile<D, NT, KIND, C::at_once, true>(at + g * T::record, at_s, lane, p0 + 16 * g, false, piece.rows, a.group,
                                                                    a.group_mul, a.window, q, sums);
                 } else {
 #pragma unroll 1
                     for (int g = 0; g < T::groups; ++g)
-                        attend_tile<D, NT, KIND, 1, false>(at + g * Record<D>::bytes, at_s, lane, p0 + 16 * g, (bad >> g) & 1, piece.rows, a.group,
+                        attend_tile<D, NT, KIND, 1, false>(at + g * T::record, at_s, lane, p0 + 16 * g, (bad >> g) & 1, piece.rows, a.group,
                                                            a.group_mul, a.window, q, sums);
                 }
                 __syncwarp();   // every lane has read the slot
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                         uint32_t w[D / 16];
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) w[j] = pack16(sums.o[nt][j][e] * inv, sums.o[nt][j][e + 2] * inv, fp16);
-                        if (KIND == kInt4) {   // D / 8 channels next to one another
+                        if (in_records(KIND)) {   // 4 bits: D / 8 channels next to one another; 8 bits: 8 in every 64
 #pragma unroll
                             for (int j = 0; j < D / 16; j += 4)
                                 *reinterpret_cast<uint4*>(to + channel_of<D, KIND>(r, j, 0)) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
@@ -883,13 +882,14 @@ cudaError_t launch(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     if ((e = launch_behind(paged_attention_kernel<D, NT, KIND>, dim3(a.grid), kThreads, smem, st, a)) != cudaSuccess || a.whole_items) return e;
-    const bool fp16 = KIND == kFp16 || (KIND == kInt4 && a.q_fp16);
+    const bool fp16 = KIND == kFp16 || (in_records(KIND) && a.q_fp16);
     return launch_behind(paged_combine_kernel<D, NT, KIND>, dim3(a.grid), kCombineWarps * 32, 0, st, a, fp16);
 }
 
 template <int D, int NT>
 cudaError_t launch_kind(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
     return a.c.kv_type == TKV_INT4   ? launch<D, NT, kInt4>(a, sms, dev, st)
+           : a.c.kv_type == TKV_E4M3 ? launch<D, NT, kE4m3>(a, sms, dev, st)
            : a.c.kv_type == TKV_BF16 ? launch<D, NT, kBf16>(a, sms, dev, st)
                                      : launch<D, NT, kFp16>(a, sms, dev, st);
 }
@@ -922,7 +922,7 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
                                           int64_t workspace_bytes, int32_t* status, void* stream) {
     if (!attention_shape_ok(cache, num_q_heads, max_new) || max_len < 1 || window < 0 || !std::isfinite((float)((double)scale * kLog2E))) return TKV_EINVAL;
     if (dtype != TKV_BF16 && dtype != TKV_FP16) return TKV_EINVAL;
-    if (cache->kv_type != TKV_INT4 && cache->kv_type != dtype) return TKV_EINVAL;
+    if (!has_records(cache->kv_type) && cache->kv_type != dtype) return TKV_EINVAL;
     if (rows < 0 || rows > 0x7FFFFFFF || !cu_tokens) return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     // row indices within a sequence (queries x heads of a group) are 32-bit
@@ -964,8 +964,8 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = rows_of_32(a, max_new, sight, sms) ? 4 : row_tiles(a.group, max_new);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
-    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && cache->kv_type == TKV_INT4);
-    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 ? 32 : 16) + 1);
+    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && has_records(cache->kv_type));
+    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 || (cache->kv_type == TKV_E4M3 && cache->head_dim == 64) ? 32 : 16) + 1);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
     e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
     if (e != cudaSuccess) {

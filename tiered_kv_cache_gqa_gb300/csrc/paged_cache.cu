@@ -11,7 +11,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "paged_tile.cuh"
+#include "paged_rows.cuh"
 
 using namespace tkv;
 
@@ -19,24 +19,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAppendCtas = 4, kGatherCtas = 8;   // on an SM at once, by their registers
-
-struct RowArgs {
-    tkv_paged c;
-    const void* k;             // append: inputs; gather: outputs
-    const void* v;
-    const float2* table;       // null: k is not rotated
-    const int32_t* positions;  // null: the row's position in the cache
-    const int32_t* cu;
-    int32_t* status;
-    int64_t rows, axis_stride, k_row, k_head, v_row, v_head;
-    int pairs, max_positions, num_axes, interleaved;
-    bool table_16;             // two pairs of the table lie on 16 bytes
-    int lanes;                 // heads that the threads of a row take at once
-    int page_shift;
-    float sign;
-    int units;                 // append: threads of a row
-    alignas(16) uint8_t pair_axis[256];
-};
 
 // Where row `row` of the step lies: page and position in the page; false for no row (behind the last
 // sequence: *page = -2) and for a bad place (*page = -1: the position or the page is outside).
@@ -97,49 +79,6 @@ __device__ __forceinline__ uint32_t quantise_half(float (&x)[8], float amax, flo
     }
     const uint32_t codes = __byte_perm(__byte_perm(pair[0], pair[1], 0x0040), __byte_perm(pair[2], pair[3], 0x0040), 0x5410);
     return bad ? 0x88888888u : codes;
-}
-
-// 16 bytes as floats, and back.
-template <typename T>
-__device__ __forceinline__ void unpack(uint4 u, float (&x)[16 / sizeof(T)]) {
-    Vec16<T> v;
-    v.u = u;
-#pragma unroll
-    for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = to_float(v.e[i]);
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float* x) {
-    Vec16<T> v;
-#pragma unroll
-    for (int i = 0; i < 16 / (int)sizeof(T); ++i) v.e[i] = from_float<T>(x[i]);
-    return v.u;
-}
-
-// How k is rotated.
-//   kNone      not at all
-//   kHalves    pairs % 16 == 0: the partners of 8 channels lie `pairs` channels away, in another block
-//   kAdjacent  pairs % 4 == 0: 8 channels hold their own 4 pairs
-//   kAny       channel by channel, partners read one at a time
-enum Turn { kNone, kHalves, kAdjacent, kAny };
-
-// Channels 8 chunk .. + 7 of head row k, turned one at a time (kAny).
-template <typename T>
-__device__ __forceinline__ void turn_any(const RowArgs& a, const T* k, int64_t row, int own_position, int chunk, float (&x)[8]) {
-    bool bad = false;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        const int ch = 8 * chunk + i;
-        if (ch >= 2 * a.pairs) break;
-        const bool first = a.interleaved ? !(ch & 1) : ch < a.pairs;
-        const int j = a.interleaved ? ch >> 1 : first ? ch : ch - a.pairs;
-        const int p = a.positions ? a.positions[a.pair_axis[j] * a.axis_stride + row] : own_position;
-        const float2 cs = table_at(a.table, a.pairs, a.max_positions, p, j, a.sign, &bad);
-        const float own = to_float(k[ch]), other = to_float(k[a.interleaved ? ch ^ 1 : first ? ch + a.pairs : ch - a.pairs]);
-        const float y = first ? rotate_pair(own, other, cs).x : rotate_pair(other, own, cs).y;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = c == i ? y : x[c];
-    }
-    if (bad) raise_status(a.status, TKV_EINVAL);
 }
 
 // x (8 values), and y if there is a partner, to their places: 4-bit pages, codes and the byte of the block's scale, `scale`
@@ -419,7 +358,7 @@ namespace tkv {
 
 tkv_status check_paged(const tkv_paged* c) {
     if (!c || !c->pages || !c->page_table || !c->lengths) return TKV_EINVAL;
-    if (c->kv_type != TKV_BF16 && c->kv_type != TKV_FP16 && c->kv_type != TKV_INT4) return TKV_EINVAL;
+    if (c->kv_type != TKV_BF16 && c->kv_type != TKV_FP16 && !has_records(c->kv_type)) return TKV_EINVAL;
     if (c->head_dim != 64 && c->head_dim != 128) return TKV_EINVAL;
     if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return TKV_EINVAL;
     if (c->batch < 1 || c->max_pages < 1 || c->num_kv_heads < 1 || c->num_pages < 1) return TKV_EINVAL;
@@ -438,7 +377,7 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
     if (dtype != TKV_BF16 && dtype != TKV_FP16) return TKV_EINVAL;
     if (row_args(cache, k, v, rows, k_row_stride, k_head_stride, v_row_stride, v_head_stride, 2, cu_tokens, status, &a) != TKV_OK)
         return TKV_EINVAL;
-    if (cache->kv_type != TKV_INT4 && cache->kv_type != dtype) return TKV_EINVAL;
+    if (!has_records(cache->kv_type) && cache->kv_type != dtype) return TKV_EINVAL;
     int turn = kNone;
     if (rotary) {
         if (check_rotary(rotary, cache->head_dim, false) != TKV_OK) return TKV_EINVAL;
@@ -457,8 +396,10 @@ extern "C" tkv_status tkv_paged_append(const tkv_paged* cache, const tkv_rotary*
     if (rows == 0) return TKV_OK;
     a.units = cache->head_dim / 8 - (turn == kHalves ? a.pairs / 8 : 0);
     const int rows_a_block = kThreads / a.units;
-    cudaError_t e = spread(a, (rows + rows_a_block - 1) / rows_a_block, kAppendCtas);
-    if (e == cudaSuccess) {
+    cudaError_t e = cudaSuccess;
+    if (cache->kv_type == TKV_E4M3) {
+        e = append_e4m3(a, dtype, (cudaStream_t)stream);
+    } else if ((e = spread(a, (rows + rows_a_block - 1) / rows_a_block, kAppendCtas)) == cudaSuccess) {
         const dim3 grid((unsigned)((rows + rows_a_block - 1) / rows_a_block), a.lanes);
         e = dtype == TKV_BF16 ? append_type<__nv_bfloat16>(a, turn, grid, (cudaStream_t)stream)
                               : append_type<__half>(a, turn, grid, (cudaStream_t)stream);
@@ -483,8 +424,10 @@ extern "C" tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v,
         return TKV_EINVAL;
     if (rows == 0) return TKV_OK;
     const int64_t threads = rows * (cache->head_dim * dtype_size(dtype) / 16);
-    cudaError_t e = spread(a, (threads + kThreads - 1) / kThreads, kGatherCtas);
-    if (e == cudaSuccess) {
+    cudaError_t e = cudaSuccess;
+    if (cache->kv_type == TKV_E4M3) {
+        e = gather_e4m3(a, dtype, (cudaStream_t)stream);
+    } else if ((e = spread(a, (threads + kThreads - 1) / kThreads, kGatherCtas)) == cudaSuccess) {
         const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), a.lanes);
         cudaStream_t st = (cudaStream_t)stream;
         e = dtype == TKV_BF16   ? gather_type<__nv_bfloat16>(a, grid, st)

@@ -17,6 +17,9 @@
 // 129 * 15 < 2^11, and 1032 * 448 / 16 is below its largest number.  So K and V enter the products as stored; what is
 // rounded is p (to fp16, 2^-11; for bf16 pages to two bf16 parts, 2^-16) and, for rows of q in bf16, what lies 2^-29 below
 // a row's largest channel (q is scaled by a power of two into fp16's range).
+// 8 bits: E4M3 codes are fp16 numbers by one conversion a pair.  A block's exponents stay out of the products: z = S scale log2 e 2^e_k
+// + e_v and p = 2^(z - m), which is the weight times V's scale, so O^T += V^T P^T adds up blocks of different scales; l += p 2^-e_v.
+// With e_v in -32 .. 31 what p loses below 2^-126 is below 2^-60 of the largest weight.
 // The channels that a lane holds of a position are those of its own bytes: K's products sum over all channels, so q is
 // laid out to match; for V the lanes' channels are rows of O^T.
 #pragma once
@@ -30,15 +33,18 @@ constexpr float kTop = 15.0f;                      // p = 2^(z - m) <= 2^15; in 
 constexpr float kLift = 5.0f;                      // a new reference lies this far below the maximum: 10 are left to grow
 constexpr float kLowest = -3.402823466e38f;        // a reference before anything is seen: 2^(-inf - it) = 0, no NaN
 
-enum PageKind { kInt4, kBf16, kFp16 };
+enum PageKind { kInt4, kBf16, kFp16, kE4m3 };
+// pages of records, copied whole; their lanes hold neighbouring channels of O
+constexpr bool in_records(int kind) { return kind == kInt4 || kind == kE4m3; }
 
 template <int D, int KIND>
 struct TileOf {
-    static constexpr int groups = KIND == kInt4 ? 2 : 1;     // of 16 positions
+    static constexpr int groups = KIND == kInt4 || (KIND == kE4m3 && D == 64) ? 2 : 1;     // of 16 positions
     static constexpr int positions = 16 * groups;
     static constexpr int row = 2 * D + 16;                   // 16 bits: bytes of a row, 16 more than it has, so that the
                                                              // rows of a fragment lie in different banks
-    static constexpr int bytes = KIND == kInt4 ? groups * Record<D>::bytes : 2 * 16 * row;
+    static constexpr int record = KIND == kInt4 ? Record<D>::bytes : KIND == kE4m3 ? Record8<D>::bytes : 2 * 16 * row;
+    static constexpr int bytes = groups * record;
 };
 
 // ------------------------------------------------------------------ PTX
@@ -211,6 +217,27 @@ __device__ __forceinline__ void scores_int4(const uint8_t* rec, int r, int cq, c
     }
 }
 
+// The same from 8-bit codes: the lane's 16 channels of rows r and r + 8 in every 64.
+template <int D, int NT>
+__device__ __forceinline__ void scores_e4m3(const uint8_t* rec, int r, int cq, const Query<D, NT>& q, float (&z)[NT][4]) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(rec + h * 1024 + r * 64 + cq * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(rec + h * 1024 + (r + 8) * 64 + cq * 16);
+        const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t f0 = half2_bits(e4m3_pair((uint16_t)wx[w])), f2 = half2_bits(e4m3_pair((uint16_t)(wx[w] >> 16)));
+            const uint32_t f1 = half2_bits(e4m3_pair((uint16_t)wy[w])), f3 = half2_bits(e4m3_pair((uint16_t)(wy[w] >> 16)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint2 b = q.get(nt, 4 * h + w);
+                mma_f16(z[nt], f0, f1, f2, f3, b.x, b.y);
+            }
+        }
+    }
+}
+
 // The same from 16-bit rows.
 template <int D, int NT, int KIND>
 __device__ __forceinline__ void scores_16(uint32_t k_at, int lane, const Query<D, NT>& q, float (&z)[NT][4]) {
@@ -287,6 +314,32 @@ __device__ __forceinline__ void values_int4(const uint8_t* rec, int r, int cq, u
         }
 }
 
+// Fragment j of V^T: rows r and r + 8 are channels 8 (r + 8 (j / 4)) + 2 (j % 4) and + 1; word j % 4 of the lane's pieces.
+__device__ __forceinline__ void v_codes8(uint32_t (&f)[4], uint32_t x, uint32_t y, uint32_t m0, uint32_t m1) {
+    f[0] = half2_bits(e4m3_pair((uint16_t)x)) & m0;
+    f[1] = half2_bits(e4m3_pair((uint16_t)(x >> 16))) & m0;
+    f[2] = half2_bits(e4m3_pair((uint16_t)y)) & m1;
+    f[3] = half2_bits(e4m3_pair((uint16_t)(y >> 16))) & m1;
+}
+
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void values_e4m3(const uint8_t* rec, int r, int cq, uint32_t keep, const Weights<NT>& p, float (&acc)[NT][D / 16][4]) {
+    const uint32_t m0 = MASKED ? pair_mask(keep) : ~0u, m1 = MASKED ? pair_mask(keep >> 2) : ~0u;
+    const uint8_t* at = rec + Record8<D>::v_codes + r * 64 + cq * 16;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + h * 512), y = *reinterpret_cast<const uint4*>(at + 8 * D + h * 512);
+        const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t f[4];
+            v_codes8(f, wx[w], wy[w], m0, m1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][4 * h + w], f[0], f[1], f[2], f[3], p.hi[nt][0], p.hi[nt][1]);
+        }
+    }
+}
+
 // Block j of V^T (channels 16 j .. 16 j + 15) from 16-bit rows.
 template <int D>
 __device__ __forceinline__ void v_block(uint32_t (&f)[4], uint32_t v_at, int lane, int j, uint32_t m0, uint32_t m1) {
@@ -318,6 +371,7 @@ template <int D, int NT, int KIND, bool MASKED>
 __device__ __forceinline__ void values(const uint8_t* tile, uint32_t tile_s, int g, int lane, uint32_t keep, const Weights<NT>& p,
                                        float (&acc)[NT][D / 16][4]) {
     if (KIND == kInt4) values_int4<D, NT, MASKED>(tile + g * Record<D>::bytes, lane >> 2, lane & 3, keep, p, acc);
+    else if (KIND == kE4m3) values_e4m3<D, NT, MASKED>(tile + g * Record8<D>::bytes, lane >> 2, lane & 3, keep, p, acc);
     else values_16<D, NT, KIND, MASKED>(tile_s + 16 * TileOf<D, KIND>::row, lane, keep, p, acc);
 }
 
@@ -332,6 +386,17 @@ __device__ __forceinline__ bool not_finite(const uint8_t* tile, uint32_t tile_s,
         return odd(v_scale_pair<D>(rec, lane >> 2, lane & 3, 0) & m0) || odd(v_scale_pair<D>(rec, lane >> 2, lane & 3, 1) & m1);
     }
     bool any = false;
+    if (KIND == kE4m3) {
+        const uint8_t* at = tile + g * Record8<D>::bytes + Record8<D>::v_codes + (lane >> 2) * 64 + (lane & 3) * 16;
+#pragma unroll 1
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t f[4];
+            const uint8_t* word = at + (j >> 2) * 512 + (j & 3) * 4;
+            v_codes8(f, *reinterpret_cast<const uint32_t*>(word), *reinterpret_cast<const uint32_t*>(word + 8 * D), m0, m1);
+            any |= odd(f[0]) || odd(f[1]) || odd(f[2]) || odd(f[3]);
+        }
+        return any;
+    }
 #pragma unroll 1
     for (int j = 0; j < D / 16; ++j) {
         uint32_t f[4];
@@ -341,7 +406,7 @@ __device__ __forceinline__ bool not_finite(const uint8_t* tile, uint32_t tile_s,
     return any;
 }
 
-// The values of V that row j of the lane's fragments stands for (two channels), at slot i of a group; 4 bits: q scale / 16.
+// The values of V that row j of the lane's fragments stands for (two channels), at slot i of a group; 4 bits: q scale / 16; 8 bits: the code.
 template <int D, int KIND>
 __device__ __forceinline__ float2 v_values(const uint8_t* tile, int g, int r, int i, int j) {
     const int p = slot_position<KIND>(i);
@@ -350,6 +415,11 @@ __device__ __forceinline__ float2 v_values(const uint8_t* tile, int g, int r, in
         const int c = (D / 8) * r + 2 * j, codes = rec[Record<D>::v_codes + p * (D / 2) + c / 2];
         const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(rec[Record<D>::v_scales + (c / 16) * 16 + p], __NV_E4M3))) * 0.0625f;
         return make_float2((float)((codes & 15) - 8) * s, (float)((codes >> 4) - 8) * s);
+    }
+    if (KIND == kE4m3) {
+        const uint8_t* at = tile + g * Record8<D>::bytes + Record8<D>::v_codes + (p >> 3) * (8 * D) + (r + 8 * (j >> 2)) * 64 + ((p & 7) >> 1) * 16 +
+                            (j & 3) * 4 + (p & 1);
+        return __half22float2(e4m3_pair((uint16_t)(at[0] | at[2] << 8)));
     }
     const uint16_t* row = reinterpret_cast<const uint16_t*>(tile + (16 + p) * TileOf<D, KIND>::row);
     const uint32_t w = row[16 * j + r] | (uint32_t)row[16 * j + r + 8] << 16;
@@ -364,15 +434,30 @@ __device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s
     constexpr int KM = D / 16;
     const int r = lane >> 2, cq = lane & 3;
     float z[NG][NT][4];
+    float un[NG];        // 8 bits: 2^-e_v of a group
     uint32_t keep[NG];   // which of the lane's four V positions of a group any row sees
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) z[g][nt][0] = z[g][nt][1] = z[g][nt][2] = z[g][nt][3] = 0.0f;
         if (KIND == kInt4) scores_int4<D, NT>(tile + g * Record<D>::bytes, r, cq, q, z[g]);
+        else if (KIND == kE4m3) scores_e4m3<D, NT>(tile + g * Record8<D>::bytes, r, cq, q, z[g]);
         else scores_16<D, NT, KIND>(tile_s, lane, q, z[g]);
+        if (KIND == kE4m3) {
+            const int2 e = *reinterpret_cast<const int2*>(tile + g * Record8<D>::bytes + Record8<D>::exponents);
+            const float ks = power_of_two(block_exponent(e.x)), ev = (float)block_exponent(e.y);
+            un[g] = power_of_two(-block_exponent(e.y));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
+                const float z0 = q.z0[nt] * ks, z1 = q.z1[nt] * ks;
+                z[g][nt][0] = fmaf(z[g][nt][0], z0, ev);
+                z[g][nt][1] = fmaf(z[g][nt][1], z1, ev);
+                z[g][nt][2] = fmaf(z[g][nt][2], z0, ev);
+                z[g][nt][3] = fmaf(z[g][nt][3], z1, ev);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT && KIND != kE4m3; ++nt) {
             z[g][nt][0] *= q.z0[nt];
             z[g][nt][1] *= q.z1[nt];
             z[g][nt][2] *= q.z0[nt];
@@ -437,8 +522,13 @@ __device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s
         for (int nt = 0; nt < NT; ++nt) {
             const float p00 = exp2_approx(z[g][nt][0] - a.m[nt][0]), p01 = exp2_approx(z[g][nt][1] - a.m[nt][1]);
             const float p10 = exp2_approx(z[g][nt][2] - a.m[nt][0]), p11 = exp2_approx(z[g][nt][3] - a.m[nt][1]);
-            a.l[nt][0] += p00 + p10;
-            a.l[nt][1] += p01 + p11;
+            if (KIND == kE4m3) {
+                a.l[nt][0] = fmaf(p00 + p10, un[g], a.l[nt][0]);
+                a.l[nt][1] = fmaf(p01 + p11, un[g], a.l[nt][1]);
+            } else {
+                a.l[nt][0] += p00 + p10;
+                a.l[nt][1] += p01 + p11;
+            }
             if (KIND == kBf16) {
                 // bf16 keeps 8 bits: p as a sum of two, which the products add up in fp32
                 const __nv_bfloat162 h0 = __floats2bfloat162_rn(p00, p01), h1 = __floats2bfloat162_rn(p10, p11);
@@ -526,6 +616,32 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
                       half2_bits(__floats2half2_rn(x[8 * w + c + 1] * up, x[8 * w + c + 5] * up)));
             }
             const float z = scale_log2 * gain * 16.0f / up;
+            q.z0[nt] = __shfl_sync(0xffffffffu, z, 8 * cq);
+            q.z1[nt] = __shfl_sync(0xffffffffu, z, 8 * cq + 4);
+        } else if (KIND == kE4m3) {
+            float x[D / 4];                              // 16 channels of every 64
+            float top = 0.0f;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (is_row) v = *reinterpret_cast<const uint4*>(x16 + 64 * (w >> 1) + 16 * cq + 8 * (w & 1));
+                const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = fp16 ? __half22float2(bits_half2(e[i])) : bf16x2_to_float2(e[i]);
+                    x[8 * w + 2 * i] = f.x;
+                    x[8 * w + 2 * i + 1] = f.y;
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = min(254, max(1, 268 - (int)(__float_as_uint(top) >> 23)));   // as above
+            const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+            for (int i = 0; i < KM; ++i)
+                q.set(nt, i, half2_bits(__floats2half2_rn(x[4 * i] * up, x[4 * i + 1] * up)), half2_bits(__floats2half2_rn(x[4 * i + 2] * up, x[4 * i + 3] * up)));
+            const float z = scale_log2 / up;
             q.z0[nt] = __shfl_sync(0xffffffffu, z, 8 * cq);
             q.z1[nt] = __shfl_sync(0xffffffffu, z, 8 * cq + 4);
         } else {

@@ -1,4 +1,5 @@
-"""The operators around a paged KV cache on torch tensors: rope, and PagedCache with append, attend, gather.
+"""The operators around a paged KV cache on torch tensors: rope, PagedCache with append, attend, gather, and beam search:
+beam_select, and PagedLayers with reorder.
 
 Thin wrappers: they check the arguments, allocate outputs with torch's allocator on the current stream of the tensors'
 device, and call the C functions of the same names (include/tkv.h), which say what is computed and what a kernel does
@@ -13,15 +14,23 @@ every call can be captured into a CUDA graph.
     q = rope(q, rotary, positions)                            # [rows, Hq, d]
     cache.append(k, v, cu_tokens, rotary=rotary, positions=positions)
     out = cache.attend(q, cu_tokens)
+
+and with beams, the batch being groups * beams sequences:
+
+    layers = PagedLayers(caches)                              # of all layers; one page table, one lengths
+    scores, beams, tokens = beam_select(logits, scores)       # logits [groups, beams, vocab]
+    layers.reorder(beams)                                     # each sequence goes on from the beam that it was given
 """
 import math
 import threading
 
-from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_OK, PagedDesc, RotaryDesc, TkvError,
+from . import (CUDA_STREAM_LEGACY, TKV_BF16, TKV_EINVAL, TKV_FP16, TKV_FP32, TKV_INT4, TKV_E4M3, TKV_OK, PagedDesc, RotaryDesc, TkvError,
                load)
 
 _torch = _raw_stream = _current_device = _capturing = _int32 = _grad_enabled = _written = _turn = None
 _DTYPES = {}
+_RECORDS = {18 * 64: (TKV_INT4, 64), 18 * 128: (TKV_INT4, 128), 32 * 64 + 16: (TKV_E4M3, 64), 32 * 128 + 16: (TKV_E4M3, 128)}
+_select_sizes = {}   # workspaces of beam_select, by device and shape
 _own = threading.local()   # .work: the thread's workspaces of the attention, by device and stream
 
 
@@ -107,6 +116,21 @@ def _call(fn, where, device, *args):
         rc = fn(*args, _raw_stream(device) or CUDA_STREAM_LEGACY)
     if rc != TKV_OK:
         raise TkvError(rc, where)
+
+
+def _workspace(size, index, device):
+    """`size` bytes for kernels that are enqueued next on the device's current stream, kept by the thread or, in a capture, new."""
+    if _current_device() != index or _capturing():
+        return _torch.empty(size, dtype=_torch.uint8, device=device)
+    try:
+        kept = _own.work
+    except AttributeError:
+        kept = _own.work = {}
+    key = index, _raw_stream(index)
+    work = kept.get(key)
+    if work is None or work.numel() < size:
+        work = kept[key] = _torch.empty(size, dtype=_torch.uint8, device=device)
+    return work
 
 
 def _status_ptr(status, where, device):
@@ -232,7 +256,8 @@ def _rope(x, rotary, positions, out, inverse, status):
 class PagedCache:
     """A paged cache in the caller's tensors; keeps them alive, writes nothing but pages.
 
-    pages       bf16 or fp16 [num_pages, Hkv, 2, page_size, d], or uint8 [num_pages, Hkv, page_size / 16, 18 d]: 4 bits
+    pages       bf16 or fp16 [num_pages, Hkv, 2, page_size, d], or uint8 [num_pages, Hkv, page_size / 16, 18 d]: 4 bits,
+                [..., 32 d + 16]: 8 bits, E4M3 with a power of two for each block of 16 positions and head
     page_table  int32 [batch, max_pages]: position p of sequence b lies in page page_table[b, p // page_size]
     lengths     int32 [batch]: positions of each sequence, the step's own included; read by every call, on the device
     k_gain, v_gain  fp32 [Hkv] > 0, 4 bits only: a value is code * scale * gain (1 if None)
@@ -249,9 +274,12 @@ class PagedCache:
             _refuse(w, "pages is not contiguous, or empty")
         c = PagedDesc()
         if pages.dtype == torch.uint8:
-            if pages.dim() != 4 or pages.shape[3] not in (18 * 64, 18 * 128):
-                _refuse(w, "4-bit pages are [num_pages, Hkv, page_size / 16, 18 d], d 64 or 128, not %s" % list(pages.shape))
-            c.kv_type, c.head_dim, c.page_size = TKV_INT4, pages.shape[3] // 18, pages.shape[2] * 16
+            found = _RECORDS.get(pages.shape[3]) if pages.dim() == 4 else None
+            if found is None:
+                _refuse(w, "4-bit pages are [num_pages, Hkv, page_size / 16, 18 d], 8-bit ones [..., 32 d + 16], d 64 or 128, not %s" % list(pages.shape))
+            (c.kv_type, c.head_dim), c.page_size = found, pages.shape[2] * 16
+            if c.kv_type == TKV_E4M3 and (k_gain is not None or v_gain is not None):
+                _refuse(w, "gains belong to 4-bit pages")
         else:
             if pages.dtype not in (torch.bfloat16, torch.float16) or pages.dim() != 5 or pages.shape[2] != 2:
                 _refuse(w, "16-bit pages are bf16 or fp16 [num_pages, Hkv, 2, page_size, d], not %s %s" % (pages.dtype, list(pages.shape)))
@@ -281,16 +309,18 @@ class PagedCache:
         self.pages, self.page_table, self.lengths, self.k_gain, self.v_gain = pages, page_table, lengths, k_gain, v_gain
         self.device, self.num_kv_heads, self.head_dim, self.page_size = pages.device, c.num_kv_heads, c.head_dim, c.page_size
         self.batch, self.max_pages, self.is_int4 = c.batch, c.max_pages, c.kv_type == TKV_INT4
+        self._any16 = c.kv_type in (TKV_INT4, TKV_E4M3)   # pages that take rows of either 16-bit type
         # what each call reads of the descriptor, without a ctypes access
         self._c, self._kv_type, self._cu_shape, self._index = c, c.kv_type, (c.batch + 1,), pages.get_device()
         self._sizes = {}   # of workspaces
 
     @classmethod
     def empty(cls, num_pages, page_table, lengths, *, num_kv_heads, head_dim, page_size, dtype="int4", k_gain=None, v_gain=None):
-        """A cache with new pages on the page table's device; dtype "int4", torch.bfloat16 or torch.float16."""
+        """A cache with new pages on the page table's device; dtype "int4", "e4m3", torch.bfloat16 or torch.float16."""
         torch = _types()
-        if dtype == "int4":
-            pages = torch.zeros(num_pages, num_kv_heads, page_size // 16, 18 * head_dim, dtype=torch.uint8, device=page_table.device)
+        if dtype == "int4" or dtype == "e4m3":
+            record = 18 * head_dim if dtype == "int4" else 32 * head_dim + 16
+            pages = torch.zeros(num_pages, num_kv_heads, page_size // 16, record, dtype=torch.uint8, device=page_table.device)
         else:
             pages = torch.zeros(num_pages, num_kv_heads, 2, page_size, head_dim, dtype=dtype, device=page_table.device)
         return cls(pages, page_table, lengths, k_gain, v_gain)
@@ -298,14 +328,14 @@ class PagedCache:
     def _rows(self, x, where, what, heads):
         """x [rows, heads, d] of a 16-bit type that fits the pages, 16-byte pieces; its element type."""
         dt = _DTYPES.get(x.dtype) if isinstance(x, _torch.Tensor) else None
-        if dt == self._kv_type or (self.is_int4 and (dt == TKV_BF16 or dt == TKV_FP16)):
+        if dt == self._kv_type or (self._any16 and (dt == TKV_BF16 or dt == TKV_FP16)):
             shape, s = x.shape, x.stride()
             if (len(shape) == 3 and shape[2] == self.head_dim and (heads is None or shape[1] == heads) and s[2] == 1 and
                     not (s[0] | s[1]) % 8 and not x.data_ptr() % 16 and x.get_device() == self._index and x.is_cuda):
                 return dt
         _on(x, where, what, None, 3, self.device)
         dt = _DTYPES.get(x.dtype)
-        if dt == TKV_FP32 or dt is None or (not self.is_int4 and dt != self._kv_type):
+        if dt == TKV_FP32 or dt is None or (not self._any16 and dt != self._kv_type):
             _refuse(where, "%s is %s, the pages are %s" % (what, x.dtype, self.pages.dtype))
         if x.shape[2] != self.head_dim or (heads is not None and x.shape[1] != heads):
             _refuse(where, "%s is %s, not [rows, %s, %d]" % (what, list(x.shape), heads or "Hq", self.head_dim))
@@ -328,17 +358,7 @@ class PagedCache:
         if size is None:
             with _torch.cuda.device(self._index):
                 size = self._sizes[hq, max_new] = load().tkv_paged_attention_workspace(self._c, hq, max_new)
-        if _current_device() != self._index or _capturing():
-            return _torch.empty(size, dtype=_torch.uint8, device=self.device)
-        try:
-            kept = _own.work
-        except AttributeError:
-            kept = _own.work = {}
-        key = self._index, _raw_stream(self._index)
-        work = kept.get(key)
-        if work is None or work.numel() < size:
-            work = kept[key] = _torch.empty(size, dtype=_torch.uint8, device=self.device)
-        return work
+        return _workspace(size, self._index, self.device)
 
     def append(self, k, v, cu_tokens, rotary=None, positions=None, status=None):
         """Writes k, v [rows, Hkv, d] (bf16 or fp16) to their places, k rotated on the way if `rotary` is given:
@@ -443,3 +463,91 @@ class PagedCache:
                   None if lse is None else lse.data_ptr(), dt, rows, hq, qs[0], qs[1], os_[0], os_[1], cu_tokens.data_ptr(),
                   max_new, max_len, window, scale, work.data_ptr(), work.numel(), _status_ptr(status, w, self.device))
         return (out, lse) if return_lse else out
+
+
+class PagedLayers:
+    """The caches of a model's layers, which share a page table and lengths; keeps them alive.
+
+    Sequences come in groups of beams: sequence g * beams + w is beam w of group g."""
+
+    def __init__(self, caches):
+        _types()
+        w, caches = "PagedLayers", list(caches)
+        if not caches or not all(isinstance(c, PagedCache) for c in caches):
+            _refuse(w, "caches is a list of PagedCache, not empty")
+        first = caches[0]
+        for c in caches:
+            if c.page_table is not first.page_table and c.page_table.data_ptr() != first.page_table.data_ptr():
+                _refuse(w, "the caches have to share one page table")
+            if c.lengths is not first.lengths and c.lengths.data_ptr() != first.lengths.data_ptr():
+                _refuse(w, "the caches have to share one lengths")
+            if (c.batch, c.max_pages, c.page_size, c._index) != (first.batch, first.max_pages, first.page_size, first._index):
+                _refuse(w, "the caches differ in batch, pages a sequence, page size or device")
+        self.caches, self.batch, self.device, self._index = caches, first.batch, first.device, first._index
+        self._c = (PagedDesc * len(caches))(*(c._c for c in caches))
+
+    def reorder(self, parents, status=None):
+        """Sequence g * beams + w goes on from g * beams + parents[g, w]; parents int32 [groups, beams], as beam_select gives
+        `beams`; a negative one keeps what the sequence has.
+
+        The page table's columns before the current page (lengths // page_size) become the parent's; what the current page holds
+        is copied in all layers.  The pages from the current one on have to be each sequence's own, those before may be
+        shared.  To hand a prompt that sequence w has appended to its group: parents of w, with the lengths of all set."""
+        w = "reorder"
+        if not (isinstance(parents, _torch.Tensor) and parents.dtype is _int32 and parents.is_cuda and parents.get_device() == self._index):
+            _on(parents, w, "parents", _int32, 2, self.device)
+        shape = parents.shape
+        if len(shape) != 2 or shape[0] * shape[1] != self.batch or not parents.is_contiguous():
+            _refuse(w, "parents are contiguous int32 [groups, beams], %d sequences, not %s" % (self.batch, list(shape)))
+        if not 1 <= shape[1] <= 32:
+            _refuse(w, "%d beams: 1 to 32" % shape[1])
+        _call(load().tkv_paged_reorder, w, self._index, self._c, len(self.caches), parents.data_ptr(), shape[1],
+              _status_ptr(status, w, self.device))
+
+
+def beam_select(logits, scores, count=None, finished=None, eos=None):
+    """The best `count` (the number of beams if None) continuations of each sequence: (scores fp32, beams int32, tokens int32), each
+    [batch, count], in descending order, ties to the lowest beam and token.
+
+    logits    [batch, beams, vocab] bf16, fp16 or fp32, the vocabulary contiguous: any strides and alignment of the rows
+    scores    fp32 [batch, beams]: sums of log probabilities so far; -inf takes a beam out
+    finished  bool or uint8 [batch, beams]: such a beam offers token `eos` with its own score, and nothing else
+    A candidate's score is scores + log_softmax(logits); where there are fewer than `count`, score -inf, beam -1, token -1.
+    The call has no gradient."""
+    w, torch = "beam_select", _types()
+    _on(logits, w, "logits", None, 3)
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        _refuse(w, "logits is %s: bf16, fp16 or fp32" % logits.dtype)
+    batch, beams, vocab = logits.shape
+    index, device, s = logits.get_device(), logits.device, logits.stride()
+    count = beams if count is None else int(count)
+    if not 1 <= beams <= 64 or not 1 <= count <= 64 or vocab < 1 or beams * vocab > 0x7FFFFF00 or batch * beams > 0x7FFFFFFF // 64:
+        _refuse(w, "%s logits, count %d: beams and count are 1 to 64, beams * vocab is below 2^31 - 256" % (list(logits.shape), count))
+    if vocab > 1 and s[2] != 1:
+        _refuse(w, "the vocabulary has to be contiguous")
+    if not (isinstance(scores, torch.Tensor) and scores.dtype is torch.float32 and scores.is_cuda and scores.get_device() == index):
+        _on(scores, w, "scores", torch.float32, 2, device)
+    if scores.shape != (batch, beams) or not scores.is_contiguous():
+        _refuse(w, "scores is a contiguous [%d, %d]" % (batch, beams))
+    done = None
+    if finished is not None:
+        _on(finished, w, "finished", None, 2, device)
+        if finished.dtype not in (torch.bool, torch.uint8) or finished.shape != (batch, beams) or not finished.is_contiguous():
+            _refuse(w, "finished is a contiguous bool or uint8 [%d, %d]" % (batch, beams))
+        if eos is None or not 0 <= int(eos) < vocab:
+            _refuse(w, "eos is %s: a token of the vocabulary" % eos)
+        done = finished.data_ptr()
+    out = torch.empty((batch, count), dtype=torch.float32, device=device)
+    out_beams = torch.empty((batch, count), dtype=_int32, device=device)
+    tokens = torch.empty((batch, count), dtype=_int32, device=device)
+    if batch:
+        key = index, dt, batch, beams, vocab, count
+        size = _select_sizes.get(key)
+        if size is None:
+            with torch.cuda.device(index):
+                size = _select_sizes[key] = load().tkv_beam_select_workspace(dt, batch, beams, vocab, count)
+        work = _workspace(size, index, device)
+        _call(load().tkv_beam_select, w, index, logits.data_ptr(), dt, batch, beams, vocab, s[0], s[1], scores.data_ptr(), done,
+              0 if eos is None else int(eos), count, out.data_ptr(), out_beams.data_ptr(), tokens.data_ptr(), work.data_ptr(), work.numel())
+    return out, out_beams, tokens
