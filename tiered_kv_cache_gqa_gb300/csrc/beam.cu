@@ -5,15 +5,16 @@
 // lower w V + v first where totals are equal.  Within a row (a beam's logits) the order is that of x itself, so a row's best `count`
 // by (x, v) are all that it can bring.  One pass over the logits: a CTA takes a chunk of a row, 16 KB at a time in registers, and
 // keeps per thread a running maximum and sum of exponentials, per CTA the best `count` so far.  A second kernel, started
-// early, joins a sequence's chunks: totals in 64 bits (two beams' totals may lie as near as fp32's rounding), the best of them.
+// early, joins a sequence's chunks.
 //
-// The best of a tile.  The count-th largest of the 256 threads' maxima (each with its place, so no two are equal) is a bound:
-// `count` values at least reach it, and only the `count` threads whose maxima do can hold any, so at most count * 32 are looked
-// at, whatever the values are: no distribution and no number of ties makes the list overflow.  Once the list is
-// full only values above its last one are looked at, which after the first tiles are few.
+// The best of a chunk.  In the first tile the count-th largest of the 256 threads' maxima (each with its place, so no two are
+// equal) is a bound: `count` values at least reach it, and only the `count` threads whose maxima do can hold any, so at most
+// count * 32 values come into the list, whatever they are.  From then on values above the bound are added without a barrier, and the
+// list is sorted, and the bound raised, after tiles 2, 4, 8, ..: of values in random order each stretch brings about `count`.
+// Values that rise along the vocabulary can overflow the list: the chunk is then looked over again, every tile like the first.
 //
-// What bounds it is memory, then issue: an element costs about seven instructions (unpack, maximum, difference, product,
-// exponential, sum).
+// What bounds it is memory, then issue: a 16-bit value costs four instructions (half of a maximum, one to unpack, half a difference, half a
+// product, an exponential, half a sum).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -28,7 +29,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCount = 64, kMaxBeams = 64;
 constexpr int kVectors = 4;                       // 16-byte pieces of a thread and tile
 constexpr int kCtas = 4;                          // on an SM at once, by their registers
-constexpr int kMostCandidates = 8192;             // of a sequence, for the joining kernel
+constexpr int kIndexBits = 13;                    // of a candidate's index in the joining kernel
+constexpr int kMostCandidates = 1 << kIndexBits;  // of a sequence
 constexpr float kLog2E = 1.44269504f;
 constexpr float kFloor = -3.402823466e38f;        // a maximum before anything is seen
 
@@ -53,52 +55,109 @@ struct SelectArgs {
     int batch, beams, vocab, eos, count, chunks, per_chunk;
 };
 
-// Larger is better: the value first, the lower place next.
-__device__ __forceinline__ uint64_t key_of(float x, int v) {
+__device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);   // -0 is 0
-    const uint32_t ordered = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return (uint64_t)ordered << 32 | (uint32_t)~v;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ Candidate of_key(uint64_t key) {
-    const uint32_t o = (uint32_t)(key >> 32);
-    return Candidate{__uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o), (int)~(uint32_t)key};
-}
+__device__ __forceinline__ float of_ordered(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o); }
+
+// Larger is better: the value first, the lower place next.  0 is none.
+__device__ __forceinline__ uint64_t key_of(float x, int v) { return (uint64_t)ordered(x) << 32 | (uint32_t)~v; }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 
 // A beam that brings nothing of its logits: finished, or with a score that is not finite.
 __device__ __forceinline__ bool is_out(const SelectArgs& a, int row) {
-    const float s = a.scores[row];
-    return !(fabsf(s) < INFINITY) || (a.finished && a.finished[row]);
+    return !(fabsf(a.scores[row]) < INFINITY) || (a.finished && a.finished[row]);
 }
 
-// A value that is left out: an infinity below, like what lies behind the vocabulary.
-template <typename T, int E>
-__device__ __forceinline__ void unpack16(uint4 u, float (&x)[E]) {
-    if (sizeof(T) == 4) {
-        x[0] = __uint_as_float(u.x);
-        x[1] = __uint_as_float(u.y);
-        x[2 % E] = __uint_as_float(u.z);
-        x[3 % E] = __uint_as_float(u.w);
-    } else {
-        Vec16<T> w;
-        w.u = u;
+// *bound = the k-th largest of the threads' keys (those that are not 0 are different, and at least k).  A warp sorts its own, a
+// key's rank is then found by a binary search in each other warp's.  A barrier follows before `bound` is read; `sorted` may be
+// written again behind another.
+__device__ __forceinline__ void kth_largest(uint64_t mine, int k, uint64_t (&sorted)[kThreads], uint64_t* bound) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = to_float(w.e[i]);
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+        for (int o = n >> 1; o; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, mine, o);
+            const bool high = ((lane & n) == 0) == ((lane & o) == 0);   // keeps the larger of the two
+            mine = (other > mine) == high ? other : mine;
+        }
+    sorted[threadIdx.x] = mine;   // descending within the warp
+    __syncthreads();
+    int rank = lane;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        const uint64_t* list = sorted + ((warp + w) & (kWarps - 1)) * 32;
+        int c = 0;
+#pragma unroll
+        for (int s = 16; s; s >>= 1) c += list[c + s - 1] > mine ? s : 0;
+        rank += c + (list[c] > mine);
     }
+    if (mine && rank == k - 1) *bound = mine;
+}
+
+// The best `count` of keys[0 .. n) (all different) into list, in order.  Barriers around it are the caller's.
+__device__ __forceinline__ void sort_best(const uint64_t* keys, int n, int count, uint64_t* list) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t k = keys[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += keys[j] > k;
+        if (rank < count) list[rank] = k;
+    }
+}
+
+// The values of a piece, two at a time.
+template <typename T>
+__device__ __forceinline__ float2 two_of(uint4 u, int i) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+// The largest of a thread's pieces; NaN counts only where nothing else is.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 (&raw)[kVectors]) {
+    float top = -INFINITY;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) top = fmaxf(fmaxf(fmaxf(top, __uint_as_float(raw[i].x)), fmaxf(__uint_as_float(raw[i].y), __uint_as_float(raw[i].z))), __uint_as_float(raw[i].w));
+    } else {
+        using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        P m[4];
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const P x = *reinterpret_cast<const P*>(&w[j]);
+                m[j] = i ? __hmax2(m[j], x) : x;
+            }
+        }
+        const P x = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+        top = fmaxf(fmaxf(top, to_float(x.x)), to_float(x.y));
+    }
+    return top;
 }
 
 // blockIdx.x: chunk, blockIdx.y (and z, behind 65,535 rows): row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __grid_constant__ SelectArgs a) {
     constexpr int E = 16 / sizeof(T), N = kVectors * E;         // values of a piece, of a thread and tile
-    constexpr int kMost = kMaxCount * N + kMaxCount;            // values that are looked at
-    __shared__ uint64_t keys[kMost];                             // the list, then what a tile adds to it
-    __shared__ uint64_t list[kMaxCount];
-    __shared__ uint64_t maxima[kThreads];
+    constexpr int kMost = kMaxCount * N + kMaxCount;            // values in the list: what one tile can bring, and the best so far
+    constexpr int kTile = kVectors * kThreads;                  // pieces
+    __shared__ uint64_t keys[kMost], list[kMaxCount], sorted[kThreads];
     __shared__ uint64_t bound;
     __shared__ int found;
     __shared__ Stat stats[kWarps];
@@ -108,92 +167,150 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     if (row >= a.batch * a.beams || is_out(a, row)) return;
     const int b = row / a.beams, w = row - b * a.beams;
     const T* x0 = reinterpret_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
-    // Pieces are counted from the 16-byte boundary at or before the row: the first and the last one may be cut.
+    // Piece p is values p E .. p E + E - 1 of the row wherever the row begins, so that equal rows have equal sums: of a row that does not
+    // begin on 16 bytes it is put together from two of memory's pieces.
     const int shift = (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
-    const uint4* pieces = reinterpret_cast<const uint4*>(x0 - shift);
-    const int first = blockIdx.x * a.per_chunk, end = min(first + a.per_chunk, (a.vocab + shift + E - 1) / E);
-    constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    const uint4* memory = reinterpret_cast<const uint4*>(x0 - shift);
+    const int first = blockIdx.x * a.per_chunk, end = min(first + a.per_chunk, (a.vocab + E - 1) / E);
+    constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;   // -infinity
     auto load = [&](int p) {
         uint4 u = make_uint4(kNone, kNone, kNone, kNone);
         if (p >= end) return u;
-        const int v0 = p * E - shift;
-        if (v0 >= 0 && v0 + E <= a.vocab) return pieces[p];
+        if (shift == 0 ? p * E + E <= a.vocab : p > 0 && (p + 2) * E - shift <= a.vocab) {
+            u = memory[p];
+            if (shift) {
+                const uint4 v = memory[p + 1];
+                const uint64_t q[4] = {u.x | (uint64_t)u.y << 32, u.z | (uint64_t)u.w << 32, v.x | (uint64_t)v.y << 32, v.z | (uint64_t)v.w << 32};
+                const int bits = shift * (int)sizeof(T) * 8;   // 8 .. 120
+                const bool far = bits >= 64;
+                const uint64_t q0 = far ? q[1] : q[0], q1 = far ? q[2] : q[1], q2 = far ? q[3] : q[2];
+                const int by = bits & 63;
+                const uint64_t r0 = by ? q0 >> by | q1 << (64 - by) : q0, r1 = by ? q1 >> by | q2 << (64 - by) : q1;
+                u = make_uint4((uint32_t)r0, (uint32_t)(r0 >> 32), (uint32_t)r1, (uint32_t)(r1 >> 32));
+            }
+            return u;
+        }
         Vec16<T> part;
         part.u = u;
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (v0 + i >= 0 && v0 + i < a.vocab) part.e[i] = x0[v0 + i];
+            if (p * E + i < a.vocab) part.e[i] = x0[p * E + i];
         return part.u;
     };
-    float m = kFloor, sum = 0.0f, last = -INFINITY;   // last: the list's last value once it is full
-    int held = 0;
-    uint4 raw[kVectors];
+    float m = kFloor, sum = 0.0f;
+    float lowest = -INFINITY;      // values below it are none of the best; the bound's
+    uint64_t least = 0;            // the bound: keys below it are none of the best
+    int held = 0, sort_at = 1;     // tiles after which the list is sorted next
+    bool careful = false;          // every tile like the first: the second time over a chunk
+    uint4 next[kVectors];
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) raw[i] = load(first + i * kThreads + tid);
+    for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
+    if (tid == 0) found = 0;
 #pragma unroll 1
-    for (int p = first; p < end; p += kVectors * kThreads) {
-        float x[N];
+    for (int p = first, tile = 1; p < end; p += kTile, ++tile) {
+        uint4 raw[kVectors];
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
-            float y[E];
-            unpack16<T, E>(raw[i], y);
-#pragma unroll
-            for (int j = 0; j < E; ++j) x[i * E + j] = y[j];
+            raw[i] = next[i];
+            next[i] = load(p + (kVectors + i) * kThreads + tid);
         }
+        const float top = largest<T>(raw);
+        if (!careful) {
+            if (top > m) {
+                sum *= exp2_fast((m - top) * kLog2E);
+                m = top;
+            }
+            F2 s[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+            const F2 minus = f2(-m, -m), log2e = f2(kLog2E, kLog2E);
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i) raw[i] = load(p + (kVectors + i) * kThreads + tid);   // the next tile's
-        float top = x[0];
+            for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-        for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-        if (top > m) {
-            sum *= exp2_fast((m - top) * kLog2E);
-            m = top;
+                for (int j = 0; j < E / 2; ++j) {
+                    const float2 x = two_of<T>(raw[i], j), y = parts(mul2(add2(f2(x.x, x.y), minus), log2e));
+                    s[j & 1] = add2(s[j & 1], f2(exp2_fast(y.x), exp2_fast(y.y)));
+                }
+            const float2 both = parts(add2(s[0], s[1]));
+            sum += both.x + both.y;
         }
-        float s[2] = {0.0f, 0.0f};
+        // ---- the tile's part of the best
+        auto place = [&](int i, int j) { return (p + i * kThreads + tid) * E + j; };
+        const bool sorts = careful || tile == sort_at || p + kTile >= end;
+        if (tile == 1 || careful) {
+            const int above = __syncthreads_count(top > -INFINITY && top >= lowest);
+            if (above > a.count) {
+                int at = 0x7FFFFFFF;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2E);
-        sum += s[0] + s[1];
-        // ---- the tile's part of the best.  Places grow from tile to tile, so an equal value comes too late.
-        const int above = __syncthreads_count(top > last);
-        if (above == 0) continue;
-        uint64_t least = 0;                            // 0: whatever is above the list
-        auto place = [&](int i) { return (p + (i / E) * kThreads + tid) * E - shift + i % E; };
-        if (above > a.count) {
-            int at = 0;
+                for (int i = kVectors - 1; i >= 0; --i)
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) at = x[i] == top ? i : at;
-            const uint64_t mine = top > last ? key_of(top, place(at)) : 0;
-            maxima[tid] = mine;
+                    for (int j = E / 2 - 1; j >= 0; --j) {
+                        const float2 x = two_of<T>(raw[i], j);
+                        if (x.y == top) at = place(i, 2 * j + 1);
+                        if (x.x == top) at = place(i, 2 * j);
+                    }
+                const uint64_t mine = top > -INFINITY && top >= lowest ? key_of(top, at) : 0;
+                kth_largest(mine, a.count, sorted, &bound);
+                __syncthreads();
+                if (bound > least) {
+                    least = bound;
+                    lowest = of_ordered((uint32_t)(least >> 32));
+                }
+            }
+        }
+        if (top >= lowest && top > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i)
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float2 two = two_of<T>(raw[i], j / 2);
+                    const float x = j & 1 ? two.y : two.x;
+                    if (x >= lowest && x > -INFINITY) {
+                        const uint64_t k = key_of(x, place(i, j));
+                        if (k >= least) {
+                            const int slot = atomicAdd(&found, 1);
+                            if (slot < kMost) keys[slot] = k;
+                        }
+                    }
+                }
+        }
+        if (!sorts) continue;
+        sort_at *= 2;
+        __syncthreads();
+        const int n = found;
+        if (n > kMost) {           // only if not careful: a tile like the first brings no more than there is room for
             __syncthreads();
-            int rank = 0;
-#pragma unroll 8
-            for (int i = 0; i < kThreads; ++i) rank += maxima[i] > mine;
-            if (mine && rank == a.count - 1) bound = mine;
+            careful = true;
+            least = 0;
+            lowest = -INFINITY;
+            held = 0;
+            if (tid == 0) found = 0;
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
+            // what is left of the sum
+            for (int q = p + kTile; q < end; q += kTile) {
+                for (int i = 0; i < kVectors; ++i) {
+                    const uint4 u = load(q + i * kThreads + tid);
+                    for (int j = 0; j < E / 2; ++j) {
+                        const float2 x = two_of<T>(u, j);
+                        const float t = fmaxf(m, fmaxf(x.x, x.y));
+                        sum = sum * exp2_fast((m - t) * kLog2E) + exp2_fast((x.x - t) * kLog2E) + exp2_fast((x.y - t) * kLog2E);
+                        m = t;
+                    }
+                }
+            }
+            p = first - kTile;
+            __syncthreads();
+            continue;
+        }
+        sort_best(keys, n, a.count, list);
+        held = min(n, a.count);
+        __syncthreads();
+        if (held == a.count) {
+            least = list[a.count - 1] + 1;
+            lowest = of_ordered((uint32_t)(least >> 32));
         }
         if (tid < held) keys[tid] = list[tid];
         if (tid == 0) found = held;
         __syncthreads();
-        if (above > a.count) least = bound;
-        if (top > last) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (x[i] > last) {
-                    const uint64_t k = key_of(x[i], place(i));
-                    if (k >= least) keys[atomicAdd(&found, 1)] = k;
-                }
-        }
-        __syncthreads();
-        const int n = found;
-        for (int i = tid; i < n; i += kThreads) {
-            const uint64_t k = keys[i];
-            int rank = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) rank += keys[j] > k;
-            if (rank < a.count) list[rank] = k;
-        }
-        __syncthreads();
-        held = min(n, a.count);
-        if (held == a.count) last = of_key(list[a.count - 1]).x;
     }
     // ---- the chunk's reference and sum
 #pragma unroll
@@ -215,101 +332,121 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         }
         a.stats[at] = t;
     }
-    if (tid < a.count) a.best[at * a.count + tid] = tid < held ? of_key(list[tid]) : Candidate{0.0f, -1};
+    if (tid < a.count) a.best[at * a.count + tid] = tid < held ? Candidate{of_ordered((uint32_t)(list[tid] >> 32)), (int)~(uint32_t)list[tid]} : Candidate{0.0f, -1};
 }
 
-// A candidate of a sequence: its total as an ordered number, its place w V + v.
-struct Total {
-    uint64_t total;   // 0: none
-    uint32_t place;
+// ------------------------------------------------------------------ joining
+// Totals are sums of two fp32 numbers, good to 2^-46 or so: fp64 instructions are few and slow here (20 us for this kernel with them).
+struct Wide {
+    float hi, lo;   // hi is the nearest to hi + lo
 };
-__device__ __forceinline__ bool better(const Total& a, const Total& b) { return a.total > b.total || (a.total == b.total && a.place < b.place); }
-__device__ __forceinline__ Total total_of(double t, int w, int v, int vocab) {
-    if (!(t > -INFINITY)) return Total{0, 0xFFFFFFFFu};
-    const uint64_t u = (uint64_t)__double_as_longlong(t + 0.0);   // no negative zero
-    return Total{u >> 63 ? ~u : u | (uint64_t)1 << 63, (uint32_t)w * (uint32_t)vocab + (uint32_t)v};
+__device__ __forceinline__ Wide sum_of(float a, float b) {   // exactly
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Wide{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double value_of(uint64_t o) { return __longlong_as_double((long long)(o >> 63 ? o & 0x7FFFFFFFFFFFFFFFull : ~o)); }
+__device__ __forceinline__ Wide plus(Wide a, Wide b) {
+    const Wide s = sum_of(a.hi, b.hi), t = sum_of(a.lo, b.lo);
+    const float e = __fadd_rn(s.lo, t.hi), h = __fadd_rn(s.hi, e), l = __fadd_rn(__fsub_rn(e, __fsub_rn(h, s.hi)), t.lo);
+    const float hi = __fadd_rn(h, l);
+    return Wide{hi, __fsub_rn(l, __fsub_rn(hi, h))};
+}
+// log x, x > 0 and finite: its power of two apart, so that what logf rounds lies below 0.35.
+__device__ __forceinline__ Wide log_of(float x) {
+    const int e = ((int)(__float_as_uint(x) - 0x3F3504F3u) >> 23);                     // x = m 2^e, m in [sqrt 1/2, sqrt 2)
+    const float m = __int_as_float(__float_as_int(x) - (e << 23)), k = (float)e;
+    return plus(sum_of(__fmul_rn(k, 0.693145751953125f), __fmul_rn(k, 1.42860682030941723e-6f)), Wide{logf(m), 0.0f});   // ln 2 in 16 bits, and the rest
+}
 
-// One CTA a sequence.
+// One CTA a sequence.  A candidate's key: its total, to 2^-43 of it, then the lower index (w, chunk, place in the chunk's list): among
+// equal totals that is the lower place w V + v.
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_constant__ SelectArgs a) {
     constexpr int kEach = kMostCandidates / kThreads;             // candidates of a thread
-    __shared__ double reference[kMaxBeams], offset[kMaxBeams];    // total = (x - reference) + offset
-    __shared__ Total maxima[kThreads];
-    __shared__ Total keys[kMaxCount * kEach + kMaxBeams];
-    __shared__ Total bound;
+    __shared__ float reference[kMaxBeams];
+    __shared__ Wide offset[kMaxBeams];                            // total = (x - reference) + offset
+    __shared__ uint64_t keys[kMaxCount * kEach], list[kMaxCount], sorted[kThreads];
+    __shared__ uint64_t bound;
     __shared__ int found;
     wait_for_previous();
-    const int b = blockIdx.x, tid = threadIdx.x, per_row = a.chunks * a.count, n = a.beams * per_row;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, per_row = a.chunks * a.count, n = a.beams * per_row;
     const Candidate* best = a.best + (int64_t)b * n;
-    if (tid < a.beams) {
-        const int row = b * a.beams + tid;
-        double o = NAN, r = 0.0;
-        if (!is_out(a, row)) {
-            const Stat* s = a.stats + (int64_t)row * a.chunks;
-            float top = kFloor;
-            for (int i = 0; i < a.chunks; ++i) top = fmaxf(top, s[i].m);
-            double sum = 0.0;
-            for (int i = 0; i < a.chunks; ++i) sum += (double)(s[i].sum * exp2_fast((s[i].m - top) * kLog2E));
-            r = (double)top;
-            o = (double)a.scores[row] - log(sum);
+    for (int w = tid >> 5; w < a.beams; w += kWarps) {            // a warp a beam
+        const int row = b * a.beams + w;
+        const float score = a.scores[row];
+        Wide o{NAN, 0.0f};
+        float top = kFloor;
+        if (fabsf(score) < INFINITY) {
+            if (a.finished && a.finished[row]) {
+                o = Wide{score, 0.0f};
+            } else {
+                const Stat* s = a.stats + (int64_t)row * a.chunks;
+                for (int i = lane; i < a.chunks; i += 32) top = fmaxf(top, s[i].m);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                Wide sum{0.0f, 0.0f};
+                for (int i = lane; i < a.chunks; i += 32) sum = plus(sum, Wide{s[i].sum * exp2_fast((s[i].m - top) * kLog2E), 0.0f});
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+                if (sum.hi > 0.0f && sum.hi < INFINITY) {   // not: a NaN or an infinity among the logits, or nothing above -infinity
+                    Wide l = log_of(sum.hi);
+                    l = plus(l, Wide{__fdividef(sum.lo, sum.hi), 0.0f});
+                    o = plus(Wide{score, 0.0f}, Wide{-l.hi, -l.lo});
+                }
+            }
         }
-        reference[tid] = r;
-        offset[tid] = o;
+        if (lane == 0) {
+            reference[w] = top;
+            offset[w] = o;
+        }
     }
-    if (tid == 0) found = 0;
+    if (tid == 0) {
+        found = 0;
+        bound = 1;   // below every candidate
+    }
     __syncthreads();
-    auto total_at = [&](int i) {   // candidate i of the sequence
+    // Candidate i of the sequence.  Thread t takes t, t + 256, ..
+    auto key_at = [&](int i) -> uint64_t {
         const int w = i / per_row;
-        if (isnan(offset[w])) return Total{0, 0xFFFFFFFFu};
-        const Candidate c = best[i];
-        return c.v < 0 ? Total{0, 0xFFFFFFFFu} : total_of(((double)c.x - reference[w]) + offset[w], w, c.v, a.vocab);
-    };
-    Total mine{0, 0xFFFFFFFFu};
-    if (tid < a.beams) {   // a finished beam's one candidate
-        const int row = b * a.beams + tid;
-        if (a.finished && a.finished[row] && fabsf(a.scores[row]) < INFINITY) mine = total_of((double)a.scores[row], tid, a.eos, a.vocab);
-    }
-    const Total own = mine;
-    for (int i = tid; i < n; i += kThreads) {
-        const Total t = total_at(i);
-        if (better(t, mine)) mine = t;
-    }
-    maxima[tid] = mine;
-    if (tid == 0) bound = Total{1, 0xFFFFFFFFu};   // below every candidate
-    __syncthreads();
-    if (mine.total) {
-        int rank = 0;
-#pragma unroll 4
-        for (int i = 0; i < kThreads; ++i) rank += better(maxima[i], mine);
-        if (rank == a.count - 1) bound = mine;
-    }
-    __syncthreads();
-    const Total least = bound;
-    if (mine.total && !better(least, mine)) {
-        if (own.total && !better(least, own)) keys[atomicAdd(&found, 1)] = own;
-        for (int i = tid; i < n; i += kThreads) {
-            const Total t = total_at(i);
-            if (t.total && !better(least, t)) keys[atomicAdd(&found, 1)] = t;
+        const Wide o = offset[w];
+        if (isnan(o.hi)) return 0;
+        Wide t = o;
+        if (a.finished && a.finished[b * a.beams + w]) {
+            if (i != w * per_row) return 0;
+        } else {
+            const Candidate c = best[i];
+            if (c.v < 0) return 0;
+            t = plus(sum_of(c.x, -reference[w]), o);
+            if (!(fabsf(t.hi) < INFINITY)) return 0;   // below the lowest number
         }
-    }
+        return (uint64_t)ordered(t.hi) << 32 | (ordered(t.lo) >> kIndexBits << kIndexBits) | (uint32_t)(kMostCandidates - 1 - i);
+    };
+    uint64_t mine = 0;
+    for (int i = tid; i < n; i += kThreads) mine = max(mine, key_at(i));
+    const int some = __syncthreads_count(mine != 0);
+    if (some > a.count) kth_largest(mine, a.count, sorted, &bound);
+    __syncthreads();
+    const uint64_t least = bound;
+    if (mine >= least)
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t k = key_at(i);
+            if (k >= least) keys[atomicAdd(&found, 1)] = k;
+        }
     __syncthreads();
     const int m = found;
-    const int64_t out = (int64_t)b * a.count;
-    for (int i = tid; i < m; i += kThreads) {
-        const Total t = keys[i];
-        int rank = 0;
-        for (int j = 0; j < m; ++j) rank += better(keys[j], t);
-        if (rank < a.count) {
-            const uint32_t w = t.place / (uint32_t)a.vocab;
-            a.out_scores[out + rank] = (float)value_of(t.total);
-            a.out_beams[out + rank] = (int)w;
-            a.out_tokens[out + rank] = (int)(t.place - w * (uint32_t)a.vocab);
+    sort_best(keys, m, a.count, list);
+    __syncthreads();
+    if (tid < a.count) {
+        const int64_t out = (int64_t)b * a.count + tid;
+        float score = -INFINITY;
+        int w = -1, v = -1;
+        if (tid < m) {
+            const int i = kMostCandidates - 1 - (int)(list[tid] & (kMostCandidates - 1));
+            w = i / per_row;
+            score = of_ordered((uint32_t)(list[tid] >> 32));
+            v = a.finished && a.finished[b * a.beams + w] ? a.eos : best[i].v;
         }
-    }
-    for (int i = m + tid; i < a.count; i += kThreads) {
-        a.out_scores[out + i] = -INFINITY;
-        a.out_beams[out + i] = a.out_tokens[out + i] = -1;
+        a.out_scores[out] = score;
+        a.out_beams[out] = w;
+        a.out_tokens[out] = v;
     }
 }
 
@@ -319,7 +456,7 @@ struct Split {
     int chunks, per_chunk;   // pieces of a chunk
 };
 Split split_rows(int64_t rows, int beams, int vocab, int count, int element, int sms) {
-    const int pieces = vocab / (16 / element) + 2;   // at most, whatever the row's alignment
+    const int pieces = (vocab + 16 / element - 1) / (16 / element);
     int64_t chunks = std::max<int64_t>(1, (int64_t)sms * kCtas / rows);
     chunks = std::min<int64_t>(chunks, (pieces + kThreads - 1) / kThreads);
     chunks = std::min<int64_t>(chunks, std::max(1, kMostCandidates / (beams * count)));
