@@ -7,14 +7,14 @@
 // keeps per thread a running maximum and sum of exponentials, per CTA the best `count` so far.  A second kernel, started
 // early, joins a sequence's chunks.
 //
-// The best of a chunk.  In the first tile the count-th largest of the 256 threads' maxima (each with its place, so no two are
-// equal) is a bound: `count` values at least reach it, and only the `count` threads whose maxima do can hold any, so at most
-// count * 32 values come into the list, whatever they are.  From then on values above the bound are added without a barrier, and the
+// The best of a chunk.  In the first tile the count-th largest of the maxima of groups of threads (each with its place, so no two are
+// equal) is a bound: `count` values at least reach it, and only the `count` groups whose maxima do can hold any, 128 threads at
+// most, so half a tile at most comes into the list, whatever the values are.  From then on values above the bound are added without a barrier, and the
 // list is sorted, and the bound raised, after tiles 2, 4, 8, ..: of values in random order each stretch brings about `count`.
 // Values that rise along the vocabulary can overflow the list: the chunk is then looked over again, every tile like the first.
 //
-// What bounds it is memory, then issue: a 16-bit value costs four instructions (half of a maximum, one to unpack, half a difference, half a
-// product, an exponential, half a sum).
+// What bounds it is memory, then issue: a 16-bit value costs three and a half instructions (half of a maximum, one to unpack, half a
+// fused multiply-add, an exponential, half a sum).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -29,9 +29,13 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCount = 64, kMaxBeams = 64;
 constexpr int kVectors = 4;                       // 16-byte pieces of a thread and tile
 constexpr int kCtas = 4;                          // on an SM at once, by their registers
-constexpr int kIndexBits = 13;                    // of a candidate's index in the joining kernel
+constexpr int kSortFirst = 2;                     // tiles before the list is sorted first, and each time as many times more
+constexpr int kIndexBits = 12;                    // of a candidate's index in the joining kernel
 constexpr int kMostCandidates = 1 << kIndexBits;  // of a sequence
+constexpr int kMostGroups = 128;
+constexpr int kFew = 128;                         // candidates of a sequence that are sorted whole
 constexpr float kLog2E = 1.44269504f;
+constexpr float kFar = 3e38f;
 constexpr float kFloor = -3.402823466e38f;        // a maximum before anything is seen
 
 struct Candidate {
@@ -68,9 +72,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
 
@@ -79,32 +83,26 @@ __device__ __forceinline__ bool is_out(const SelectArgs& a, int row) {
     return !(fabsf(a.scores[row]) < INFINITY) || (a.finished && a.finished[row]);
 }
 
-// *bound = the k-th largest of the threads' keys (those that are not 0 are different, and at least k).  A warp sorts its own, a
-// key's rank is then found by a binary search in each other warp's.  A barrier follows before `bound` is read; `sorted` may be
-// written again behind another.
-__device__ __forceinline__ void kth_largest(uint64_t mine, int k, uint64_t (&sorted)[kThreads], uint64_t* bound) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int n = 2; n <= 32; n <<= 1)
-#pragma unroll
-        for (int o = n >> 1; o; o >>= 1) {
-            const uint64_t other = __shfl_xor_sync(0xffffffffu, mine, o);
-            const bool high = ((lane & n) == 0) == ((lane & o) == 0);   // keeps the larger of the two
-            mine = (other > mine) == high ? other : mine;
-        }
-    sorted[threadIdx.x] = mine;   // descending within the warp
+// *bound = the k-th largest of the maxima of groups of 2^shift threads (their keys are different where they are not 0; at least k
+// groups have one).  A barrier follows before `bound` is read; `maxima` may be written again behind another.
+__device__ __forceinline__ void kth_largest(uint64_t mine, int k, int shift, uint64_t (&maxima)[kMostGroups], uint64_t* bound) {
+    for (int o = 1; o < 1 << shift; o <<= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    const int groups = kThreads >> shift, tid = threadIdx.x;
+    if ((tid & ((1 << shift) - 1)) == 0) maxima[tid >> shift] = mine;
     __syncthreads();
-    int rank = lane;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        const uint64_t* list = sorted + ((warp + w) & (kWarps - 1)) * 32;
-        int c = 0;
-#pragma unroll
-        for (int s = 16; s; s >>= 1) c += list[c + s - 1] > mine ? s : 0;
-        rank += c + (list[c] > mine);
+    if (tid >= groups) return;
+    mine = maxima[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < groups; i += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(maxima + i);
+        rank += (two.x > mine) + (two.y > mine);
     }
     if (mine && rank == k - 1) *bound = mine;
 }
+// Groups are as large as leaves twice as many of them as wanted, and at least 8: their k largest then reach little further down than
+// single threads' would, and k of them have at most 128 threads.
+__device__ __forceinline__ int group_shift(int k) { return min(5, 31 - __clz(kThreads / 2 / k)); }
 
 // The best `count` of keys[0 .. n) (all different) into list, in order.  Barriers around it are the caller's.
 __device__ __forceinline__ void sort_best(const uint64_t* keys, int n, int count, uint64_t* list) {
@@ -115,6 +113,18 @@ __device__ __forceinline__ void sort_best(const uint64_t* keys, int n, int count
         for (int j = 0; j < n; ++j) rank += keys[j] > k;
         if (rank < count) list[rank] = k;
     }
+}
+
+// 16 bytes from `shift` elements (not 0) into two pieces on.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(uint4 u, uint4 v, int shift) {
+    const int words = shift * (int)sizeof(T) / 4, bits = sizeof(T) == 4 ? 0 : (shift & 1) * 16;
+    uint32_t x0, x1, x2, x3, x4;
+    if (words == 0) x0 = u.x, x1 = u.y, x2 = u.z, x3 = u.w, x4 = v.x;
+    else if (words == 1) x0 = u.y, x1 = u.z, x2 = u.w, x3 = v.x, x4 = v.y;
+    else if (words == 2) x0 = u.z, x1 = u.w, x2 = v.x, x3 = v.y, x4 = v.z;
+    else x0 = u.w, x1 = v.x, x2 = v.y, x3 = v.z, x4 = v.w;
+    return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits), __funnelshift_r(x2, x3, bits), __funnelshift_r(x3, x4, bits));
 }
 
 // The values of a piece, two at a time.
@@ -151,20 +161,79 @@ __device__ __forceinline__ float largest(const uint4 (&raw)[kVectors]) {
     return top;
 }
 
+// Which of a thread's values reach `lowest`: a bit each, see value_of_bit.
+template <typename T>
+__device__ __forceinline__ uint32_t at_least(const uint4 (&raw)[kVectors], float lowest) {
+    uint32_t bits = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bits |= __uint_as_float(w[j]) >= lowest ? 1u << (4 * i + j) : 0u;
+        }
+    } else {
+        using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        P low;   // rounded up: no value of T lies in between
+        if constexpr (std::is_same<T, __half>::value) low = __half2half2(__float2half_ru(lowest));
+        else low = __bfloat162bfloat162(__float2bfloat16_ru(lowest));
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bits |= __hge2_mask(*reinterpret_cast<const P*>(&w[j]), low) & 0x00010001u << (4 * i + j);
+            }
+        }
+    }
+    return bits;
+}
+
+// 16 bits a value: the low halves of the words first, then the high ones.
+template <typename T>
+__device__ __forceinline__ int value_of_bit(int bit) { return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4); }
+
+// The value of a bit.
+template <typename T>
+__device__ __forceinline__ float value_at(const uint4 (&raw)[kVectors], int bit) {
+    uint4 u = bit & 8 ? (bit & 4 ? raw[3] : raw[2]) : (bit & 4 ? raw[1] : raw[0]);
+    const uint32_t w = bit & 2 ? (bit & 1 ? u.w : u.z) : (bit & 1 ? u.y : u.x);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    const uint16_t h = (uint16_t)(bit & 16 ? w >> 16 : w);
+    return to_float(*reinterpret_cast<const T*>(&h));
+}
+
+// The block's reference and sum, to every thread.  `stats` is written again behind a barrier.
+__device__ __forceinline__ Stat join_stats(Stat a, Stat b) {
+    const float top = fmaxf(a.m, b.m);
+    return Stat{top, a.sum * exp2_fast((a.m - top) * kLog2E) + b.sum * exp2_fast((b.m - top) * kLog2E)};
+}
+__device__ __forceinline__ Stat sum_block(Stat t, Stat (&stats)[kWarps]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t = join_stats(t, Stat{__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.sum, o)});
+    if ((threadIdx.x & 31) == 0) stats[threadIdx.x >> 5] = t;
+    __syncthreads();
+    t = stats[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) t = join_stats(t, stats[i]);
+    return t;
+}
+
 // blockIdx.x: chunk, blockIdx.y (and z, behind 65,535 rows): row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __grid_constant__ SelectArgs a) {
     constexpr int E = 16 / sizeof(T), N = kVectors * E;         // values of a piece, of a thread and tile
-    constexpr int kMost = kMaxCount * N + kMaxCount;            // values in the list: what one tile can bring, and the best so far
+    constexpr int kMost = 128 * N + kMaxCount;                  // values in the list: what one tile can bring, and the best so far
     constexpr int kTile = kVectors * kThreads;                  // pieces
-    __shared__ uint64_t keys[kMost], list[kMaxCount], sorted[kThreads];
+    __shared__ uint64_t keys[kMost], list[kMaxCount];
+    __shared__ __align__(16) uint64_t maxima[kMostGroups];
     __shared__ uint64_t bound;
     __shared__ int found;
     __shared__ Stat stats[kWarps];
-    let_next_start();
     wait_for_previous();
-    const int row = blockIdx.y + blockIdx.z * 65535, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (row >= a.batch * a.beams || is_out(a, row)) return;
+    let_next_start();   // not earlier: the joining kernel reads scores and finished before its own wait
+    const int row = blockIdx.y + blockIdx.z * 65535, tid = threadIdx.x, lane = tid & 31;
+    if (row >= a.batch * a.beams) return;
     const int b = row / a.beams, w = row - b * a.beams;
     const T* x0 = reinterpret_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
     // Piece p is values p E .. p E + E - 1 of the row wherever the row begins, so that equal rows have equal sums: of a row that does not
@@ -172,24 +241,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     const int shift = (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
     const uint4* memory = reinterpret_cast<const uint4*>(x0 - shift);
     const int first = blockIdx.x * a.per_chunk, end = min(first + a.per_chunk, (a.vocab + E - 1) / E);
+    const int whole = shift ? (a.vocab + shift) / E - 1 : a.vocab / E;   // pieces before it (and behind 0, if shifted) are read whole
     constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;   // -infinity
     auto load = [&](int p) {
         uint4 u = make_uint4(kNone, kNone, kNone, kNone);
         if (p >= end) return u;
-        if (shift == 0 ? p * E + E <= a.vocab : p > 0 && (p + 2) * E - shift <= a.vocab) {
-            u = memory[p];
-            if (shift) {
-                const uint4 v = memory[p + 1];
-                const uint64_t q[4] = {u.x | (uint64_t)u.y << 32, u.z | (uint64_t)u.w << 32, v.x | (uint64_t)v.y << 32, v.z | (uint64_t)v.w << 32};
-                const int bits = shift * (int)sizeof(T) * 8;   // 8 .. 120
-                const bool far = bits >= 64;
-                const uint64_t q0 = far ? q[1] : q[0], q1 = far ? q[2] : q[1], q2 = far ? q[3] : q[2];
-                const int by = bits & 63;
-                const uint64_t r0 = by ? q0 >> by | q1 << (64 - by) : q0, r1 = by ? q1 >> by | q2 << (64 - by) : q1;
-                u = make_uint4((uint32_t)r0, (uint32_t)(r0 >> 32), (uint32_t)r1, (uint32_t)(r1 >> 32));
-            }
-            return u;
-        }
+        if (p < whole && (p > 0 || !shift)) return shift ? shifted<T>(memory[p], memory[p + 1], shift) : memory[p];
         Vec16<T> part;
         part.u = u;
 #pragma unroll
@@ -197,36 +254,45 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
             if (p * E + i < a.vocab) part.e[i] = x0[p * E + i];
         return part.u;
     };
-    float m = kFloor, sum = 0.0f;
+    // The thread's maximum m and sum of 2^(x log2 e - c), c = m log2 e rounded: one fused multiply-add a pair.  Beyond 3e38 c stays there
+    // and the sum is 0 or infinite: the row is then added up again below.
+    float m = kFloor, c = -kFar, sum = 0.0f;
     float lowest = -INFINITY;      // values below it are none of the best; the bound's
     uint64_t least = 0;            // the bound: keys below it are none of the best
-    int held = 0, sort_at = 1;     // tiles after which the list is sorted next
+    int held = 0, sort_at = kSortFirst;   // tiles after which the list is sorted next
     bool careful = false;          // every tile like the first: the second time over a chunk
     uint4 next[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
+    if (is_out(a, row)) return;
     if (tid == 0) found = 0;
 #pragma unroll 1
     for (int p = first, tile = 1; p < end; p += kTile, ++tile) {
         uint4 raw[kVectors];
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
-            raw[i] = next[i];
-            next[i] = load(p + (kVectors + i) * kThreads + tid);
+        for (int i = 0; i < kVectors; ++i) raw[i] = next[i];
+        if (!shift && p + 2 * kTile <= min(end, whole)) {
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) next[i] = memory[p + kTile + i * kThreads + tid];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) next[i] = load(p + kTile + i * kThreads + tid);
         }
         const float top = largest<T>(raw);
         if (!careful) {
             if (top > m) {
-                sum *= exp2_fast((m - top) * kLog2E);
+                const float z = fminf(fmaxf(top * kLog2E, -kFar), kFar);
+                sum *= exp2_fast(c - z);
                 m = top;
+                c = z;
             }
             F2 s[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-            const F2 minus = f2(-m, -m), log2e = f2(kLog2E, kLog2E);
+            const F2 minus = f2(-c, -c), log2e = f2(kLog2E, kLog2E);
 #pragma unroll
             for (int i = 0; i < kVectors; ++i)
 #pragma unroll
                 for (int j = 0; j < E / 2; ++j) {
-                    const float2 x = two_of<T>(raw[i], j), y = parts(mul2(add2(f2(x.x, x.y), minus), log2e));
+                    const float2 x = two_of<T>(raw[i], j), y = parts(fma2(f2(x.x, x.y), log2e, minus));
                     s[j & 1] = add2(s[j & 1], f2(exp2_fast(y.x), exp2_fast(y.y)));
                 }
             const float2 both = parts(add2(s[0], s[1]));
@@ -236,19 +302,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         auto place = [&](int i, int j) { return (p + i * kThreads + tid) * E + j; };
         const bool sorts = careful || tile == sort_at || p + kTile >= end;
         if (tile == 1 || careful) {
-            const int above = __syncthreads_count(top > -INFINITY && top >= lowest);
+            // groups with a value above the bound: where they are no more than `count`, all of theirs come into the list
+            const bool has = top > -INFINITY && top >= lowest;
+            const uint32_t with = __ballot_sync(0xffffffffu, has);
+            const int shift_of = group_shift(a.count), in_group = lane & ~((1 << shift_of) - 1);
+            const uint32_t group = (shift_of == 5 ? 0xffffffffu : (1u << (1 << shift_of)) - 1) << in_group;
+            const int above = __syncthreads_count((lane == in_group) && (with & group));
             if (above > a.count) {
-                int at = 0x7FFFFFFF;
-#pragma unroll
-                for (int i = kVectors - 1; i >= 0; --i)
-#pragma unroll
-                    for (int j = E / 2 - 1; j >= 0; --j) {
-                        const float2 x = two_of<T>(raw[i], j);
-                        if (x.y == top) at = place(i, 2 * j + 1);
-                        if (x.x == top) at = place(i, 2 * j);
-                    }
-                const uint64_t mine = top > -INFINITY && top >= lowest ? key_of(top, at) : 0;
-                kth_largest(mine, a.count, sorted, &bound);
+                const uint32_t tops = at_least<T>(raw, top);
+                int i = value_of_bit<T>(__ffs(tops) - 1);                            // the lowest place of them
+                if (sizeof(T) == 2 && tops >> 16) i = min((tops & 0xFFFFu) ? i : N, value_of_bit<T>(__ffs(tops >> 16) + 15));
+                const uint64_t mine = has ? key_of(top, place(i / E, i % E)) : 0;
+                kth_largest(mine, a.count, shift_of, maxima, &bound);
                 __syncthreads();
                 if (bound > least) {
                     least = bound;
@@ -256,24 +321,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
                 }
             }
         }
-        if (top >= lowest && top > -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kVectors; ++i)
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float2 two = two_of<T>(raw[i], j / 2);
-                    const float x = j & 1 ? two.y : two.x;
-                    if (x >= lowest && x > -INFINITY) {
-                        const uint64_t k = key_of(x, place(i, j));
-                        if (k >= least) {
-                            const int slot = atomicAdd(&found, 1);
-                            if (slot < kMost) keys[slot] = k;
-                        }
-                    }
+        if (top >= lowest && top > -INFINITY)
+            for (uint32_t from = at_least<T>(raw, lowest); from; from &= from - 1) {
+                const int bit = __ffs(from) - 1, i = value_of_bit<T>(bit);
+                const float x = value_at<T>(raw, bit);
+                const uint64_t k = key_of(x, place(i / E, i % E));
+                if (k >= least && x > -INFINITY) {
+                    const int slot = atomicAdd(&found, 1);
+                    if ((uint32_t)slot < (uint32_t)kMost) keys[slot] = k;
                 }
-        }
+            }
         if (!sorts) continue;
-        sort_at *= 2;
+        sort_at *= kSortFirst;
         __syncthreads();
         const int n = found;
         if (n > kMost) {           // only if not careful: a tile like the first brings no more than there is room for
@@ -285,18 +344,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
             if (tid == 0) found = 0;
 #pragma unroll
             for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
-            // what is left of the sum
-            for (int q = p + kTile; q < end; q += kTile) {
+            for (int q = p + kTile; q < end; q += kTile)   // what is left of the sum
                 for (int i = 0; i < kVectors; ++i) {
                     const uint4 u = load(q + i * kThreads + tid);
                     for (int j = 0; j < E / 2; ++j) {
                         const float2 x = two_of<T>(u, j);
-                        const float t = fmaxf(m, fmaxf(x.x, x.y));
-                        sum = sum * exp2_fast((m - t) * kLog2E) + exp2_fast((x.x - t) * kLog2E) + exp2_fast((x.y - t) * kLog2E);
+                        const float t = fmaxf(m, fmaxf(x.x, x.y)), z = fminf(fmaxf(t * kLog2E, -kFar), kFar);
+                        sum = sum * exp2_fast(c - z) + exp2_fast(fmaf(x.x, kLog2E, -z)) + exp2_fast(fmaf(x.y, kLog2E, -z));
                         m = t;
+                        c = z;
                     }
                 }
-            }
             p = first - kTile;
             __syncthreads();
             continue;
@@ -313,25 +371,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         __syncthreads();
     }
     // ---- the chunk's reference and sum
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o), top = fmaxf(m, m2);
-        sum = sum * exp2_fast((m - top) * kLog2E) + s2 * exp2_fast((m2 - top) * kLog2E);
-        m = top;
-    }
-    if (lane == 0) stats[warp] = Stat{m, sum};
-    __syncthreads();
+    if (fabsf(c) < kFar) sum *= exp2_fast(-fmaf(m, kLog2E, -c));   // from c to m
     const int64_t at = (int64_t)row * a.chunks + blockIdx.x;
-    if (tid == 0) {
-        Stat t = stats[0];
-#pragma unroll
-        for (int i = 1; i < kWarps; ++i) {
-            const float top = fmaxf(t.m, stats[i].m);
-            t.sum = t.sum * exp2_fast((t.m - top) * kLog2E) + stats[i].sum * exp2_fast((stats[i].m - top) * kLog2E);
-            t.m = top;
+    Stat t = sum_block(Stat{m, sum}, stats);
+    if (held && !(t.sum > 0.0f && t.sum < INFINITY)) {   // the largest beyond 2e38 either way, or a NaN or an infinity: the slow way
+        m = of_ordered((uint32_t)(list[0] >> 32));
+        sum = 0.0f;
+        for (int p = first + tid; p < end; p += kThreads) {
+            const uint4 u = load(p);
+            for (int j = 0; j < E / 2; ++j) {
+                const float2 x = two_of<T>(u, j);
+                sum += exp2_fast((x.x - m) * kLog2E) + exp2_fast((x.y - m) * kLog2E);
+            }
         }
-        a.stats[at] = t;
+        __syncthreads();
+        t = sum_block(Stat{m, sum}, stats);
     }
+    if (tid == 0) a.stats[at] = t;
     if (tid < a.count) a.best[at * a.count + tid] = tid < held ? Candidate{of_ordered((uint32_t)(list[tid] >> 32)), (int)~(uint32_t)list[tid]} : Candidate{0.0f, -1};
 }
 
@@ -357,25 +413,39 @@ __device__ __forceinline__ Wide log_of(float x) {
     return plus(sum_of(__fmul_rn(k, 0.693145751953125f), __fmul_rn(k, 1.42860682030941723e-6f)), Wide{logf(m), 0.0f});   // ln 2 in 16 bits, and the rest
 }
 
-// One CTA a sequence.  A candidate's key: its total, to 2^-43 of it, then the lower index (w, chunk, place in the chunk's list): among
+// One CTA a sequence.  A candidate's key: its total, to 2^-44 of it, then the lower index (w, chunk, place in the chunk's list): among
 // equal totals that is the lower place w V + v.
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_constant__ SelectArgs a) {
     constexpr int kEach = kMostCandidates / kThreads;             // candidates of a thread
-    __shared__ float reference[kMaxBeams];
+    __shared__ float reference[kMaxBeams], score_of[kMaxBeams];
+    __shared__ bool is_done[kMaxBeams];
     __shared__ Wide offset[kMaxBeams];                            // total = (x - reference) + offset
-    __shared__ uint64_t keys[kMaxCount * kEach], list[kMaxCount], sorted[kThreads];
+    __shared__ __align__(16) uint64_t maxima[kMostGroups];
+    __shared__ uint64_t keys[128 * kEach];
+    __shared__ int tokens[128 * kEach];
     __shared__ uint64_t bound;
     __shared__ int found;
-    wait_for_previous();
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, per_row = a.chunks * a.count, n = a.beams * per_row;
     const Candidate* best = a.best + (int64_t)b * n;
+    for (int w = tid; w < a.beams; w += kThreads) {               // what precedes the main kernel has been done before this one starts
+        const int row = b * a.beams + w;
+        score_of[w] = __ldcg(a.scores + row);
+        is_done[w] = a.finished && __ldcg(a.finished + row);
+    }
+    __syncthreads();
+    wait_for_previous();
+    // the thread's first candidates, while the sums are on their way
+    constexpr int kEarly = 2;
+    Candidate early[kEarly];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) early[k] = tid + k * kThreads < n ? best[tid + k * kThreads] : Candidate{0.0f, -1};
     for (int w = tid >> 5; w < a.beams; w += kWarps) {            // a warp a beam
         const int row = b * a.beams + w;
-        const float score = a.scores[row];
+        const float score = score_of[w];
         Wide o{NAN, 0.0f};
         float top = kFloor;
         if (fabsf(score) < INFINITY) {
-            if (a.finished && a.finished[row]) {
+            if (is_done[w]) {
                 o = Wide{score, 0.0f};
             } else {
                 const Stat* s = a.stats + (int64_t)row * a.chunks;
@@ -387,8 +457,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
 #pragma unroll
                 for (int d = 16; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
                 if (sum.hi > 0.0f && sum.hi < INFINITY) {   // not: a NaN or an infinity among the logits, or nothing above -infinity
-                    Wide l = log_of(sum.hi);
-                    l = plus(l, Wide{__fdividef(sum.lo, sum.hi), 0.0f});
+                    const Wide l = plus(log_of(sum.hi), Wide{__fdividef(sum.lo, sum.hi), 0.0f});
                     o = plus(Wide{score, 0.0f}, Wide{-l.hi, -l.lo});
                 }
             }
@@ -404,15 +473,14 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     }
     __syncthreads();
     // Candidate i of the sequence.  Thread t takes t, t + 256, ..
-    auto key_at = [&](int i) -> uint64_t {
+    auto key_of_candidate = [&](int i, Candidate c) -> uint64_t {
         const int w = i / per_row;
         const Wide o = offset[w];
         if (isnan(o.hi)) return 0;
         Wide t = o;
-        if (a.finished && a.finished[b * a.beams + w]) {
+        if (is_done[w]) {
             if (i != w * per_row) return 0;
         } else {
-            const Candidate c = best[i];
             if (c.v < 0) return 0;
             t = plus(sum_of(c.x, -reference[w]), o);
             if (!(fabsf(t.hi) < INFINITY)) return 0;   // below the lowest number
@@ -420,33 +488,48 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
         return (uint64_t)ordered(t.hi) << 32 | (ordered(t.lo) >> kIndexBits << kIndexBits) | (uint32_t)(kMostCandidates - 1 - i);
     };
     uint64_t mine = 0;
-    for (int i = tid; i < n; i += kThreads) mine = max(mine, key_at(i));
-    const int some = __syncthreads_count(mine != 0);
-    if (some > a.count) kth_largest(mine, a.count, sorted, &bound);
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+        if (tid + k * kThreads < n) mine = max(mine, key_of_candidate(tid + k * kThreads, early[k]));
+    for (int i = tid + kEarly * kThreads; i < n; i += kThreads) mine = max(mine, key_of_candidate(i, best[i]));
+    // few candidates are sorted as they are
+    if (n > kFew) {
+        const int shift_of = group_shift(a.count), in_group = lane & ~((1 << shift_of) - 1);
+        const uint32_t with = __ballot_sync(0xffffffffu, mine != 0), group = (shift_of == 5 ? 0xffffffffu : (1u << (1 << shift_of)) - 1) << in_group;
+        if (__syncthreads_count((lane == in_group) && (with & group)) > a.count) kth_largest(mine, a.count, shift_of, maxima, &bound);
+    }
     __syncthreads();
     const uint64_t least = bound;
-    if (mine >= least)
-        for (int i = tid; i < n; i += kThreads) {
-            const uint64_t k = key_at(i);
-            if (k >= least) keys[atomicAdd(&found, 1)] = k;
-        }
+    auto add = [&](int i, Candidate c) {
+        const uint64_t k = key_of_candidate(i, c);
+        if (k < least) return;
+        const int slot = atomicAdd(&found, 1);
+        keys[slot] = k;
+        tokens[slot] = c.v;
+    };
+    if (mine >= least) {
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k)
+            if (tid + k * kThreads < n) add(tid + k * kThreads, early[k]);
+        for (int i = tid + kEarly * kThreads; i < n; i += kThreads) add(i, best[i]);
+    }
     __syncthreads();
     const int m = found;
-    sort_best(keys, m, a.count, list);
-    __syncthreads();
-    if (tid < a.count) {
-        const int64_t out = (int64_t)b * a.count + tid;
-        float score = -INFINITY;
-        int w = -1, v = -1;
-        if (tid < m) {
-            const int i = kMostCandidates - 1 - (int)(list[tid] & (kMostCandidates - 1));
-            w = i / per_row;
-            score = of_ordered((uint32_t)(list[tid] >> 32));
-            v = a.finished && a.finished[b * a.beams + w] ? a.eos : best[i].v;
-        }
-        a.out_scores[out] = score;
-        a.out_beams[out] = w;
-        a.out_tokens[out] = v;
+    const int64_t out = (int64_t)b * a.count;
+    for (int i = tid; i < m; i += kThreads) {
+        const uint64_t k = keys[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < m; ++j) rank += keys[j] > k;
+        if (rank >= a.count) continue;
+        const int w = (kMostCandidates - 1 - (int)(k & (kMostCandidates - 1))) / per_row;
+        a.out_scores[out + rank] = of_ordered((uint32_t)(k >> 32));
+        a.out_beams[out + rank] = w;
+        a.out_tokens[out + rank] = is_done[w] ? a.eos : tokens[i];
+    }
+    for (int i = m + tid; i < a.count; i += kThreads) {
+        a.out_scores[out + i] = -INFINITY;
+        a.out_beams[out + i] = a.out_tokens[out + i] = -1;
     }
 }
 
