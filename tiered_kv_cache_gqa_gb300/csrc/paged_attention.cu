@@ -1,12 +1,12 @@
-// Attention of a step's queries over a paged cache held in 4 bits or in 16: tkv_paged_attention.  The mathematics of a
+// Attention of a step's queries over a paged cache held in 4 bits, in 8 or in 16: tkv_paged_attention.  The mathematics of a
 // tile is in paged_tile.cuh; here is how the work is split and the cache brought in.
 //
 // Work split.  The positions of every item (sequence, KV head, tile of rows) are cut into tiles of 32 (16 with 16-bit
-// pages).  The tiles of all items, in that order, are dealt out in equal contiguous shares to the CTAs that fit on the
+// pages, and with 8-bit pages of d 128: about 4 KB each).  The tiles of all items, in that order, are dealt out in equal contiguous shares to the CTAs that fit on the
 // device at once, and within a CTA to its seven computing warps, whatever the lengths are.  Every CTA computes the
 // deal itself, from lengths and cu_tokens.  An eighth warp, four lanes for each of the seven, walks over the pieces of
 // items in their shares, looks up the pages and copies the tiles into a ring of each warp's, as far ahead as the ring has
-// room, across the pieces' ends: a 4-bit record by one cp.async.bulk, 16-bit rows by cp.async in 16-byte pieces (a bulk
+// room, across the pieces' ends: a 4-bit or 8-bit record by one cp.async.bulk, 16-bit rows by cp.async in 16-byte pieces (a bulk
 // copy a row, 256 bytes, took 110 us for 134 MB where these take 30).  A warp
 // computes alone and writes an item that ends within its share as soon as it is done.  Only the last piece of every warp
 // waits for the others: the CTA joins them in shared memory, and what is cut at a CTA's end goes to the
@@ -28,12 +28,15 @@ constexpr int kWarps = 7, kThreads = (kWarps + 1) * 32;   // warps that compute,
 constexpr int kCombineWarps = 8;
 constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, joining costs more than it brings
 // Up to these numbers of positions in sight a CTA takes whole items, and nothing is left to join: always; where the items
-// may be as many as the SMs and the pages are of 4 bits.  One launch instead of two, but uneven shares.  Whole and cut, us, 8 KV
+// may be as many as the SMs and the pages are of 4 or 8 bits.  One launch instead of two, but uneven shares.  Whole and cut, us, 8 KV
 // heads, groups of 4:
 //   4 bits, d 128: batch 1, 256 positions 6.9 and 8.1, 512 positions 8.7 and 8.3; batch 8, 512 positions 10.5 and 9.9; batch 64,
 //     256 positions 11.8 and 13.7, 512 positions 16.7 and 19.7, 1,024 positions 25.2 and 26.5
 //   4 bits, d 64: batch 1, 256 positions 6.2 and 7.1; batch 64, 512 positions 11.7 and 13.5, 1,024 positions 18.1 and 18.9; but
 //     batch 67 of mixed lengths with a window of 700 positions 20.3 and 16.2, so not beyond 512
+//   8 bits, d 128: batch 1, 256 positions 7.0 and 7.4, 512 positions 8.1 and 7.6; batch 8, 512 positions 9.6 and 9.4; batch 64, 256
+//     positions 12.8 and 16.3, 512 positions 17.9 and 21.9; mixed lengths up to 1,024 31.8 and 26.5; d 64: 5.9 and 6.6, 7.0 and 6.8, 8.0
+//     and 8.0, 8.7 and 10.3, 11.6 and 13.8, 16.7 and 14.8
 //   bf16, d 128: batch 1, 64 positions 5.5 and 9.0, 256 positions 7.6 and 7.6; batch 64, 256 positions 20.0 and 20.4, 512 positions
 //     33.1 and 32.3; d 64: batch 64, 256 positions 15.8 and 16.0, 512 positions 24.6 and 23.7
 constexpr int kWholeShort = 256, kWholeMany = 512;
@@ -114,10 +117,9 @@ __device__ __forceinline__ int window_begin(const PagedAttnArgs& a, int position
 // kernel lets the joining one start behind its own wait, on every SM.  Ordinary loads: the lines are there from the main
 // kernel's reads (8 x 4,096 positions in bf16 30.2 us; with reads from L2 31.1).
 template <int R, int TP>
-__device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
+__device__ __forceinline__ Seq sequence_of(const PagedAttnArgs& a, int c0, int c1, int length) {
     Seq s;
-    const int c0 = a.cu[b], c1 = a.cu[b + 1];
-    s.full = max(0, a.c.lengths[b]);
+    s.full = max(0, length);
     s.first_row = c0;
     s.n = (c0 < 0 || c1 < c0 || c1 > a.rows) ? -1 : c1 - c0;
     s.len = min(s.full, a.c.max_pages << a.page_shift);
@@ -126,6 +128,11 @@ __device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
     s.units = max(1, (s.len - s.lo + TP - 1) / TP);   // a row that sees nothing is written too
     s.tiles = s.n > 0 ? (int)(((int64_t)s.n * a.group + R - 1) / R) : 0;
     return s;
+}
+
+template <int R, int TP>
+__device__ __forceinline__ Seq sequence(const PagedAttnArgs& a, int b) {
+    return sequence_of<R, TP>(a, a.cu[b], a.cu[b + 1], a.c.lengths[b]);
 }
 
 // Tiles of a sequence.  The host has made sure that the batch's tiles are fewer than 2^31.
@@ -238,6 +245,10 @@ struct Shared {
     int stopped[kWarps], issued[kWarps];   // the warp takes no more tiles; tiles that were brought for it
     uint8_t bad[kWarps][C::stages][2];  // records of a stage that have no page
     uint2 q[kWarps][Query<D, NT>::words];
+    // 8 bits: what a warp's last piece counts in its item's sums, two rows each; what the record of the item's end counts, and the sums
+    static constexpr int weights = KIND == kE4m3 ? kWarps : 1;
+    float2 weight[weights][C::R / 2], tail_weight[weights][C::R / 2];
+    float4 total[weights][C::R / 2];
 };
 
 // ------------------------------------------------------------------ out
@@ -327,8 +338,19 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     // the next piece's place
     int b = left ? from.b : 0, h = 0, row_tile = 0, unit = 0;
     Seq s{};
+    // 8 bits: the next sequence is read while this one is copied, its pages once for all its heads (below)
+    int next_c0 = 0, next_c1 = 0, next_length = 0;
+    auto read_next = [&]() {
+        if (b + 1 < a.c.batch) {
+            next_c1 = a.cu[b + 2];
+            next_length = a.c.lengths[b + 1];
+        }
+    };
     if (left) {
-        s = sequence<R, TP>(a, b);
+        const int c1 = a.cu[b + 1];
+        s = sequence_of<R, TP>(a, a.cu[b], c1, a.c.lengths[b]);
+        next_c0 = c1;
+        if (KIND == kE4m3) read_next();
         const int item = from.in_seq / s.units;
         unit = from.in_seq - item * s.units;
         h = item / s.tiles;
@@ -340,6 +362,15 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     const uint8_t* pages = nullptr;
     int st = 0, parity = 0, spins = 0, issued = 0;
     bool first = true;   // the ring's first round: nothing to wait for
+    // 8 bits: the four lanes look up the pages of 64 positions at once, and those of the next 64 while these are copied: the copying
+    // warp as a whole waits for what any of its lanes needs next.  Those at the beginning of a sequence serve all its items.
+    constexpr bool kAhead = KIND == kE4m3;
+    constexpr int kBatch = 4 / T::groups;   // tiles
+    int now = -2, ahead = -2, in_batch = 0, first_now = -2, first_ahead = -2, first_of = -1;
+    auto page_of = [&](int p) {
+        p += k * 16;
+        return p < s.len ? table[p >> a.page_shift] : -2;
+    };
     auto look_up = [&]() {   // a tile may have two records, which may lie in two pages
         const int p = pos + (T::groups == 2 ? (k & 1) * 16 : 0);
         page = p < end ? table[p >> a.page_shift] : -2;
@@ -349,10 +380,18 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
         uint32_t tile_to = 0, tile_bar = 0;
         int tile_rows = 0;
         uint64_t tile_src = 0;
+        if (kAhead) page = __shfl_sync(0xffffffffu, now, (lane & ~3) + in_batch * T::groups + (k & (T::groups - 1)));
         if (left + tiles > 0 && spins < kSpinLimit) {
             if (tiles == 0) {
                 while (h >= a.c.num_kv_heads || s.tiles == 0) {   // the deal leaves tiles, so there is a next item
-                    s = sequence<R, TP>(a, ++b);
+                    ++b;
+                    if (kAhead) {
+                        s = sequence_of<R, TP>(a, next_c0, next_c1, next_length);
+                        next_c0 = next_c1;
+                        read_next();
+                    } else {
+                        s = sequence<R, TP>(a, b);
+                    }
                     h = 0;
                 }
                 Piece p;
@@ -384,7 +423,24 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                 end = p.rows.any_until;
                 table = a.c.page_table + (int64_t)b * a.c.max_pages;
                 pages = reinterpret_cast<const uint8_t*>(a.c.pages) + head_bytes * h;
-                look_up();
+                if (kAhead) {
+                    if (pos != s.lo) {
+                        now = page_of(pos);
+                        ahead = page_of(pos + 64);
+                    } else {
+                        if (first_of != b) {
+                            first_of = b;
+                            first_now = page_of(pos);
+                            first_ahead = page_of(pos + 64);
+                        }
+                        now = first_now;
+                        ahead = first_ahead;
+                    }
+                    page = now;
+                    in_batch = 0;
+                } else {
+                    look_up();
+                }
                 unit += tiles;
                 if (unit == s.units) {
                     unit = 0;
@@ -397,6 +453,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
             if (first || mbar_test(empty0 + 8 * st, parity)) {
                 moved = true;
                 ++issued;
+                if (kAhead && pos + (T::groups == 2 ? (k & 1) * 16 : 0) >= end) page = -2;   // nothing of the sequence that a row sees
                 const bool ok = page >= 0 && page < a.c.num_pages;
                 const uint32_t bar = full0 + 8 * st, to = ring + st * T::bytes;
                 if (!ok && page != -2) raise_status(a.status, TKV_ECAPACITY);
@@ -426,7 +483,16 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
                     first = false;
                 }
                 pos += TP;
-                if (--tiles > 0) look_up();
+                --tiles;
+                if (kAhead) {
+                    if (++in_batch == kBatch && tiles > 0) {
+                        now = ahead;
+                        ahead = page_of(pos + 64);
+                        in_batch = 0;
+                    }
+                } else if (tiles > 0) {
+                    look_up();
+                }
             }
             spins = moved ? 0 : spins + 1;
             if (!moved && *(volatile int*)&sh.stopped[w]) left = tiles = 0;
@@ -457,6 +523,88 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared<D, NT,
     if (spins >= kSpinLimit) raise_status(a.status, TKV_ETIMEOUT);
     issued = max(issued, __shfl_xor_sync(0xffffffffu, issued, 1));   // of both lanes that bring records
     if (k == 0 && lane >> 2 < kWarps) sh.issued[w] = issued;
+}
+
+// ------------------------------------------------------------------ joining in a CTA, 8 bits
+// The warps' last pieces lie in sh.merge and sh.ml: `leads` are those that begin an item here.  The weights of all pieces come first, a
+// thread a piece's two rows: then a sum is products alone, with no exponentials between one piece and the next, and a thread
+// has 8 channels of a row to write at once.  Sequences of 2,000 positions and one of 70, windows of 1,000, 9 rows a KV head of 128:
+// 3.8 us for the CTA that joins seven items and 1.7 for one that joins three, where one piece after the other took 10 and 2.5.
+template <int D, int NT>
+__device__ __forceinline__ void join_pieces(const PagedAttnArgs& a, Shared<D, NT, kE4m3>& sh, uint32_t valid, uint32_t continues, uint32_t ends,
+                                            uint32_t heads, uint32_t leads) {
+    constexpr int TWOS = 4 * NT, SUMS = Rec4<D, NT>::sums, SIZE = Rec4<D, NT>::size;
+    const int tid = threadIdx.x, lane = tid & 31;
+    auto last_of = [&](int g) { return __ffs((leads | heads | ~valid) & (~1u << g)) - 2; };   // the last piece that follows
+    auto tail_of = [&](int w1) { return (heads >> (w1 + 1)) & 1 && !((ends >> w1) & 1) ? w1 + 1 : -1; };
+    auto tail_record = [&](int tail) { return a.part + ((int64_t)a.grid * 2 + (int64_t)blockIdx.x * kWarps + tail) * SIZE; };
+    const float4 nothing = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+    if (tid < kWarps * TWOS) {
+        const int g = tid / TWOS, two = tid - g * TWOS;
+        if (leads >> g & 1) {
+            const int w1 = last_of(g), tail = tail_of(w1);
+            const float4 t = tail >= 0 ? tail_record(tail)[SUMS + two] : nothing;
+            float m0 = t.x, m1 = t.z;
+            for (int w = g; w <= w1; ++w) {
+                m0 = fmaxf(m0, sh.ml[w][two].x);
+                m1 = fmaxf(m1, sh.ml[w][two].z);
+            }
+            float f0 = exp2_approx(t.x - m0), f1 = exp2_approx(t.z - m1), l0 = t.y * f0, l1 = t.w * f1;
+            sh.tail_weight[g][two] = make_float2(f0, f1);
+            for (int w = g; w <= w1; ++w) {
+                const float4 ml = sh.ml[w][two];
+                f0 = exp2_approx(ml.x - m0);
+                f1 = exp2_approx(ml.z - m1);
+                l0 = fmaf(ml.y, f0, l0);
+                l1 = fmaf(ml.w, f1, l1);
+                sh.weight[w][two] = make_float2(f0, f1);
+            }
+            sh.total[g][two] = make_float4(m0, l0, m1, l1);
+        }
+    }
+    __syncthreads();
+    constexpr int H = D / 64, UNITS = NT * H * 32;   // of an item: 8 channels of two rows
+    const int all = __popc(leads) * UNITS;
+#pragma unroll 1
+    for (int i = tid; i < all; i += kThreads) {
+        const int q = i / UNITS, nt = (i - q * UNITS) / (H * 32), h = i / 32 % H, two = 4 * nt + (lane & 3), at = (nt * (D / 16) + 4 * h) * 32 + lane;
+        const int g = (int)__fns(leads, 0, q + 1), w1 = last_of(g), tail = tail_of(w1);
+        const bool begins = !((continues >> g) & 1);
+        float4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = make_float4(0, 0, 0, 0);
+        auto add = [&](const float4* from, float2 f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 y = from[at + 32 * j];
+                x[j] = make_float4(fmaf(y.x, f.x, x[j].x), fmaf(y.y, f.y, x[j].y), fmaf(y.z, f.x, x[j].z), fmaf(y.w, f.y, x[j].w));
+            }
+        };
+        if (tail >= 0) add(tail_record(tail), sh.tail_weight[g][two]);
+#pragma unroll 2
+        for (int w = g; w <= w1; ++w) add(sh.merge[w], sh.weight[w][two]);
+        const float4 ml = sh.total[g][two];
+        if (begins && (((ends >> w1) & 1) || tail >= 0)) {
+            const Rows& rows = sh.queue[g][sh.last[g]].rows;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float* lse;
+                uint16_t* to = out_row(a, rows, 8 * nt + 2 * (lane & 3) + e, &lse);
+                if (!to) continue;
+                const float l = e ? ml.w : ml.y, inv = inverse(l, 1.0f);
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = pack16((e ? x[j].y : x[j].x) * inv, (e ? x[j].w : x[j].z) * inv, a.q_fp16);
+                *reinterpret_cast<uint4*>(to + channel_of<D, kE4m3>(lane >> 2, 4 * h, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (lse && h == 0 && lane < 4) *lse = lse_of(e ? ml.z : ml.x, l);
+            }
+        } else {
+            float4* record = a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * SIZE;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) record[at + 32 * j] = x[j];
+            if (h == 0 && lane < 4) record[SUMS + two] = ml;
+        }
+    }
 }
 
 // ------------------------------------------------------------------ a wait that ran out
@@ -691,6 +839,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
     const uint32_t valid = __ballot_sync(0xffffffffu, f & kValid), continues = __ballot_sync(0xffffffffu, f & kContinues);
     const uint32_t ends = __ballot_sync(0xffffffffu, f & kEnds), heads = __ballot_sync(0xffffffffu, f & kHead);
     const uint32_t leads = valid & ~(continues & ~1u);
+    if constexpr (KIND == kE4m3) {
+        join_pieces<D, NT>(a, sh, valid, continues, ends, heads, leads);
+        return;
+    }
     // all groups at once, each with its share of the CTA's warps
     const int groups = __popc(leads), team = groups <= 1 ? 8 : groups == 2 ? 4 : groups <= 4 ? 2 : 1;
     if (warp / team < groups) {
@@ -838,16 +990,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
 // twice the rows.
 int row_tiles(int group, int max_new) { return (int64_t)group * max_new > 8 ? 2 : 1; }
 
-// Tiles of 32 rows of 4-bit pages do that once more, but the code is long and the joining heavy: worth it from so many tiles a
+// Tiles of 32 rows of 4-bit and 8-bit pages do that once more, but the code is long and the joining heavy: worth it from so many tiles a
 // computing warp on, by the host's estimate.  30 rows a KV head, 8 x 8 heads of 64: 36.3 us with 16 rows and 37.3 with 32 at
 // 8,192 positions (15 tiles a warp), 65.7 and 58.4 at 16,384, 244 and 170 at 65,536; of 128: 90.0 and 93.1 at 16,384 (31
-// tiles), 163.5 and 156.2 at 32,768, 307 and 276 at 65,536.  Measured on sequences of one length; the rule takes every
+// tiles), 163.5 and 156.2 at 32,768, 307 and 276 at 65,536.  8 bits, 24 or 32 rows, heads of 64: 22.1 and 22.7 at 4,096 (7.7), 35.2
+// and 30.2 at 8,192, 117 and 75 at 32,768; of 128: 29.8 and 31.7 at 4,096, 49.5 and 46.3 at 8,192 (15), 174 and 124 at 32,768.  Measured on sequences of one length; the rule takes every
 // sequence to have max_new queries, so a ragged step may get the longer code for less than it is worth.
 bool rows_of_32(const PagedAttnArgs& a, int max_new, int64_t sight, int sms) {
     const int64_t rows = (int64_t)a.group * max_new;
-    if (a.c.kv_type != TKV_INT4 || rows <= 16) return false;
+    if (!has_records(a.c.kv_type) || rows <= 16) return false;
     const double tiles = (double)a.c.batch * a.c.num_kv_heads * ((rows + 31) / 32) * ((sight + 31) / 32);
-    return tiles >= (a.c.head_dim == 64 ? 18.0 : 45.0) * kWarps * sms;
+    return tiles >= (a.c.kv_type == TKV_E4M3 ? 10.0 : a.c.head_dim == 64 ? 18.0 : 45.0) * kWarps * sms;
 }
 
 // TKV_FAULT_INJECT=wait:N: computing warp N of every attention's grid gives up at its first wait, as if a copy had not come.
@@ -896,7 +1049,7 @@ cudaError_t launch_kind(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_rows(PagedAttnArgs& a, int nt, int sms, int dev, cudaStream_t st) {
-    return nt == 1 ? launch_kind<D, 1>(a, sms, dev, st) : nt == 2 ? launch_kind<D, 2>(a, sms, dev, st) : launch<D, 4, kInt4>(a, sms, dev, st);
+    return nt == 1 ? launch_kind<D, 1>(a, sms, dev, st) : nt == 2 ? launch_kind<D, 2>(a, sms, dev, st) : a.c.kv_type == TKV_E4M3 ? launch<D, 4, kE4m3>(a, sms, dev, st) : launch<D, 4, kInt4>(a, sms, dev, st);
 }
 
 bool attention_shape_ok(const tkv_paged* c, int32_t hq, int32_t max_new) {

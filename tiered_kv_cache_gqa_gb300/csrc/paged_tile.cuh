@@ -581,6 +581,17 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
                                            float scale_log2, float gain, int lane, const Rows& rows, Query<D, NT>& q) {
     constexpr int KM = D / 16;
     const int r = lane >> 2, cq = lane & 3;
+    uint4 raw[KIND == kE4m3 ? NT : 1][D / 32];   // 8 bits: all rows at once, 16 channels of every 64
+    if (KIND == kE4m3) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = rows.row0 + nt * 8 + r, t = row < rows.seq_rows ? query_of(row, group, mul) : 0;
+            const uint16_t* x16 = q16 + (rows.first_row + t) * row_stride + (rows.h * group + row - t * group) * head_stride + 16 * cq;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w)
+                raw[KIND == kE4m3 ? nt : 0][w] = row < rows.seq_rows ? *reinterpret_cast<const uint4*>(x16 + 64 * (w >> 1) + 8 * (w & 1)) : make_uint4(0, 0, 0, 0);
+        }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int row = rows.row0 + nt * 8 + r;
@@ -619,12 +630,11 @@ __device__ __forceinline__ void load_query(const uint16_t* q16, int64_t row_stri
             q.z0[nt] = __shfl_sync(0xffffffffu, z, 8 * cq);
             q.z1[nt] = __shfl_sync(0xffffffffu, z, 8 * cq + 4);
         } else if (KIND == kE4m3) {
-            float x[D / 4];                              // 16 channels of every 64
+            float x[D / 4];
             float top = 0.0f;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (is_row) v = *reinterpret_cast<const uint4*>(x16 + 64 * (w >> 1) + 16 * cq + 8 * (w & 1));
+                const uint4 v = raw[KIND == kE4m3 ? nt : 0][w];
                 const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
