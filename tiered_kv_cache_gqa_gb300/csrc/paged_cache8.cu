@@ -4,9 +4,9 @@
 //   a = max |x| over what is finite of them (k after its rotation),  e_new = least e with a <= 448 2^e, within -32 .. 31
 //   e = e_new if f = 0, else max(e, e_new);  code = e4m3(x 2^-e), to nearest even, saturating; an infinity or a NaN is NaN
 // and where e grows the rows [0, f) are written anew: value 2^-e, rounded once more (exact but for what becomes subnormal).
-// So a block and not a row is what one CTA owns: four warps take its K, two or four its V, and walk over KV heads; a thread has
-// two rows of 8 channels, whose cosines and sines it finds once for all heads, and the CTA meets once a head, for the
-// maxima.
+// So a block and not a row is what one CTA owns: half of its warps take K, the others V, and walk over KV heads; a thread has 16 values
+// of each head, and half of the CTA meets once a head, for the maxima.  Of K they are a row's 8 channels and the 8 that hold their
+// partners, whose cosines and sines are found once for all heads; of V 8 channels of two rows, which are written together.
 //
 // A CTA's block.  A sequence's n rows touch at most (n + 14) / 16 + 1 blocks, so the slots from (cu[b] >> 4) + 2 b up to
 // (cu[b + 1] >> 4) + 2 (b + 1) hold them all wherever they begin: slots are CTAs, the sequence of a slot is found by a search over cu,
@@ -19,12 +19,11 @@ using namespace tkv;
 
 namespace {
 
-constexpr int kAppendCtas = 3, kGatherCtas = 6;   // on an SM at once, by their registers
+constexpr int kAppendCtas = 4, kGatherCtas = 6;   // of d 128 on an SM at once, by their registers
 
+// D threads for K and D for V, 16 values each.
 template <int D>
-struct Threads {
-    static constexpr int k = 128, v = D, all = k + v;   // 16 rows of D / 8 pieces of 8 channels: two (of K at d 64: one) a thread of K, two of V
-};
+constexpr int ctas_of(int of_128) { return of_128 * 128 / D; }
 
 // A block of a step: its new rows are those at offsets [lo, hi), row0 + offset in the step's tensors.
 struct Block {
@@ -75,233 +74,276 @@ __device__ __forceinline__ int exponent_for(float amax) {
 // Two values as codes, the first in the low byte.
 __device__ __forceinline__ uint32_t code_pair(float a, float b) { return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3); }
 
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // Four codes as values.
 __device__ __forceinline__ void decode4(uint32_t w, float scale, float (&x)[4]) {
     const float2 a = __half22float2(e4m3_pair((uint16_t)w)), b = __half22float2(e4m3_pair((uint16_t)(w >> 16)));
-    x[0] = a.x * scale;
-    x[1] = a.y * scale;
-    x[2] = b.x * scale;
-    x[3] = b.y * scale;
+    const float2 c = parts(mul2(f2(a.x, a.y), f2(scale, scale))), d = parts(mul2(f2(b.x, b.y), f2(scale, scale)));
+    x[0] = c.x;
+    x[1] = c.y;
+    x[2] = d.x;
+    x[3] = d.y;
 }
 
-// A thread's pieces of a record: 8 channels from `channel` on, of the rows r[0] and r[1] (16: none), and where they lie.
-struct Pieces {
-    int channel, r[2], at[2];
-    bool is_k;
-};
+// The largest of three magnitudes; NaN counts for nothing.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float y;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 
+// The largest magnitude of a thread's 16 values over what is finite; an infinity becomes a NaN, which its code is then.
+__device__ __forceinline__ float largest_finite(float (&x)[2][8]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) top = max_abs(x[i][j], x[i][j + 1], top);
+    if (top == INFINITY) {
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (fabsf(x[i][j]) == INFINITY) x[i][j] = __int_as_float(0x7FC00000);
+                top = fmaxf(top, fabsf(x[i][j]));
+            }
+    }
+    return top;
+}
+
+// The largest over the D threads of K (half 0) or V (half 1), which are whole warps and meet at a barrier of their own.
 template <int D>
-__device__ __forceinline__ Pieces pieces_of_thread() {
-    Pieces p;
-    p.is_k = threadIdx.x < Threads<D>::k;
-    if (p.is_k) {
-        const int t = threadIdx.x, chunk = t & (D / 8 - 1);
-        p.channel = 8 * chunk;
-        p.r[0] = t / (D / 8);
-        p.r[1] = D == 128 ? p.r[0] + 8 : 16;
+__device__ __forceinline__ float largest_of_half(float top, int half, uint32_t (&maxima)[D / 32]) {
+    const uint32_t warp_max = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if ((threadIdx.x & 31) == 0) maxima[(threadIdx.x >> 5) & (D / 32 - 1)] = warp_max;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(D) : "memory");
+    uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) p.at[i] = (chunk >> 3) * 1024 + p.r[i] * 64 + (chunk & 7) * 8;
-    } else {
-        const int t = threadIdx.x - Threads<D>::k, chunk = (t >> 2) & (D / 8 - 1), half = t / (D / 2);
-        p.channel = 8 * chunk;
-        p.r[0] = half * 8 + (t & 3) * 2;
-        p.r[1] = p.r[0] + 1;
-        p.at[0] = Record8<D>::v_codes + half * (8 * D) + chunk * 64 + (t & 3) * 16;
-        p.at[1] = p.at[0] + 1;   // every other byte each
-    }
-    return p;
+    for (int w = 0; w < D / 32; ++w) most = max(most, maxima[w]);
+    return __uint_as_float(most);
 }
 
-// blockIdx.y: the first head.
-template <typename T, int D, int TURN>
-__global__ void __launch_bounds__(Threads<D>::all, kAppendCtas) append8_kernel(const __grid_constant__ RowArgs a) {
-    let_next_start();
-    wait_for_previous();
-    using R = Record8<D>;
-    Block blk;
-    if (!find_block(a, blockIdx.x, &blk)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (blk.page < 0) {
-        if (tid == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
-        return;
-    }
-    __shared__ uint32_t maxima[2][Threads<D>::all / 32];
-    const Pieces p = pieces_of_thread<D>();
-    const bool is_new[2] = {p.r[0] >= blk.lo && p.r[0] < blk.hi, p.r[1] >= blk.lo && p.r[1] < blk.hi};
-    const int64_t stride = p.is_k ? a.k_row : a.v_row, head = p.is_k ? a.k_head : a.v_head;
-    const T* from[2];
-    uint4 raw[2] = {};
+__device__ __forceinline__ void scale16(float (&x)[2][8], float f) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) from[i] = reinterpret_cast<const T*>(p.is_k ? a.k : a.v) + (blk.row0 + p.r[i]) * stride + blockIdx.y * head + p.channel;
-    auto read = [&](int h) {   // the next head's values, while the last one's are worked on
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (is_new[i] && h < a.c.num_kv_heads) raw[i] = *reinterpret_cast<const uint4*>(from[i]);
-            from[i] += a.lanes * head;
+        for (int j = 0; j < 8; j += 2) {
+            const float2 y = parts(mul2(f2(x[i][j], x[i][j + 1]), f2(f, f)));
+            x[i][j] = y.x;
+            x[i][j + 1] = y.y;
         }
+}
+
+// Chunks of 8 channels.  Unit u of a row: where k is turned by halves the first pairs / 8 units are chunk u and its partner, otherwise
+// two neighbours.
+struct Chunks {
+    int c[2];
+    bool turned;
+};
+template <int TURN>
+__device__ __forceinline__ Chunks chunks_of(int u, int pairs) {
+    const int pc = TURN == kHalves ? pairs >> 3 : 0;
+    if (u < pc) return Chunks{{u, u + pc}, true};
+    const int c = 2 * pc + 2 * (u - pc);
+    return Chunks{{c, c + 1}, TURN != kNone && TURN != kHalves};
+}
+__device__ __forceinline__ int k_place(int row, int chunk) { return (chunk >> 3) * 1024 + row * 64 + (chunk & 7) * 8; }
+
+// K of a block: a thread has 16 channels of one row.
+template <typename T, int D, int TURN>
+__device__ __forceinline__ void append_k(const RowArgs& a, const Block& blk, uint8_t* rec, int64_t next_rec, uint32_t (&maxima)[2][D / 32]) {
+    const int t = threadIdx.x, r = t / (D / 16);
+    const Chunks ch = chunks_of<TURN>(t & (D / 16 - 1), a.pairs);
+    const bool is_new = r >= blk.lo && r < blk.hi;
+    const int64_t row = blk.row0 + r;
+    const T* from = reinterpret_cast<const T*>(a.k) + row * a.k_row + blockIdx.y * a.k_head;
+    uint4 raw[2] = {};
+    auto read = [&](int h) {   // the next head's values, while the last one's are worked on
+        if (is_new && h < a.c.num_kv_heads) {
+            raw[0] = *reinterpret_cast<const uint4*>(from + 8 * ch.c[0]);
+            raw[1] = *reinterpret_cast<const uint4*>(from + 8 * ch.c[1]);
+        }
+        from += a.lanes * a.k_head;
     };
     read(blockIdx.y);
-    // the angles of the thread's rows: halves: with the sign that the partner's product has
-    constexpr int NCS = TURN == kHalves ? 8 : TURN == kAdjacent ? 4 : 1;
-    const bool turned = TURN != kNone && p.is_k && p.channel < 2 * a.pairs, first = p.channel < a.pairs;
-    float2 cs[2][NCS];
-    if ((TURN == kHalves || TURN == kAdjacent) && turned) {
+    constexpr int NCS = TURN == kHalves || TURN == kAdjacent ? 8 : 1;
+    float2 cs[NCS];
+    bool turned[2] = {ch.turned, ch.turned};   // adjacent pairs: a chunk holds its own four
+    if (TURN == kAdjacent || TURN == kAny) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!is_new[i]) continue;
-            int pos[4] = {(int)(blk.first + p.r[i]), 0, 0, 0};
-            if (a.positions) {
+        for (int i = 0; i < 2; ++i) turned[i] = 8 * ch.c[i] < 2 * a.pairs;
+    }
+    if (NCS == 8 && is_new && (turned[0] || turned[1])) {
+        int pos[4] = {(int)(blk.first + r), 0, 0, 0};
+        if (a.positions) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (x < a.num_axes) pos[x] = a.positions[x * a.axis_stride + blk.row0 + p.r[i]];
-            }
-            load_angles<NCS>(a, pos, TURN == kHalves ? (first ? p.channel : p.channel - a.pairs) : p.channel / 2, cs[i]);
-            if (TURN == kHalves && first) {
+            for (int x = 0; x < 4; ++x)
+                if (x < a.num_axes) pos[x] = a.positions[x * a.axis_stride + row];
+        }
+        if (TURN == kHalves) {
+            load_angles<NCS>(a, pos, 8 * ch.c[0], cs);
+        } else {
+            float2 four[4];
 #pragma unroll
-                for (int j = 0; j < NCS; ++j) cs[i][j].y = -cs[i][j].y;
-            }
+            for (int i = 0; i < 2; ++i)
+                if (turned[i]) {
+                    load_angles<4>(a, pos, 4 * ch.c[i], four);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cs[(4 * i + j) % NCS] = four[j];
+                }
         }
     }
-    const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * R::bytes;
-    uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) + (blk.page * a.c.num_kv_heads + blockIdx.y) * head_bytes +
-                   (((int)blk.first & (a.c.page_size - 1)) >> 4) * R::bytes;
-    const int partner = lane + (first ? a.pairs / 8 : -(a.pairs / 8));
-    int turn = 0;
+    int side = 0;
 #pragma unroll 1
-    for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, rec += a.lanes * head_bytes, turn ^= 1) {
-        int* exponent = reinterpret_cast<int*>(rec + R::exponents) + !p.is_k;
+    for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, rec += next_rec, side ^= 1) {
+        int* exponent = reinterpret_cast<int*>(rec + Record8<D>::exponents);
         int e_old = kLowestExponent;
         if (blk.lo > 0) e_old = block_exponent(*exponent);
         float x[2][8];
-        const uint4 now[2] = {raw[0], raw[1]};
-        unpack<T>(now[0], x[0]);
-        unpack<T>(now[1], x[1]);
+        unpack<T>(raw[0], x[0]);
+        unpack<T>(raw[1], x[1]);
         read(h + a.lanes);
-        if (TURN == kHalves && p.is_k) {
+        if (TURN == kHalves && ch.turned && is_new) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint4 other;
-                other.x = __shfl_sync(0xffffffffu, now[i].x, partner);
-                other.y = __shfl_sync(0xffffffffu, now[i].y, partner);
-                other.z = __shfl_sync(0xffffffffu, now[i].z, partner);
-                other.w = __shfl_sync(0xffffffffu, now[i].w, partner);
-                if (turned && is_new[i]) {
-                    float y[8];
-                    unpack<T>(other, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] = __fadd_rn(__fmul_rn(x[i][j], cs[i][j % NCS].x), __fmul_rn(y[j], cs[i][j % NCS].y));
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float2 z = rotate_pair(x[0][j], x[1][j], cs[j % NCS]);
+                x[0][j] = z.x;
+                x[1][j] = z.y;
             }
-        } else if (TURN == kAdjacent && turned) {
+        } else if (TURN == kAdjacent && is_new) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (is_new[i]) {
+                if (turned[i]) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 z = rotate_pair(x[i][2 * j], x[i][2 * j + 1], cs[i][j % NCS]);
+                        const float2 z = rotate_pair(x[i][2 * j], x[i][2 * j + 1], cs[(4 * i + j) % NCS]);
                         x[i][2 * j] = z.x;
                         x[i][2 * j + 1] = z.y;
                     }
                 }
-        } else if (TURN == kAny && turned) {
+        } else if (TURN == kAny && is_new) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (turned[i]) turn_any(a, reinterpret_cast<const T*>(a.k) + row * a.k_row + h * a.k_head, row, (int)(blk.first + r), ch.c[i], x[i]);
+        }
+        const float top = largest_of_half<D>(largest_finite(x), 0, maxima[side]);   // rows that are not new are zeros here
+        const int e_new = exponent_for(top), e = max(e_old, e_new);
+        const bool grows = blk.lo > 0 && e_new > e_old;
+        if (grows && r < blk.lo) {   // the rows that were there before, from their codes
+            const float scale = power_of_two(e_old);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t row = blk.row0 + p.r[i];
-                if (is_new[i]) turn_any(a, reinterpret_cast<const T*>(a.k) + row * a.k_row + h * a.k_head, row, (int)(blk.first + p.r[i]), p.channel >> 3, x[i]);
+                const uint2 w = *reinterpret_cast<const uint2*>(rec + k_place(r, ch.c[i]));
+                float y[4], z[4];
+                decode4(w.x, scale, y);
+                decode4(w.y, scale, z);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = y[j];
+                    x[i][4 + j] = z[j];
+                }
             }
         }
-        // the largest of the block: NaN counts for nothing here, and neither does an infinity, which becomes one
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (is_new[i]) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i][j]));
-            }
-        if (top == INFINITY) {
-            top = 0.0f;
+        if (is_new || (grows && r < blk.lo)) {
+            scale16(x, power_of_two(-e));
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (fabsf(x[i][j]) == INFINITY) x[i][j] = __int_as_float(0x7FC00000);
-                    if (is_new[i]) top = fmaxf(top, fabsf(x[i][j]));
-                }
+                *reinterpret_cast<uint2*>(rec + k_place(r, ch.c[i])) = make_uint2(code_pair(x[i][0], x[i][1]) | code_pair(x[i][2], x[i][3]) << 16,
+                                                                                   code_pair(x[i][4], x[i][5]) | code_pair(x[i][6], x[i][7]) << 16);
         }
-        const uint32_t warp_max = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (lane == 0) maxima[turn][warp] = warp_max;
-        __syncthreads();   // the next head's maxima lie in the other half, so once a head is enough
-        uint32_t most = 0;
-        if (p.is_k) {
+        if (t == 0 && (blk.lo == 0 || grows)) *exponent = e;   // everyone has read the old one before the barrier
+    }
+}
+
+// V of a block: a thread has 8 channels of two rows, every other byte of 16 each.
+template <typename T, int D>
+__device__ __forceinline__ void append_v(const RowArgs& a, const Block& blk, uint8_t* rec, int64_t next_rec, uint32_t (&maxima)[2][D / 32]) {
+    const int t = threadIdx.x - D, chunk = (t >> 2) & (D / 8 - 1), r = t / (D / 2) * 8 + (t & 3) * 2;
+    const bool is_new[2] = {r >= blk.lo && r < blk.hi, r + 1 >= blk.lo && r + 1 < blk.hi};
+    const T* from = reinterpret_cast<const T*>(a.v) + (blk.row0 + r) * a.v_row + blockIdx.y * a.v_head + 8 * chunk;
+    uint4 raw[2] = {};
+    auto read = [&](int h) {
 #pragma unroll
-            for (int w = 0; w < Threads<D>::k / 32; ++w) most = max(most, maxima[turn][w]);
-        } else {
-#pragma unroll
-            for (int w = 0; w < Threads<D>::v / 32; ++w) most = max(most, maxima[turn][Threads<D>::k / 32 + w]);
-        }
-        const int e_new = exponent_for(__uint_as_float(most)), e = max(e_old, e_new);
+        for (int i = 0; i < 2; ++i)
+            if (is_new[i] && h < a.c.num_kv_heads) raw[i] = *reinterpret_cast<const uint4*>(from + i * a.v_row);
+        from += a.lanes * a.v_head;
+    };
+    read(blockIdx.y);
+    rec += Record8<D>::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16;
+    const int to_exponent = Record8<D>::exponents + 4 - (Record8<D>::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16);
+    int side = 0;
+#pragma unroll 1
+    for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, rec += next_rec, side ^= 1) {
+        int* exponent = reinterpret_cast<int*>(rec + to_exponent);
+        int e_old = kLowestExponent;
+        if (blk.lo > 0) e_old = block_exponent(*exponent);
+        float x[2][8];
+        unpack<T>(raw[0], x[0]);
+        unpack<T>(raw[1], x[1]);
+        read(h + a.lanes);
+        const float top = largest_of_half<D>(largest_finite(x), 1, maxima[side]);
+        const int e_new = exponent_for(top), e = max(e_old, e_new);
         const bool grows = blk.lo > 0 && e_new > e_old;
         bool writes[2] = {is_new[0], is_new[1]};
-        if (grows) {   // the rows that were there before, from their codes
+        if (grows && r < blk.lo) {
             const float scale = power_of_two(e_old);
-            if (p.is_k) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(rec);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (p.r[i] < blk.lo) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(rec + p.at[i]);
-                        float y[4];
-                        decode4(w.x, scale, y);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[i][j] = y[j];
-                        decode4(w.y, scale, y);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[i][4 + j] = y[j];
-                        writes[i] = true;
-                    }
-            } else if (p.r[0] < blk.lo) {
-                const uint4 w4 = *reinterpret_cast<const uint4*>(rec + p.at[0]);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float y[4];
-                    decode4(w[q], scale, y);
-                    x[0][2 * q] = y[0];
-                    x[0][2 * q + 1] = y[2];
-                    if (p.r[1] < blk.lo) {
-                        x[1][2 * q] = y[1];
-                        x[1][2 * q + 1] = y[3];
-                    }
+            for (int q = 0; q < 4; ++q) {
+                float y[4];
+                decode4(w[q], scale, y);
+                x[0][2 * q] = y[0];
+                x[0][2 * q + 1] = y[2];
+                if (r + 1 < blk.lo) {
+                    x[1][2 * q] = y[1];
+                    x[1][2 * q + 1] = y[3];
                 }
-                writes[0] = true;
-                writes[1] = writes[1] || p.r[1] < blk.lo;
             }
+            writes[0] = true;
+            writes[1] = writes[1] || r + 1 < blk.lo;
         }
-        const float inv = power_of_two(-e);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] *= inv;
-        if (p.is_k) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (writes[i])
-                    *reinterpret_cast<uint2*>(rec + p.at[i]) = make_uint2(code_pair(x[i][0], x[i][1]) | code_pair(x[i][2], x[i][3]) << 16,
-                                                                          code_pair(x[i][4], x[i][5]) | code_pair(x[i][6], x[i][7]) << 16);
-        } else if (writes[0] && writes[1]) {
+        scale16(x, power_of_two(-e));
+        if (writes[0] && writes[1]) {
             uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) w[q] = code_pair(x[0][2 * q], x[1][2 * q]) | code_pair(x[0][2 * q + 1], x[1][2 * q + 1]) << 16;
-            *reinterpret_cast<uint4*>(rec + p.at[0]) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(rec) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (writes[i]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) rec[p.at[i] + 2 * j] = (uint8_t)code_pair(x[i][j], 0.0f);
+                    for (int j = 0; j < 8; ++j) rec[i + 2 * j] = (uint8_t)code_pair(x[i][j], 0.0f);
                 }
         }
-        if ((tid == 0 || tid == Threads<D>::k) && (blk.lo == 0 || grows)) *exponent = e;
+        if (t == 0 && (blk.lo == 0 || grows)) *exponent = e;
     }
+}
+
+// blockIdx.y: the first head.
+template <typename T, int D, int TURN>
+__global__ void __launch_bounds__(2 * D, ctas_of<D>(kAppendCtas)) append8_kernel(const __grid_constant__ RowArgs a) {
+    let_next_start();
+    wait_for_previous();
+    __shared__ uint32_t maxima[2][2][D / 32];   // of K and V; one head's and the next's in turn, so one barrier a head is enough
+    Block blk;
+    if (!find_block(a, blockIdx.x, &blk)) return;
+    if (blk.page < 0) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
+        return;
+    }
+    const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * Record8<D>::bytes;
+    uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) + (blk.page * a.c.num_kv_heads + blockIdx.y) * head_bytes +
+                   (((int)blk.first & (a.c.page_size - 1)) >> 4) * Record8<D>::bytes;
+    if (threadIdx.x < D) append_k<T, D, TURN>(a, blk, rec, a.lanes * head_bytes, maxima[0]);
+    else append_v<T, D>(a, blk, rec, a.lanes * head_bytes, maxima[1]);
 }
 
 // 8 values to their row, as TO.
@@ -313,69 +355,67 @@ __device__ __forceinline__ void put8(TO* to, const float (&x)[8]) {
 }
 
 template <typename TO, int D>
-__global__ void __launch_bounds__(Threads<D>::all, kGatherCtas) gather8_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(2 * D, ctas_of<D>(kGatherCtas)) gather8_kernel(const __grid_constant__ RowArgs a) {
     let_next_start();
     wait_for_previous();
     using R = Record8<D>;
     Block blk;
     if (!find_block(a, blockIdx.x, &blk)) return;
-    const bool good = blk.page >= 0;
+    const bool good = blk.page >= 0, is_k = threadIdx.x < D;
     if (!good && threadIdx.x == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
-    const Pieces p = pieces_of_thread<D>();
-    const bool wanted[2] = {p.r[0] >= blk.lo && p.r[0] < blk.hi, p.r[1] >= blk.lo && p.r[1] < blk.hi};
+    // 16 bytes a thread: of K 16 channels of a row, of V 8 channels of two
+    const int t = threadIdx.x & (D - 1), chunk = is_k ? 2 * (t & (D / 16 - 1)) : (t >> 2) & (D / 8 - 1);
+    const int r = is_k ? t / (D / 16) : t / (D / 2) * 8 + (t & 3) * 2;
+    const bool wanted[2] = {r >= blk.lo && r < blk.hi, is_k ? r >= blk.lo && r < blk.hi : r + 1 >= blk.lo && r + 1 < blk.hi};
     if (!wanted[0] && !wanted[1]) return;
-    const int64_t stride = p.is_k ? a.k_row : a.v_row, head = p.is_k ? a.k_head : a.v_head;
-    TO* to = reinterpret_cast<TO*>(const_cast<void*>(p.is_k ? a.k : a.v)) + blockIdx.y * head + p.channel;
+    const int64_t stride = is_k ? a.k_row : a.v_row, head = is_k ? a.k_head : a.v_head, second = is_k ? 8 : stride;
+    TO* to = reinterpret_cast<TO*>(const_cast<void*>(is_k ? a.k : a.v)) + (blk.row0 + r) * stride + blockIdx.y * head + 8 * chunk;
     const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * R::bytes;
-    const uint8_t* rec = reinterpret_cast<const uint8_t*>(a.c.pages) + ((good ? blk.page : 0) * a.c.num_kv_heads + blockIdx.y) * head_bytes +
-                         (((int)blk.first & (a.c.page_size - 1)) >> 4) * R::bytes;
-    uint4 w = {}, next = {};
-    int e = 0, next_e = 0;
-    auto read = [&](int h) {   // K: 8 bytes of each row; V: 16 bytes of both
+    const int at = is_k ? k_place(r, chunk) : R::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16;
+    const int to_exponent = R::exponents + (is_k ? 0 : 4) - at;
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(a.c.pages) + ((good ? blk.page : 0) * a.c.num_kv_heads + blockIdx.y) * head_bytes +
+                          (((int)blk.first & (a.c.page_size - 1)) >> 4) * R::bytes + at;
+    // V's bytes in turn belong to the two rows: put beside those of their row
+    const uint32_t low = is_k ? 0x3210u : 0x6420u, high = is_k ? 0x7654u : 0x7531u;
+    uint4 next = {};
+    int next_e = 0;
+    auto read = [&](int h) {
         if (!good || h >= a.c.num_kv_heads) return;
-        if (p.is_k) {
-            const uint2 u = wanted[0] ? *reinterpret_cast<const uint2*>(rec + p.at[0]) : make_uint2(0, 0);
-            const uint2 v = wanted[1] ? *reinterpret_cast<const uint2*>(rec + p.at[1]) : make_uint2(0, 0);
-            next = make_uint4(u.x, u.y, v.x, v.y);
-        } else {
-            next = *reinterpret_cast<const uint4*>(rec + p.at[0]);
-        }
-        next_e = reinterpret_cast<const int*>(rec + R::exponents)[!p.is_k];
-        rec += a.lanes * head_bytes;
+        next = *reinterpret_cast<const uint4*>(from);
+        next_e = *reinterpret_cast<const int*>(from + to_exponent);
+        from += a.lanes * head_bytes;
     };
     read(blockIdx.y);
 #pragma unroll 1
     for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, to += a.lanes * head) {
-        w = next;
-        e = next_e;
+        const float scale = good ? power_of_two(block_exponent(next_e)) : __int_as_float(0x7FC00000);
+        // words of the first piece (row), then of the second
+        const uint32_t first[2] = {__byte_perm(next.x, next.y, low), __byte_perm(next.x, next.y, high)};
+        const uint32_t last[2] = {__byte_perm(next.z, next.w, low), __byte_perm(next.z, next.w, high)};
+        const uint32_t w[2][2] = {{first[0], is_k ? first[1] : last[0]}, {is_k ? last[0] : first[1], last[1]}};
         read(h + a.lanes);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        const float scale = good ? power_of_two(block_exponent(e)) : __int_as_float(0x7FC00000);
-        float x[2][8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float y[4];
-            decode4(v[q], scale, y);
+        for (int i = 0; i < 2; ++i) {
+            float x[8], y[4];
+            decode4(w[i][0], scale, y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (p.is_k) x[q >> 1][4 * (q & 1) + j] = y[j];
-                else x[j & 1][2 * q + (j >> 1)] = y[j];
-            }
+            for (int j = 0; j < 4; ++j) x[j] = y[j];
+            decode4(w[i][1], scale, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 + j] = y[j];
+            if (wanted[i]) put8(to + i * second, x);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (wanted[i]) put8(to + (blk.row0 + p.r[i]) * stride, x[i]);
     }
 }
 
 // Slots of a step: the place behind the last sequence's, cu[batch] <= rows.
 int64_t slots_of(const RowArgs& a) { return (a.rows >> 4) + 2 * (int64_t)a.c.batch; }
 
-cudaError_t spread(RowArgs& a, int ctas) {
+cudaError_t spread(RowArgs& a, int of_128) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) a.lanes = spread_heads(slots_of(a), a.c.num_kv_heads, (int64_t)sms * ctas, 8);
+    if (e == cudaSuccess) a.lanes = spread_heads(slots_of(a), a.c.num_kv_heads, (int64_t)sms * (a.c.head_dim == 128 ? ctas_of<128>(of_128) : ctas_of<64>(of_128)), 8);
     return e;
 }
 
@@ -386,14 +426,14 @@ cudaError_t append_turn(const RowArgs& a, cudaStream_t st) {
                          : turn == kHalves   ? append8_kernel<T, D, kHalves>
                          : turn == kAdjacent ? append8_kernel<T, D, kAdjacent>
                                              : append8_kernel<T, D, kAny>,
-                         dim3((unsigned)slots_of(a), a.lanes), Threads<D>::all, 0, st, a);
+                         dim3((unsigned)slots_of(a), a.lanes), 2 * D, 0, st, a);
 }
 
 template <typename TO>
 cudaError_t gather_type(const RowArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)slots_of(a), a.lanes);
-    return a.c.head_dim == 128 ? launch_behind(gather8_kernel<TO, 128>, grid, Threads<128>::all, 0, st, a)
-                               : launch_behind(gather8_kernel<TO, 64>, grid, Threads<64>::all, 0, st, a);
+    return a.c.head_dim == 128 ? launch_behind(gather8_kernel<TO, 128>, grid, 256, 0, st, a)
+                               : launch_behind(gather8_kernel<TO, 64>, grid, 128, 0, st, a);
 }
 
 }  // namespace
