@@ -23,6 +23,9 @@ Modules:
                reading each token from the container of its tier.
   paged     -- rotary positions, 4-bit page records and ragged attention over a
                paged cache, from the definitions in include/tkv.h.
+  paged8    -- 8-bit records of a paged cache, their appending and ragged attention
+               over them.
+  beam      -- the choice of beams' continuations, and caches that follow it.
   session   -- a decode session: prefill, per-step append + attention +
                score update, and a re-tier every Delta steps.
 
@@ -32,6 +35,6 @@ routine, a closed form, a hand-derived fixture under ``tests/golden/`` or an
 invariant).  None is "parity unpinned".
 """
 
-from . import fp8, tiering, attention, paged, session  # noqa: F401
+from . import fp8, tiering, attention, paged, paged8, beam, session  # noqa: F401
 
-__all__ = ["fp8", "tiering", "attention", "paged", "session"]
+__all__ = ["fp8", "tiering", "attention", "paged", "paged8", "beam", "session"]
