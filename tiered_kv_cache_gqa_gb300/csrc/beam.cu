@@ -7,11 +7,14 @@
 // keeps per thread a running maximum and sum of exponentials, per CTA the best `count` so far.  A second kernel, started
 // early, joins a sequence's chunks.
 //
-// The best of a chunk.  In the first tile the count-th largest of the maxima of groups of threads (each with its place, so no two are
-// equal) is a bound: `count` values at least reach it, and only the `count` groups whose maxima do can hold any, 128 threads at
-// most, so half a tile at most comes into the list, whatever the values are.  From then on values above the bound are added without a barrier, and the
-// list is sorted, and the bound raised, after tiles 2, 4, 8, ..: of values in random order each stretch brings about `count`.
-// Values that rise along the vocabulary can overflow the list: the chunk is then looked over again, every tile like the first.
+// The best of a chunk.  While the logits stream past, a thread only notes the maximum of each of its cells (its 32 values of a tile, of
+// as many tiles as make 16 cells of the chunk): choosing from every tile, with its barriers, took 12 us of 39 for 512 rows of 131,072.
+// Behind the stream the count-th largest maximum of all cells is a bound: no more than `count` cells lie above it, and only those
+// and the ones that are equal to it can hold any of the best.  They are read once more.
+// Where too many maxima are equal (a mask, say) the chunk is looked over tile by tile instead.  There, and where the chunk is one
+// tile, the bound is the count-th largest of the maxima of groups of threads, each with its place, so that no two are equal:
+// `count` values at least reach it, and only the `count` groups whose maxima do can hold any, so a quarter of a tile at most
+// comes into the list, whatever the values are.
 //
 // What bounds it is memory, then issue: a 16-bit value costs three and a half instructions (half of a maximum, one to unpack, half a
 // fused multiply-add, an exponential, half a sum).
@@ -29,10 +32,10 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCount = 64, kMaxBeams = 64;
 constexpr int kVectors = 4;                       // 16-byte pieces of a thread and tile
 constexpr int kCtas = 4;                          // on an SM at once, by their registers
-constexpr int kSortFirst = 2;                     // tiles before the list is sorted first, and each time as many times more
+constexpr int kCells = 16;                        // of a thread
 constexpr int kIndexBits = 12;                    // of a candidate's index in the joining kernel
 constexpr int kMostCandidates = 1 << kIndexBits;  // of a sequence
-constexpr int kMostGroups = 128;
+constexpr int kMostGroups = kThreads;
 constexpr int kFew = 128;                         // candidates of a sequence that are sorted whole
 constexpr float kLog2E = 1.44269504f;
 constexpr float kFar = 3e38f;
@@ -100,9 +103,17 @@ __device__ __forceinline__ void kth_largest(uint64_t mine, int k, int shift, uin
     }
     if (mine && rank == k - 1) *bound = mine;
 }
-// Groups are as large as leaves twice as many of them as wanted, and at least 8: their k largest then reach little further down than
-// single threads' would, and k of them have at most 128 threads.
-__device__ __forceinline__ int group_shift(int k) { return min(5, 31 - __clz(kThreads / 2 / k)); }
+// Groups are as large as leaves four times as many of them as wanted, and at least 8: their k largest then reach little further down
+// than single threads' would, and k of them have at most kGroupThreads threads.
+constexpr int kGroupThreads = 64;
+__device__ __forceinline__ int group_shift(int k) { return min(5, 31 - __clz(kGroupThreads / k)); }
+
+// How many groups have a thread with `has`, to every thread.
+__device__ __forceinline__ int groups_with(bool has, int shift) {
+    const int lane = threadIdx.x & 31, in_group = lane & ~((1 << shift) - 1);
+    const uint32_t with = __ballot_sync(0xffffffffu, has), group = (shift == 5 ? 0xffffffffu : (1u << (1 << shift)) - 1) << in_group;
+    return __syncthreads_count((lane == in_group) && (with & group));
+}
 
 // The best `count` of keys[0 .. n) (all different) into list, in order.  Barriers around it are the caller's.
 __device__ __forceinline__ void sort_best(const uint64_t* keys, int n, int count, uint64_t* list) {
@@ -136,72 +147,52 @@ __device__ __forceinline__ float2 two_of(uint4 u, int i) {
     else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-// The largest of a thread's pieces; NaN counts only where nothing else is.
-template <typename T>
-__device__ __forceinline__ float largest(const uint4 (&raw)[kVectors]) {
-    float top = -INFINITY;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < kVectors; ++i) top = fmaxf(fmaxf(fmaxf(top, __uint_as_float(raw[i].x)), fmaxf(__uint_as_float(raw[i].y), __uint_as_float(raw[i].z))), __uint_as_float(raw[i].w));
-    } else {
-        using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-        P m[4];
-#pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const P x = *reinterpret_cast<const P*>(&w[j]);
-                m[j] = i ? __hmax2(m[j], x) : x;
-            }
-        }
-        const P x = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
-        top = fmaxf(fmaxf(top, to_float(x.x)), to_float(x.y));
-    }
-    return top;
+// 16-bit values are compared two at a time.
+template <typename T> struct Two { using type = float; };
+template <> struct Two<__half> { using type = __half2; };
+template <> struct Two<__nv_bfloat16> { using type = __nv_bfloat162; };
+__device__ __forceinline__ float max2(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ __half2 max2(__half2 a, __half2 b) { return __hmax2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 max2(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(a, b); }
+__device__ __forceinline__ float larger_of(float x) { return x; }
+__device__ __forceinline__ float larger_of(__half2 x) { return fmaxf(__low2float(x), __high2float(x)); }
+__device__ __forceinline__ float larger_of(__nv_bfloat162 x) { return fmaxf(__low2float(x), __high2float(x)); }
+// Both halves as large as the least value of their type that is not below x.
+template <typename P> __device__ __forceinline__ P both_at_least(float x);
+template <> __device__ __forceinline__ float both_at_least<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half2 both_at_least<__half2>(float x) { return __half2half2(__float2half_ru(x)); }
+template <> __device__ __forceinline__ __nv_bfloat162 both_at_least<__nv_bfloat162>(float x) { return __bfloat162bfloat162(__float2bfloat16_ru(x)); }
+__device__ __forceinline__ uint32_t reach(float x, float low) { return x >= low ? 0xFFFFFFFFu : 0u; }
+__device__ __forceinline__ uint32_t reach(__half2 x, __half2 low) { return __hge2_mask(x, low); }
+__device__ __forceinline__ uint32_t reach(__nv_bfloat162 x, __nv_bfloat162 low) { return __hge2_mask(x, low); }
+
+// The largest of a piece (of each half of its words); NaN counts only where nothing else is.
+template <typename P>
+__device__ __forceinline__ P largest_of(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const P* x = reinterpret_cast<const P*>(w);
+    return max2(max2(x[0], x[1]), max2(x[2], x[3]));
 }
 
-// Which of a thread's values reach `lowest`: a bit each, see value_of_bit.
-template <typename T>
-__device__ __forceinline__ uint32_t at_least(const uint4 (&raw)[kVectors], float lowest) {
-    uint32_t bits = 0;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bits |= __uint_as_float(w[j]) >= lowest ? 1u << (4 * i + j) : 0u;
-        }
-    } else {
-        using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-        P low;   // rounded up: no value of T lies in between
-        if constexpr (std::is_same<T, __half>::value) low = __half2half2(__float2half_ru(lowest));
-        else low = __bfloat162bfloat162(__float2bfloat16_ru(lowest));
-#pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bits |= __hge2_mask(*reinterpret_cast<const P*>(&w[j]), low) & 0x00010001u << (4 * i + j);
-            }
-        }
-    }
-    return bits;
+// Which values of a piece reach `low`: bit j for the low half of word j, bit 16 + j for the high one; bit j for word j of 32 bits.
+template <typename P>
+__device__ __forceinline__ uint32_t at_least(uint4 u, P low) {
+    constexpr uint32_t kBit = sizeof(P) == 4 && std::is_same<P, float>::value ? 1u : 0x00010001u;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const P* x = reinterpret_cast<const P*>(w);
+    return (reach(x[0], low) & kBit) | (reach(x[1], low) & kBit << 1) | (reach(x[2], low) & kBit << 2) | (reach(x[3], low) & kBit << 3);
 }
 
-// 16 bits a value: the low halves of the words first, then the high ones.
+// A bit's value, and its place in the piece.
 template <typename T>
-__device__ __forceinline__ int value_of_bit(int bit) { return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4); }
-
-// The value of a bit.
-template <typename T>
-__device__ __forceinline__ float value_at(const uint4 (&raw)[kVectors], int bit) {
-    uint4 u = bit & 8 ? (bit & 4 ? raw[3] : raw[2]) : (bit & 4 ? raw[1] : raw[0]);
+__device__ __forceinline__ float value_at(uint4 u, int bit) {
     const uint32_t w = bit & 2 ? (bit & 1 ? u.w : u.z) : (bit & 1 ? u.y : u.x);
     if constexpr (sizeof(T) == 4) return __uint_as_float(w);
     const uint16_t h = (uint16_t)(bit & 16 ? w >> 16 : w);
     return to_float(*reinterpret_cast<const T*>(&h));
 }
+template <typename T>
+__device__ __forceinline__ int place_of(int bit) { return sizeof(T) == 4 ? bit : 2 * (bit & 3) + (bit >> 4); }
 
 // The block's reference and sum, to every thread.  `stats` is written again behind a barrier.
 __device__ __forceinline__ Stat join_stats(Stat a, Stat b) {
@@ -219,23 +210,102 @@ __device__ __forceinline__ Stat sum_block(Stat t, Stat (&stats)[kWarps]) {
     return t;
 }
 
+constexpr int kMost = kGroupThreads * 32 + kMaxCount;   // values in a list: what one tile can bring, and the best so far
+
+// The best so far: a list that the CTA adds to and sorts.
+struct Best {
+    uint64_t keys[kMost], list[kMaxCount];
+    __align__(16) uint64_t maxima[kMostGroups];
+    uint64_t bound;
+    int found;
+};
+
+// What a thread knows of it.
+struct Bound {
+    float lowest;     // values below it are none of the best
+    uint64_t least;   // and keys below this
+    int held;         // in the list, sorted
+};
+
+__device__ __forceinline__ void add_key(Best& best, uint64_t k) {
+    const int slot = atomicAdd(&best.found, 1);
+    if ((uint32_t)slot < (uint32_t)kMost) best.keys[slot] = k;
+}
+
+// Adds a piece's values that reach the bound; v0: the place of its first.
+template <typename T>
+__device__ __forceinline__ void add_piece(Best& best, uint4 u, int v0, const Bound& b) {
+    using P = typename Two<T>::type;
+    for (uint32_t bits = at_least(u, both_at_least<P>(b.lowest)); bits; bits &= bits - 1) {
+        const int bit = __ffs(bits) - 1;
+        const float x = value_at<T>(u, bit);
+        const uint64_t k = key_of(x, v0 + place_of<T>(bit));
+        if (k >= b.least && x > -INFINITY) add_key(best, k);
+    }
+}
+
+// A tile's part of the best: pieces p + i kThreads + tid.  Tiles come in order.
+template <typename T>
+__device__ __forceinline__ void look_over(Best& best, const uint4 (&raw)[kVectors], int p, int count, Bound& b) {
+    using P = typename Two<T>::type;
+    constexpr int E = 16 / sizeof(T);
+    const int tid = threadIdx.x;
+    P tops[kVectors];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) tops[i] = largest_of<P>(raw[i]);
+    const float top = larger_of(max2(max2(tops[0], tops[1]), max2(tops[2], tops[3])));
+    const bool has = top > -INFINITY && top >= b.lowest;
+    const int shift = group_shift(count), above = groups_with(has, shift);
+    if (above == 0) return;
+    if (above > count) {   // otherwise all of theirs come into the list
+        int at = 0;                                        // the lowest place of the largest
+#pragma unroll
+        for (int i = kVectors - 1; i >= 0; --i) {
+            const uint32_t bits = at_least(raw[i], both_at_least<P>(top));
+            const int low = place_of<T>(__ffs(bits) - 1), high = sizeof(T) == 2 && bits >> 16 ? place_of<T>(__ffs(bits >> 16) + 15) : E;
+            if (bits) at = (p + i * kThreads + tid) * E + min(sizeof(T) == 2 && !(bits & 0xFFFFu) ? E : low, high);
+        }
+        kth_largest(has ? key_of(top, at) : 0, count, shift, best.maxima, &best.bound);
+        __syncthreads();
+        if (best.bound > b.least) {
+            b.least = best.bound;
+            b.lowest = of_ordered((uint32_t)(b.least >> 32));
+        }
+    }
+    if (top >= b.lowest && top > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+            if (larger_of(tops[i]) >= b.lowest) add_piece<T>(best, raw[i], (p + i * kThreads + tid) * E, b);
+    }
+    __syncthreads();
+    const int n = best.found;
+    sort_best(best.keys, n, count, best.list);
+    b.held = min(n, count);
+    __syncthreads();
+    if (b.held == count) {
+        b.least = best.list[count - 1] + 1;
+        b.lowest = of_ordered((uint32_t)(best.list[count - 1] >> 32) + 1);   // the next number: what is equal comes too late
+    }
+    if (tid < b.held) best.keys[tid] = best.list[tid];
+    if (tid == 0) best.found = b.held;
+    __syncthreads();
+}
+
 // blockIdx.x: chunk, blockIdx.y (and z, behind 65,535 rows): row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __grid_constant__ SelectArgs a) {
-    constexpr int E = 16 / sizeof(T), N = kVectors * E;         // values of a piece, of a thread and tile
-    constexpr int kMost = 128 * N + kMaxCount;                  // values in the list: what one tile can bring, and the best so far
+    using P = typename Two<T>::type;
+    constexpr int E = 16 / sizeof(T);                           // values of a piece
     constexpr int kTile = kVectors * kThreads;                  // pieces
-    __shared__ uint64_t keys[kMost], list[kMaxCount];
-    __shared__ __align__(16) uint64_t maxima[kMostGroups];
-    __shared__ uint64_t bound;
-    __shared__ int found;
+    __shared__ Best best;
+    __shared__ float cells[kCells][kThreads];
     __shared__ Stat stats[kWarps];
     wait_for_previous();
     let_next_start();   // not earlier: the joining kernel reads scores and finished before its own wait
-    const int row = blockIdx.y + blockIdx.z * 65535, tid = threadIdx.x, lane = tid & 31;
+    const int row = blockIdx.y + blockIdx.z * 65535, tid = threadIdx.x;
     if (row >= a.batch * a.beams) return;
-    const int b = row / a.beams, w = row - b * a.beams;
-    const T* x0 = reinterpret_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
+    const int seq = row / a.beams, w = row - seq * a.beams;
+    const T* x0 = reinterpret_cast<const T*>(a.logits) + seq * a.batch_stride + w * a.beam_stride;
     // Piece p is values p E .. p E + E - 1 of the row wherever the row begins, so that equal rows have equal sums: of a row that does not
     // begin on 16 bytes it is put together from two of memory's pieces.
     const int shift = (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
@@ -257,18 +327,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     // The thread's maximum m and sum of 2^(x log2 e - c), c = m log2 e rounded: one fused multiply-add a pair.  Beyond 3e38 c stays there
     // and the sum is 0 or infinite: the row is then added up again below.
     float m = kFloor, c = -kFar, sum = 0.0f;
-    float lowest = -INFINITY;      // values below it are none of the best; the bound's
-    uint64_t least = 0;            // the bound: keys below it are none of the best
-    int held = 0, sort_at = kSortFirst;   // tiles after which the list is sorted next
-    bool careful = false;          // every tile like the first: the second time over a chunk
-    uint4 next[kVectors];
+    uint4 raw[kVectors], next[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
     if (is_out(a, row)) return;
-    if (tid == 0) found = 0;
+    if (tid == 0) best.found = 0;
+    const int tiles = (end - first + kTile - 1) / kTile, span = (tiles + kCells - 1) / kCells;   // tiles of a cell
+    float cell = -INFINITY;
+    int in_cell = 0, cell_at = tid;
 #pragma unroll 1
-    for (int p = first, tile = 1; p < end; p += kTile, ++tile) {
-        uint4 raw[kVectors];
+    for (int p = first; p < end; p += kTile) {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) raw[i] = next[i];
         if (!shift && p + 2 * kTile <= min(end, whole)) {
@@ -278,104 +346,125 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < kVectors; ++i) next[i] = load(p + kTile + i * kThreads + tid);
         }
-        const float top = largest<T>(raw);
-        if (!careful) {
-            if (top > m) {
-                const float z = fminf(fmaxf(top * kLog2E, -kFar), kFar);
-                sum *= exp2_fast(c - z);
-                m = top;
-                c = z;
-            }
-            F2 s[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-            const F2 minus = f2(-c, -c), log2e = f2(kLog2E, kLog2E);
+        P tops = largest_of<P>(raw[0]);
 #pragma unroll
-            for (int i = 0; i < kVectors; ++i)
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    const float2 x = two_of<T>(raw[i], j), y = parts(fma2(f2(x.x, x.y), log2e, minus));
-                    s[j & 1] = add2(s[j & 1], f2(exp2_fast(y.x), exp2_fast(y.y)));
-                }
-            const float2 both = parts(add2(s[0], s[1]));
-            sum += both.x + both.y;
+        for (int i = 1; i < kVectors; ++i) tops = max2(tops, largest_of<P>(raw[i]));
+        const float top = larger_of(tops);
+        cell = fmaxf(cell, top);
+        if (++in_cell == span) {
+            (&cells[0][0])[cell_at] = cell;
+            cell_at += kThreads;
+            in_cell = 0;
+            cell = -INFINITY;
         }
-        // ---- the tile's part of the best
-        auto place = [&](int i, int j) { return (p + i * kThreads + tid) * E + j; };
-        const bool sorts = careful || tile == sort_at || p + kTile >= end;
-        if (tile == 1 || careful) {
-            // groups with a value above the bound: where they are no more than `count`, all of theirs come into the list
-            const bool has = top > -INFINITY && top >= lowest;
-            const uint32_t with = __ballot_sync(0xffffffffu, has);
-            const int shift_of = group_shift(a.count), in_group = lane & ~((1 << shift_of) - 1);
-            const uint32_t group = (shift_of == 5 ? 0xffffffffu : (1u << (1 << shift_of)) - 1) << in_group;
-            const int above = __syncthreads_count((lane == in_group) && (with & group));
-            if (above > a.count) {
-                const uint32_t tops = at_least<T>(raw, top);
-                int i = value_of_bit<T>(__ffs(tops) - 1);                            // the lowest place of them
-                if (sizeof(T) == 2 && tops >> 16) i = min((tops & 0xFFFFu) ? i : N, value_of_bit<T>(__ffs(tops >> 16) + 15));
-                const uint64_t mine = has ? key_of(top, place(i / E, i % E)) : 0;
-                kth_largest(mine, a.count, shift_of, maxima, &bound);
+        if (top > m) {
+            const float z = fminf(fmaxf(top * kLog2E, -kFar), kFar);
+            sum *= exp2_fast(c - z);
+            m = top;
+            c = z;
+        }
+        F2 s[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+        const F2 minus = f2(-c, -c), log2e = f2(kLog2E, kLog2E);
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const float2 x = two_of<T>(raw[i], j), y = parts(fma2(f2(x.x, x.y), log2e, minus));
+                s[j & 1] = add2(s[j & 1], f2(exp2_fast(y.x), exp2_fast(y.y)));
+            }
+        const float2 both = parts(add2(s[0], s[1]));
+        sum += both.x + both.y;
+    }
+    if (in_cell) (&cells[0][0])[cell_at] = cell;
+    // ---- the best
+    Bound b{-INFINITY, 0, 0};
+    __syncthreads();
+    bool by_tiles = false;
+    if (tiles == 1) {
+        look_over<T>(best, raw, first, a.count, b);
+    } else {
+        // A bound from below: `count` groups of threads at least have a value that reaches it.  Then the cells that do.
+        const int used = (tiles + span - 1) / span, group = group_shift(a.count);
+        const bool has = m > kFloor;
+        float low = -INFINITY;
+        if (groups_with(has, group) > a.count) {
+            kth_largest(has ? (uint64_t)ordered(m) << 32 | (uint32_t)~tid : 0, a.count, group, best.maxima, &best.bound);
+            __syncthreads();
+            low = of_ordered((uint32_t)(best.bound >> 32));
+        }
+        if (m >= low)
+            for (int i = 0; i < used; ++i) {
+                const float x = cells[i][tid];
+                if (x >= low && x > -INFINITY) add_key(best, (uint64_t)ordered(x) << 32 | (uint32_t)(i * kThreads + tid));
+            }
+        __syncthreads();
+        int n = best.found;
+        by_tiles = n > kMost;
+        if (!by_tiles) {
+            if (n >= a.count) {
+                sort_best(best.keys, n, a.count, best.list);
                 __syncthreads();
-                if (bound > least) {
-                    least = bound;
-                    lowest = of_ordered((uint32_t)(least >> 32));
-                }
+                b.lowest = of_ordered((uint32_t)(best.list[a.count - 1] >> 32));   // the count-th largest cell's
             }
-        }
-        if (top >= lowest && top > -INFINITY)
-            for (uint32_t from = at_least<T>(raw, lowest); from; from &= from - 1) {
-                const int bit = __ffs(from) - 1, i = value_of_bit<T>(bit);
-                const float x = value_at<T>(raw, bit);
-                const uint64_t k = key_of(x, place(i / E, i % E));
-                if (k >= least && x > -INFINITY) {
-                    const int slot = atomicAdd(&found, 1);
-                    if ((uint32_t)slot < (uint32_t)kMost) keys[slot] = k;
-                }
+            // The cells that reach it move to the front: keys, of which no two are equal, become places in that order.
+            for (int i = tid; i < n; i += kThreads) {
+                const uint64_t k = best.keys[i];
+                if (of_ordered((uint32_t)(k >> 32)) < b.lowest) best.keys[i] = 0;
             }
-        if (!sorts) continue;
-        sort_at *= kSortFirst;
-        __syncthreads();
-        const int n = found;
-        if (n > kMost) {           // only if not careful: a tile like the first brings no more than there is room for
             __syncthreads();
-            careful = true;
-            least = 0;
-            lowest = -INFINITY;
-            held = 0;
-            if (tid == 0) found = 0;
+            if (tid == 0) best.found = 0;
+            uint32_t mine[kMost / kThreads + 1];
 #pragma unroll
-            for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
-            for (int q = p + kTile; q < end; q += kTile)   // what is left of the sum
-                for (int i = 0; i < kVectors; ++i) {
-                    const uint4 u = load(q + i * kThreads + tid);
-                    for (int j = 0; j < E / 2; ++j) {
-                        const float2 x = two_of<T>(u, j);
-                        const float t = fmaxf(m, fmaxf(x.x, x.y)), z = fminf(fmaxf(t * kLog2E, -kFar), kFar);
-                        sum = sum * exp2_fast(c - z) + exp2_fast(fmaf(x.x, kLog2E, -z)) + exp2_fast(fmaf(x.y, kLog2E, -z));
-                        m = t;
-                        c = z;
-                    }
-                }
-            p = first - kTile;
+            for (int i = 0; i <= kMost / kThreads; ++i) mine[i] = i * kThreads + tid < n && best.keys[i * kThreads + tid] ? (uint32_t)best.keys[i * kThreads + tid] : 0xFFFFFFFFu;
             __syncthreads();
-            continue;
+            int* places = reinterpret_cast<int*>(best.maxima);   // of cells: no more are looked into
+            constexpr int kPlaces = sizeof(best.maxima) / sizeof(int);
+#pragma unroll
+            for (int i = 0; i <= kMost / kThreads; ++i)
+                if (mine[i] != 0xFFFFFFFFu) {
+                    const int slot = atomicAdd(&best.found, 1);
+                    if (slot < kPlaces) places[slot] = (int)mine[i];
+                }
+            __syncthreads();
+            n = best.found;
+            by_tiles = n > kPlaces;
+            __syncthreads();
+            if (tid == 0) best.found = 0;
+            __syncthreads();
+            if (!by_tiles) {
+                for (int i = tid; i < n * span * kVectors; i += kThreads) {
+                    const int cell_of = places[i / (span * kVectors)], in = i % (span * kVectors);
+                    const int q = first + (cell_of / kThreads * span + in / kVectors) * kTile + in % kVectors * kThreads + cell_of % kThreads;
+                    add_piece<T>(best, load(q), q * E, b);
+                }
+                __syncthreads();
+                n = best.found;
+                by_tiles = n > kMost;
+                if (!by_tiles) {
+                    sort_best(best.keys, n, a.count, best.list);
+                    b.held = min(n, a.count);
+                }
+            }
+            __syncthreads();
         }
-        sort_best(keys, n, a.count, list);
-        held = min(n, a.count);
-        __syncthreads();
-        if (held == a.count) {
-            least = list[a.count - 1] + 1;
-            lowest = of_ordered((uint32_t)(least >> 32));
+        if (by_tiles) {
+            __syncthreads();   // everyone has read it
+            if (tid == 0) best.found = 0;
+            b = Bound{-INFINITY, 0, 0};
+            __syncthreads();
+            for (int p = first; p < end; p += kTile) {
+#pragma unroll
+                for (int i = 0; i < kVectors; ++i) raw[i] = load(p + i * kThreads + tid);
+                look_over<T>(best, raw, p, a.count, b);
+            }
         }
-        if (tid < held) keys[tid] = list[tid];
-        if (tid == 0) found = held;
-        __syncthreads();
     }
     // ---- the chunk's reference and sum
     if (fabsf(c) < kFar) sum *= exp2_fast(-fmaf(m, kLog2E, -c));   // from c to m
     const int64_t at = (int64_t)row * a.chunks + blockIdx.x;
     Stat t = sum_block(Stat{m, sum}, stats);
-    if (held && !(t.sum > 0.0f && t.sum < INFINITY)) {   // the largest beyond 2e38 either way, or a NaN or an infinity: the slow way
-        m = of_ordered((uint32_t)(list[0] >> 32));
+    if (b.held && !(t.sum > 0.0f && t.sum < INFINITY)) {   // the largest beyond 2e38 either way, or a NaN or an infinity: the slow way
+        m = of_ordered((uint32_t)(best.list[0] >> 32));
         sum = 0.0f;
         for (int p = first + tid; p < end; p += kThreads) {
             const uint4 u = load(p);
@@ -388,7 +477,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         t = sum_block(Stat{m, sum}, stats);
     }
     if (tid == 0) a.stats[at] = t;
-    if (tid < a.count) a.best[at * a.count + tid] = tid < held ? Candidate{of_ordered((uint32_t)(list[tid] >> 32)), (int)~(uint32_t)list[tid]} : Candidate{0.0f, -1};
+    if (tid < a.count) {
+        const uint64_t k = best.list[tid];
+        a.best[at * a.count + tid] = tid < b.held ? Candidate{of_ordered((uint32_t)(k >> 32)), (int)~(uint32_t)k} : Candidate{0.0f, -1};
+    }
 }
 
 // ------------------------------------------------------------------ joining
@@ -421,8 +513,8 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     __shared__ bool is_done[kMaxBeams];
     __shared__ Wide offset[kMaxBeams];                            // total = (x - reference) + offset
     __shared__ __align__(16) uint64_t maxima[kMostGroups];
-    __shared__ uint64_t keys[128 * kEach];
-    __shared__ int tokens[128 * kEach];
+    __shared__ uint64_t keys[kGroupThreads * kEach];
+    __shared__ int tokens[kGroupThreads * kEach];
     __shared__ uint64_t bound;
     __shared__ int found;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, per_row = a.chunks * a.count, n = a.beams * per_row;
@@ -494,9 +586,8 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     for (int i = tid + kEarly * kThreads; i < n; i += kThreads) mine = max(mine, key_of_candidate(i, best[i]));
     // few candidates are sorted as they are
     if (n > kFew) {
-        const int shift_of = group_shift(a.count), in_group = lane & ~((1 << shift_of) - 1);
-        const uint32_t with = __ballot_sync(0xffffffffu, mine != 0), group = (shift_of == 5 ? 0xffffffffu : (1u << (1 << shift_of)) - 1) << in_group;
-        if (__syncthreads_count((lane == in_group) && (with & group)) > a.count) kth_largest(mine, a.count, shift_of, maxima, &bound);
+        const int shift = group_shift(a.count);
+        if (groups_with(mine != 0, shift) > a.count) kth_largest(mine, a.count, shift, maxima, &bound);
     }
     __syncthreads();
     const uint64_t least = bound;
