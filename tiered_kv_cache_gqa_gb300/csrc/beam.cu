@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     }
 }
 
-// How the rows are cut: as many CTAs as the device holds at once, chunks of 256 pieces at least, and no more candidates than the
+// How the rows are cut: as many CTAs as the device holds at once, chunks of 512 pieces at least, and no more candidates than the
 // joining kernel takes.
 struct Split {
     int chunks, per_chunk;   // pieces of a chunk
@@ -632,7 +632,7 @@ struct Split {
 Split split_rows(int64_t rows, int beams, int vocab, int count, int element, int sms) {
     const int pieces = (vocab + 16 / element - 1) / (16 / element);
     int64_t chunks = std::max<int64_t>(1, (int64_t)sms * kCtas / rows);
-    chunks = std::min<int64_t>(chunks, (pieces + kThreads - 1) / kThreads);
+    chunks = std::min<int64_t>(chunks, (pieces + 2 * kThreads - 1) / (2 * kThreads));
     chunks = std::min<int64_t>(chunks, std::max(1, kMostCandidates / (beams * count)));
     Split s;
     s.per_chunk = (int)((pieces + chunks - 1) / chunks);
@@ -659,7 +659,7 @@ cudaError_t device_sms(int* sms) {
 // a permutation needs no second buffer.  Pages before the current one are only read from then on, so that beams may share them.
 // A CTA serves one cache and one sequence of beams: it reads the sequence's parents, lengths and pages once (three trips to memory
 // in a row) and walks over 16-byte pieces.
-constexpr int kMaxCaches = 64;   // of a launch
+constexpr int kMaxCaches = 128;   // of a launch: 5 KB of arguments
 
 struct CacheRef {
     uint8_t* pages;
@@ -684,9 +684,8 @@ struct ReorderArgs {
 
 template <int W>
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
-    __shared__ int parent[W], page[W];
+    __shared__ int page[W], length;
     __shared__ uint32_t children[W];   // beams that go on from this one, itself not among them
-    __shared__ int length, bad;
     let_next_start();
     wait_for_previous();
     const int tid = threadIdx.x;
@@ -698,44 +697,41 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     unit /= parts_of;
     const int64_t group = unit % a.groups;
     const CacheRef& c = a.cache[is_table ? 0 : (int)(unit / a.groups)];
-    if (tid == 0) {
-        length = a.lengths[group * a.beams];
-        bad = 0;
-    }
-    if (tid < W) children[tid] = 0;
-    __syncthreads();
-    const int len = length, column = len >> a.page_shift, rest = len & ((1 << a.page_shift) - 1);
-    const bool fits = len >= 0 && (column < a.max_pages || (column == a.max_pages && rest == 0));
-    if (tid < a.beams) {
+    if (tid < 32) {   // a lane a beam
         const int64_t seq = group * a.beams + tid;
-        int p = a.parents[seq], pg = -1;
+        const bool is_beam = tid < a.beams;
+        int p = is_beam ? a.parents[seq] : -1;
+        const int mine = is_beam ? a.lengths[seq] : 0, len = __shfl_sync(0xffffffffu, mine, 0);
+        const int column = len >> a.page_shift, rest = len & ((1 << a.page_shift) - 1);
+        const bool fits = len >= 0 && (column < a.max_pages || (column == a.max_pages && rest == 0));
+        const bool same = __all_sync(0xffffffffu, !is_beam || mine == len), has_page = is_beam && fits && rest && !is_table;
+        const int pg = has_page ? a.table[seq * a.max_pages + column] : -1;
+        int report = !same ? TKV_EINVAL : !fits ? TKV_ECAPACITY : TKV_OK;
         if (p >= a.beams) {
-            raise_status(a.status, TKV_EINVAL);
+            report = max(report, (int)TKV_EINVAL);
             p = -1;
         }
-        if (a.lengths[seq] != len) atomicOr(&bad, 1);
-        if (fits && rest) pg = a.table[seq * a.max_pages + column];
-        parent[tid] = p < 0 ? tid : p;   // none: it stays
-        page[tid] = pg;
-    }
-    __syncthreads();
-    if (bad || !fits) {
-        if (tid == 0 && part == 0) raise_status(a.status, bad ? TKV_EINVAL : TKV_ECAPACITY);
-        return;
-    }
-    if (tid < a.beams && parent[tid] != tid) {
-        const int p = parent[tid];
-        bool goes = true;
-        if (!is_table) {
-            goes = page[p] != page[tid];
-            if (rest && ((uint32_t)page[p] >= c.num_pages || (uint32_t)page[tid] >= c.num_pages)) {
-                if (part == 0) raise_status(a.status, TKV_ECAPACITY);
+        if (p < 0) p = tid;   // none: it stays
+        const int from = __shfl_sync(0xffffffffu, pg, p);
+        bool goes = is_beam && p != tid && same && fits;
+        if (goes && !is_table) {
+            goes = from != pg;
+            if (rest && ((uint32_t)from >= c.num_pages || (uint32_t)pg >= c.num_pages)) {
+                report = max(report, (int)TKV_ECAPACITY);
                 goes = false;
             }
         }
-        if (goes) atomicOr(&children[p], 1u << tid);
+        if (report != TKV_OK && part == 0) raise_status(a.status, report);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint32_t of = __ballot_sync(0xffffffffu, goes && p == i);
+            if (tid == i) children[i] = of;
+        }
+        if (tid < W) page[tid] = pg;
+        if (tid == 0) length = len;
     }
     __syncthreads();
+    const int len = length, column = len >> a.page_shift, rest = len & ((1 << a.page_shift) - 1);
     uint32_t kids[W];
     bool any = false;
 #pragma unroll
@@ -875,8 +871,9 @@ extern "C" tkv_status tkv_paged_reorder(const tkv_paged* caches, int32_t num_cac
             r.head_bytes = (int64_t)(c.page_size / r.per) * r.unit * r.parts;
             most = std::max(most, r.head_bytes * r.heads / 16);
         }
-        // CTAs: two times what the device holds, none without a piece
-        const int64_t wanted = std::max<int64_t>(1, (int64_t)sms * 16 / (a.groups * a.num_caches));
+        // CTAs: eight times what the device holds at once, none without a piece (80 layers of 8 x 8 beams: 80.5 us; with four times as many
+        // 84.6, with two 94, with sixteen 95)
+        const int64_t wanted = std::max<int64_t>(1, (int64_t)sms * 32 / (a.groups * a.num_caches));
         a.split = (int)std::min(wanted, (most + kThreads - 1) / kThreads);
         a.table_split = from ? 0 : std::max(1, std::min((a.max_pages + kThreads - 1) / kThreads, 16));
         const int64_t grid = a.groups * ((int64_t)a.num_caches * a.split + a.table_split);
