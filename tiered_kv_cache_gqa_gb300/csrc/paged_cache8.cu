@@ -10,7 +10,9 @@
 //
 // A CTA's block.  A sequence's n rows touch at most (n + 14) / 16 + 1 blocks, so the slots from (cu[b] >> 4) + 2 b up to
 // (cu[b + 1] >> 4) + 2 (b + 1) hold them all wherever they begin: slots are CTAs, the sequence of a slot is found by a search over cu,
-// 32 lanes at a time (one trip to memory up to 32 sequences, two up to 1,024), and at most 2 slots a sequence stay idle.
+// 32 lanes at a time (one trip to memory up to 32 sequences, two up to 1,024), and at most 2 slots a sequence stay idle.  What a CTA
+// waits for at its begin is memory: the search, then the page together with the first head's values and the positions, then the
+// angles; in a prompt each of its two rounds of CTAs spent 4.7 of 14 us there while the page was asked for first.
 //
 // What bounds both is memory: 2 bytes a value on one side, 1 on the other.
 #include "paged_rows.cuh"
@@ -28,26 +30,44 @@ constexpr int gather_ctas() { return D == 128 ? 8 : 12; }
 
 // A block of a step: its new rows are those at offsets [lo, hi), row0 + offset in the step's tensors.
 struct Block {
-    int64_t first, row0, page;   // position of offset 0; page -1: it has no place
-    int lo, hi;
+    int64_t first, row0;   // position of offset 0
+    int lo, hi, page;      // page: as the table has it, or -1; on its way when find_block returns
 };
 
 // The block of a slot; false: the slot has none.  Every lane of the warp calls it.
 __device__ __forceinline__ bool find_block(const RowArgs& a, int64_t slot, Block* k) {
     const int lane = threadIdx.x & 31;
     int begin = 0, len = a.c.batch;   // sequences [begin, begin + len) are not known yet; those before begin at or before the slot
+    int64_t c0 = 0, c1 = 0, length = 0;
+    bool known = false;
     while (len > 0) {
         const int step = (len + 31) / 32, at = lane * step;
-        const bool before = at < len && (int64_t)(a.cu[begin + at] >> 4) + 2 * (int64_t)(begin + at) <= slot;
+        const int mine = at < len ? a.cu[begin + at] : 0;
+        int next = 0, its = 0;
+        if (step == 1 && at < len) {   // the last round: what is wanted of the sequence comes along
+            next = a.cu[begin + at + 1];
+            its = a.c.lengths[begin + at];
+        }
+        const bool before = at < len && (int64_t)(mine >> 4) + 2 * (int64_t)(begin + at) <= slot;
         const int n = __popc(__ballot_sync(0xffffffffu, before));
         if (n == 0) break;
-        const int known = (n - 1) * step + 1;
-        begin += known;
-        len = min(step - 1, len - known);
+        if (step == 1) {
+            c0 = __shfl_sync(0xffffffffu, mine, n - 1);
+            c1 = __shfl_sync(0xffffffffu, next, n - 1);
+            length = __shfl_sync(0xffffffffu, its, n - 1);
+            known = true;
+        }
+        const int behind = (n - 1) * step + 1;
+        begin += behind;
+        len = min(step - 1, len - behind);
     }
     const int b = begin - 1;
     if (b < 0) return false;
-    const int64_t c0 = a.cu[b], c1 = a.cu[b + 1], length = a.c.lengths[b];
+    if (!known) {
+        c0 = a.cu[b];
+        c1 = a.cu[b + 1];
+        length = a.c.lengths[b];
+    }
     const int64_t p0 = length - (c1 - c0);   // position of the sequence's first row
     const int64_t block = (p0 >> 4) + (slot - ((c0 >> 4) + 2 * (int64_t)b));
     k->first = block * 16;
@@ -58,13 +78,17 @@ __device__ __forceinline__ bool find_block(const RowArgs& a, int64_t slot, Block
     k->lo = (int)max((int64_t)k->lo, min((int64_t)16, -k->row0));          // the rows that there are, whatever cu holds
     k->hi = (int)min((int64_t)k->hi, max((int64_t)0, a.rows - k->row0));
     if (k->lo >= k->hi) return false;
-    k->page = -1;
     const int64_t column = k->first >> a.page_shift;
-    if (k->first >= 0 && column < a.c.max_pages) {
-        const int p = a.c.page_table[(int64_t)b * a.c.max_pages + column];
-        if (p >= 0 && p < a.c.num_pages) k->page = p;
-    }
+    k->page = k->first >= 0 && column < a.c.max_pages ? a.c.page_table[(int64_t)b * a.c.max_pages + column] : -1;
     return true;
+}
+
+__device__ __forceinline__ bool has_place(const RowArgs& a, const Block& k) { return k.page >= 0 && k.page < a.c.num_pages; }
+
+// Where the block's record of the CTA's first head lies (of page 0, if it has no place).
+template <int D>
+__device__ __forceinline__ int64_t record_at(const RowArgs& a, const Block& k, int64_t head_bytes) {
+    return ((has_place(a, k) ? (int64_t)k.page : 0) * a.c.num_kv_heads + blockIdx.y) * head_bytes + (((int)k.first & (a.c.page_size - 1)) >> 4) * Record8<D>::bytes;
 }
 
 // The least e with amax <= 448 * 2^e (448 = 1.75 * 2^8), within the format's range.
@@ -179,7 +203,7 @@ __device__ __forceinline__ void put_v(uint8_t* to, const float (&x)[2][8], int e
 
 // K of a block: a thread has 16 channels of one row.
 template <typename T, int D, int TURN>
-__device__ __forceinline__ void append_k(const RowArgs& a, const Block& blk, uint8_t* rec, int64_t next_rec, uint32_t (&maxima)[3][D / 32]) {
+__device__ __forceinline__ void append_k(const RowArgs& a, const Block& blk, uint32_t (&maxima)[3][D / 32]) {
     const int t = threadIdx.x, r = t / (D / 16);
     const Chunks ch = chunks_of<TURN>(t & (D / 16 - 1), a.pairs);
     const bool is_new = r >= blk.lo && r < blk.hi;
@@ -221,6 +245,12 @@ __device__ __forceinline__ void append_k(const RowArgs& a, const Block& blk, uin
                 }
         }
     }
+    if (!has_place(a, blk)) {
+        if (t == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
+        return;
+    }
+    const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * Record8<D>::bytes, next_rec = a.lanes * head_bytes;
+    uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) + record_at<D>(a, blk, head_bytes);
     int side = 0;
 #pragma unroll 1
     for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, rec += next_rec, side ^= 1) {
@@ -292,7 +322,7 @@ __device__ __forceinline__ void append_k(const RowArgs& a, const Block& blk, uin
 
 // V of a block: a thread has 8 channels of two rows, every other byte of 16 each.
 template <typename T, int D>
-__device__ __forceinline__ void append_v(const RowArgs& a, const Block& blk, uint8_t* rec, int64_t next_rec, uint32_t (&maxima)[3][D / 32]) {
+__device__ __forceinline__ void append_v(const RowArgs& a, const Block& blk, uint32_t (&maxima)[3][D / 32]) {
     const int t = threadIdx.x - D, chunk = (t >> 2) & (D / 8 - 1), r = t / (D / 2) * 8 + (t & 3) * 2;
     const bool is_new[2] = {r >= blk.lo && r < blk.hi, r + 1 >= blk.lo && r + 1 < blk.hi};
     const T* from = reinterpret_cast<const T*>(a.v) + (blk.row0 + r) * a.v_row + blockIdx.y * a.v_head + 8 * chunk;
@@ -304,8 +334,10 @@ __device__ __forceinline__ void append_v(const RowArgs& a, const Block& blk, uin
         from += a.lanes * a.v_head;
     };
     read(blockIdx.y);
-    rec += Record8<D>::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16;
-    const int to_exponent = Record8<D>::exponents + 4 - (Record8<D>::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16);
+    if (!has_place(a, blk)) return;
+    const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * Record8<D>::bytes, next_rec = a.lanes * head_bytes;
+    const int at = Record8<D>::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16, to_exponent = Record8<D>::exponents + 4 - at;
+    uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) + record_at<D>(a, blk, head_bytes) + at;
     int side = 0;
 #pragma unroll 1
     for (int h = blockIdx.y; h < a.c.num_kv_heads; h += a.lanes, rec += next_rec, side ^= 1) {
@@ -359,15 +391,8 @@ __global__ void __launch_bounds__(2 * D, append_ctas<D>()) append8_kernel(const 
     __shared__ uint32_t maxima[2][3][D / 32];   // of K and V; one head's and the next's in turn, so one barrier a head is enough
     Block blk;
     if (!find_block(a, blockIdx.x, &blk)) return;
-    if (blk.page < 0) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
-        return;
-    }
-    const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * Record8<D>::bytes;
-    uint8_t* rec = reinterpret_cast<uint8_t*>(a.c.pages) + (blk.page * a.c.num_kv_heads + blockIdx.y) * head_bytes +
-                   (((int)blk.first & (a.c.page_size - 1)) >> 4) * Record8<D>::bytes;
-    if (threadIdx.x < D) append_k<T, D, TURN>(a, blk, rec, a.lanes * head_bytes, maxima[0]);
-    else append_v<T, D>(a, blk, rec, a.lanes * head_bytes, maxima[1]);
+    if (threadIdx.x < D) append_k<T, D, TURN>(a, blk, maxima[0]);
+    else append_v<T, D>(a, blk, maxima[1]);
 }
 
 // 8 values to their row, as TO.
@@ -385,7 +410,7 @@ __global__ void __launch_bounds__(2 * D, gather_ctas<D>()) gather8_kernel(const 
     using R = Record8<D>;
     Block blk;
     if (!find_block(a, blockIdx.x, &blk)) return;
-    const bool good = blk.page >= 0, is_k = threadIdx.x < D;
+    const bool good = has_place(a, blk), is_k = threadIdx.x < D;
     if (!good && threadIdx.x == 0 && blockIdx.y == 0) raise_status(a.status, TKV_ECAPACITY);
     // 8 channels of two rows a thread, 8 apart of K and neighbours of V: with 16 channels of one each store writes half of its sectors
     // (22.7 us instead of 18.3 for 18,432 rows of 8 heads of 128 as bf16)
@@ -398,8 +423,7 @@ __global__ void __launch_bounds__(2 * D, gather_ctas<D>()) gather8_kernel(const 
     const int64_t head_bytes = (int64_t)(a.c.page_size >> 4) * R::bytes;
     const int at = is_k ? k_place(r, chunk) : R::v_codes + t / (D / 2) * (8 * D) + chunk * 64 + (t & 3) * 16;
     const int to_exponent = R::exponents + (is_k ? 0 : 4) - at;
-    const uint8_t* from = reinterpret_cast<const uint8_t*>(a.c.pages) + ((good ? blk.page : 0) * a.c.num_kv_heads + blockIdx.y) * head_bytes +
-                          (((int)blk.first & (a.c.page_size - 1)) >> 4) * R::bytes + at;
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(a.c.pages) + record_at<D>(a, blk, head_bytes) + at;
     // V's bytes in turn belong to the two rows: put beside those of their row
     const uint32_t low = is_k ? 0x3210u : 0x6420u, high = is_k ? 0x7654u : 0x7531u;
     uint4 next = {};
