@@ -279,6 +279,9 @@ __device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, const Rows&
 
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718056f; }
 __device__ __forceinline__ float inverse(float l, float gain) { return l == 0.0f ? 0.0f : gain / l; }   // a row that saw nothing is 0
+// The same for 8-bit pages, in a few instructions: 2^-22 of l and of its logarithm, far below the 2^-11 of p.
+__device__ __forceinline__ float inverse8(float l) { return l == 0.0f ? 0.0f : __fdividef(1.0f, l); }
+__device__ __forceinline__ float lse8_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718056f; }
 
 // float4 j of row tile nt, of rows with these m and l, to out (lse with j = 0, lane row 0).
 template <int D, int KIND>
@@ -591,12 +594,12 @@ __device__ __forceinline__ void join_pieces(const PagedAttnArgs& a, Shared<D, NT
                 float* lse;
                 uint16_t* to = out_row(a, rows, 8 * nt + 2 * (lane & 3) + e, &lse);
                 if (!to) continue;
-                const float l = e ? ml.w : ml.y, inv = inverse(l, 1.0f);
+                const float l = e ? ml.w : ml.y, inv = inverse8(l);
                 uint32_t w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = pack16((e ? x[j].y : x[j].x) * inv, (e ? x[j].w : x[j].z) * inv, a.q_fp16);
                 *reinterpret_cast<uint4*>(to + channel_of<D, kE4m3>(lane >> 2, 4 * h, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (lse && h == 0 && lane < 4) *lse = lse_of(e ? ml.z : ml.x, l);
+                if (lse && h == 0 && lane < 4) *lse = lse8_of(e ? ml.z : ml.x, l);
             }
         } else {
             float4* record = a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * SIZE;
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                         float* lse;
                         uint16_t* to = out_row(a, piece.rows, 8 * nt + 2 * (lane & 3) + e, &lse);
                         if (!to) continue;
-                        const float l = e ? ml.w : ml.y, inv = inverse(l, gain);
+                        const float l = e ? ml.w : ml.y, inv = KIND == kE4m3 ? inverse8(l) : inverse(l, gain);
                         uint32_t w[D / 16];
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) w[j] = pack16(sums.o[nt][j][e] * inv, sums.o[nt][j][e + 2] * inv, fp16);
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                                 to[channel_of<D, KIND>(r, j, 2)] = (uint16_t)(w[j] >> 16);
                             }
                         }
-                        if (lse && r == 0) *lse = lse_of(e ? ml.z : ml.x, l);
+                        if (lse && r == 0) *lse = KIND == kE4m3 ? lse8_of(e ? ml.z : ml.x, l) : lse_of(e ? ml.z : ml.x, l);
                     }
                 }
             }

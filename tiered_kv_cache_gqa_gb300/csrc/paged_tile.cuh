@@ -385,18 +385,21 @@ __device__ __forceinline__ bool not_finite(const uint8_t* tile, uint32_t tile_s,
         const uint8_t* rec = tile + g * Record<D>::bytes;
         return odd(v_scale_pair<D>(rec, lane >> 2, lane & 3, 0) & m0) || odd(v_scale_pair<D>(rec, lane >> 2, lane & 3, 1) & m1);
     }
-    bool any = false;
-    if (KIND == kE4m3) {
+    if (KIND == kE4m3) {   // a NaN is a byte 0x7F or 0xFF; the bytes of two positions alternate
         const uint8_t* at = tile + g * Record8<D>::bytes + Record8<D>::v_codes + (lane >> 2) * 64 + (lane & 3) * 16;
-#pragma unroll 1
-        for (int j = 0; j < D / 16; ++j) {
-            uint32_t f[4];
-            const uint8_t* word = at + (j >> 2) * 512 + (j & 3) * 4;
-            v_codes8(f, *reinterpret_cast<const uint32_t*>(word), *reinterpret_cast<const uint32_t*>(word + 8 * D), m0, m1);
-            any |= odd(f[0]) || odd(f[1]) || odd(f[2]) || odd(f[3]);
+        uint32_t found = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t bytes = (keep >> (2 * i) & 1 ? 0x007F007Fu : 0u) | (keep >> (2 * i) & 2 ? 0x7F007F00u : 0u);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                const uint4 x = *reinterpret_cast<const uint4*>(at + i * (8 * D) + h * 512);
+                found |= ((x.x & bytes) + 0x01010101u) | ((x.y & bytes) + 0x01010101u) | ((x.z & bytes) + 0x01010101u) | ((x.w & bytes) + 0x01010101u);
+            }
         }
-        return any;
+        return found & 0x80808080u;
     }
+    bool any = false;
 #pragma unroll 1
     for (int j = 0; j < D / 16; ++j) {
         uint32_t f[4];
