@@ -515,32 +515,33 @@ def beam_select(logits, scores, count=None, finished=None, eos=None):
     A candidate's score is scores + log_softmax(logits); where there are fewer than `count`, score -inf, beam -1, token -1.
     The call has no gradient."""
     w, torch = "beam_select", _types()
-    _on(logits, w, "logits", None, 3)
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 3):
+        _on(logits, w, "logits", None, 3)
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
         _refuse(w, "logits is %s: bf16, fp16 or fp32" % logits.dtype)
-    batch, beams, vocab = logits.shape
-    index, device, s = logits.get_device(), logits.device, logits.stride()
+    shape, s, device = logits.shape, logits.stride(), logits.device
+    batch, beams, vocab = shape
+    index = device.index
     count = beams if count is None else int(count)
-    if not 1 <= beams <= 64 or not 1 <= count <= 64 or vocab < 1 or beams * vocab > 0x7FFFFF00 or batch * beams > 0x7FFFFFFF // 64:
-        _refuse(w, "%s logits, count %d: beams and count are 1 to 64, beams * vocab is below 2^31 - 256" % (list(logits.shape), count))
-    if vocab > 1 and s[2] != 1:
+    if not (1 <= beams <= 64 and 1 <= count <= 64 and vocab >= 1 and beams * vocab <= 0x7FFFFF00 and batch * beams <= 0x7FFFFFFF // 64):
+        _refuse(w, "%s logits, count %d: beams and count are 1 to 64, beams * vocab is below 2^31 - 256" % (list(shape), count))
+    if s[2] != 1 and vocab > 1:
         _refuse(w, "the vocabulary has to be contiguous")
     if not (isinstance(scores, torch.Tensor) and scores.dtype is torch.float32 and scores.is_cuda and scores.get_device() == index):
         _on(scores, w, "scores", torch.float32, 2, device)
-    if scores.shape != (batch, beams) or not scores.is_contiguous():
+    if scores.shape != shape[:2] or not scores.is_contiguous():
         _refuse(w, "scores is a contiguous [%d, %d]" % (batch, beams))
-    done = None
+    done, last = None, 0
     if finished is not None:
         _on(finished, w, "finished", None, 2, device)
-        if finished.dtype not in (torch.bool, torch.uint8) or finished.shape != (batch, beams) or not finished.is_contiguous():
+        if finished.dtype not in (torch.bool, torch.uint8) or finished.shape != shape[:2] or not finished.is_contiguous():
             _refuse(w, "finished is a contiguous bool or uint8 [%d, %d]" % (batch, beams))
         if eos is None or not 0 <= int(eos) < vocab:
             _refuse(w, "eos is %s: a token of the vocabulary" % eos)
-        done = finished.data_ptr()
-    out = torch.empty((batch, count), dtype=torch.float32, device=device)
-    out_beams = torch.empty((batch, count), dtype=_int32, device=device)
-    tokens = torch.empty((batch, count), dtype=_int32, device=device)
+        done, last = finished.data_ptr(), int(eos)
+    empty, size = torch.empty, (batch, count)
+    out, out_beams, tokens = empty(size, dtype=torch.float32, device=device), empty(size, dtype=_int32, device=device), empty(size, dtype=_int32, device=device)
     if batch:
         key = index, dt, batch, beams, vocab, count
         size = _select_sizes.get(key)
@@ -548,6 +549,6 @@ def beam_select(logits, scores, count=None, finished=None, eos=None):
             with torch.cuda.device(index):
                 size = _select_sizes[key] = load().tkv_beam_select_workspace(dt, batch, beams, vocab, count)
         work = _workspace(size, index, device)
-        _call(load().tkv_beam_select, w, index, logits.data_ptr(), dt, batch, beams, vocab, s[0], s[1], scores.data_ptr(), done,
-              0 if eos is None else int(eos), count, out.data_ptr(), out_beams.data_ptr(), tokens.data_ptr(), work.data_ptr(), work.numel())
+        _call(load().tkv_beam_select, w, index, logits.data_ptr(), dt, batch, beams, vocab, s[0], s[1], scores.data_ptr(), done, last, count,
+              out.data_ptr(), out_beams.data_ptr(), tokens.data_ptr(), work.data_ptr(), work.numel())
     return out, out_beams, tokens
