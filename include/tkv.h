@@ -554,8 +554,9 @@ int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_head
  * finished (device uint8 [batch][beams], or NULL): a beam where it is not 0 offers
  * one candidate, token eos with the beam's own score; its logits are not read.
  * A beam with a score that is not finite, or with a NaN or +infinity among its logits, offers
- * none, and no candidate has a total of -infinity.  Places that are left over get
- * score -infinity, beam -1 and token -1.
+ * none, and no candidate has a logit of -infinity or a total below the lowest fp32 number.
+ * Places that are left over get score -infinity, beam -1 and token -1.  Totals are sums of two fp32
+ * numbers; a row's log of its sum is good to about 2^-20, and the same for equal rows.
  * logits: device [batch][beams][vocab] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, the
  * vocabulary contiguous, strides in elements (any alignment); scores: device fp32
  * [batch][beams]; out_scores, out_beams, out_tokens: device [batch][count].
@@ -575,7 +576,7 @@ int64_t tkv_beam_select_workspace(int32_t dtype, int64_t batch, int32_t beams, i
 /* The caches of a model's layers follow the chosen beams: sequence g * beams + w goes on
  * from sequence g * beams + parents[g * beams + w].
  * caches: host array of num_caches descriptors that share page_table, lengths, batch,
- * max_pages and page_size; pages, types, heads and head_dim may differ.  parents:
+ * max_pages and page_size; types, heads and head_dim may differ, and no two have the same pages.  parents:
  * device int32 [batch]; a negative one means that the sequence keeps what it has.
  * The columns of the page table before a sequence's current page (lengths / page_size) become
  * its parent's, so beams share pages that are full; what the current, partly filled

@@ -316,7 +316,7 @@ def test_reordering_captured_behind_a_selection():
 def test_reordering_refuses():
     b = Beams(2, 2, 20, 16, ("e4m3", "bf16"))
     other = Beams(2, 2, 20, 16, ("e4m3",))
-    for call in (lambda: tkv.PagedLayers([]), lambda: tkv.PagedLayers(b.caches + other.caches), lambda: tkv.PagedLayers([b.caches[0], None]),
+    for call in (lambda: tkv.PagedLayers([]), lambda: tkv.PagedLayers(b.caches + other.caches), lambda: tkv.PagedLayers([b.caches[0], None]), lambda: tkv.PagedLayers([b.caches[0], b.caches[1], b.caches[0]]),
                  lambda: b.layers.reorder(ints([0, 1, 0, 1])), lambda: b.layers.reorder(ints([[0, 1]])), lambda: b.layers.reorder(ints([[0, 1, 0, 1]]).long()),
                  lambda: b.layers.reorder(ints([[0, 1], [0, 1]]).t()), lambda: b.layers.reorder(ints([[0, 1], [0, 1]]).cpu()), lambda: b.layers.reorder(None),
                  lambda: b.layers.reorder(ints([[0, 1], [0, 1]]), status=torch.zeros(1, device="cuda"))):

@@ -466,7 +466,7 @@ class PagedCache:
 
 
 class PagedLayers:
-    """The caches of a model's layers, which share a page table and lengths; keeps them alive.
+    """The caches of a model's layers, which share a page table and lengths, each with pages of its own; keeps them alive.
 
     Sequences come in groups of beams: sequence g * beams + w is beam w of group g."""
 
@@ -483,6 +483,8 @@ class PagedLayers:
                 _refuse(w, "the caches have to share one lengths")
             if (c.batch, c.max_pages, c.page_size, c._index) != (first.batch, first.max_pages, first.page_size, first._index):
                 _refuse(w, "the caches differ in batch, pages a sequence, page size or device")
+        if first.pages.numel() and len({c.pages.data_ptr() for c in caches}) != len(caches):
+            _refuse(w, "two caches have the same pages")
         self.caches, self.batch, self.device, self._index = caches, first.batch, first.device, first._index
         self._c = (PagedDesc * len(caches))(*(c._c for c in caches))
 
