@@ -36,7 +36,7 @@ constexpr int kCells = 16;                        // of a thread
 constexpr int kIndexBits = 12;                    // of a candidate's index in the joining kernel
 constexpr int kMostCandidates = 1 << kIndexBits;  // of a sequence
 constexpr int kMostGroups = kThreads;
-constexpr int kFew = 128;                         // candidates of a sequence that are sorted whole
+constexpr int kFew = 64;                          // candidates of a sequence that are sorted whole
 constexpr float kLog2E = 1.44269504f;
 constexpr float kFar = 3e38f;
 constexpr float kFloor = -3.402823466e38f;        // a maximum before anything is seen
@@ -638,7 +638,9 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
 
 // How the rows are cut: as many CTAs as the device holds at once, chunks of 512 pieces at least, and no more candidates than the
 // joining kernel takes.  With c chunks a row, a chunk's stream takes about 0.4 ns for each of its pieces / c pieces and joining 3 ns for
-// each of beams count c candidates: the sum is least at c = sqrt(pieces / (8 beams count)).  One sequence of 8 beams of 131,072, 16 of
+// each of beams count c candidates: the sum is least at c = sqrt(pieces / (8 beams count)).  Up to a candidate a thread joining costs the
+// same, so with no more than two CTAs an SM there are as many chunks as that allows (4 beams of 32,000, 8 chosen: 7.5 us with 8 chunks, 8.2
+// with the 4 of the root).  One sequence of 8 beams of 131,072, 16 of
 // them chosen: 11.2 us with 4 chunks, 18.8 with the most, 32; 2 x 5 beams of 100,003 in fp32, 10 chosen: 12.7 and 15.9.
 struct Split {
     int chunks, per_chunk;   // pieces of a chunk
@@ -648,7 +650,8 @@ Split split_rows(int64_t rows, int beams, int vocab, int count, int element, int
     int64_t chunks = std::max<int64_t>(1, (int64_t)sms * kCtas / rows);
     chunks = std::min<int64_t>(chunks, (pieces + 2 * kThreads - 1) / (2 * kThreads));
     chunks = std::min<int64_t>(chunks, std::max(1, kMostCandidates / (beams * count)));
-    chunks = std::min<int64_t>(chunks, std::max<int64_t>(1, std::llrint(std::sqrt(pieces / (8.0 * beams * count)))));
+    const int64_t balanced = std::llrint(std::sqrt(pieces / (8.0 * beams * count))), cheap = std::min<int64_t>(kThreads / (beams * count), 2 * sms / rows);
+    chunks = std::min(chunks, std::max<int64_t>({1, balanced, cheap}));
     Split s;
     s.per_chunk = (int)((pieces + chunks - 1) / chunks);
     s.chunks = (pieces + s.per_chunk - 1) / s.per_chunk;
