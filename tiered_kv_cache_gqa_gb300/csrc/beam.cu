@@ -194,19 +194,20 @@ __device__ __forceinline__ float value_at(uint4 u, int bit) {
 template <typename T>
 __device__ __forceinline__ int place_of(int bit) { return sizeof(T) == 4 ? bit : 2 * (bit & 3) + (bit >> 4); }
 
-// The block's reference and sum, to every thread.  `stats` is written again behind a barrier.
-__device__ __forceinline__ Stat join_stats(Stat a, Stat b) {
-    const float top = fmaxf(a.m, b.m);
-    return Stat{top, a.sum * exp2_fast((a.m - top) * kLog2E) + b.sum * exp2_fast((b.m - top) * kLog2E)};
+// A warp's part of the block's reference and sum, and, behind a barrier, all of it, to every thread.
+__device__ __forceinline__ void sum_warp(float m, float sum, Stat (&stats)[kWarps]) {
+    const float top = of_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+    sum *= exp2_fast((m - top) * kLog2E);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) stats[threadIdx.x >> 5] = Stat{top, sum};
 }
-__device__ __forceinline__ Stat sum_block(Stat t, Stat (&stats)[kWarps]) {
+__device__ __forceinline__ Stat sum_block(const Stat (&stats)[kWarps]) {
+    Stat t{kFloor, 0.0f};
 #pragma unroll
-    for (int o = 16; o; o >>= 1) t = join_stats(t, Stat{__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.sum, o)});
-    if ((threadIdx.x & 31) == 0) stats[threadIdx.x >> 5] = t;
-    __syncthreads();
-    t = stats[0];
+    for (int i = 0; i < kWarps; ++i) t.m = fmaxf(t.m, stats[i].m);
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) t = join_stats(t, stats[i]);
+    for (int i = 0; i < kWarps; ++i) t.sum += stats[i].sum * exp2_fast((stats[i].m - t.m) * kLog2E);
     return t;
 }
 
@@ -214,10 +215,13 @@ constexpr int kMost = kGroupThreads * 32 + kMaxCount;   // values in a list: wha
 
 // The best so far: a list that the CTA adds to and sorts.
 struct Best {
-    uint64_t keys[kMost], list[kMaxCount];
+    __align__(16) uint64_t keys[kMost];
     __align__(16) uint64_t maxima[kMostGroups];
-    uint64_t bound;
+    uint64_t list[kMaxCount], bound;
     int found;
+    // of cells: how many come into question, how many hold the best, and the least of those cells' maxima, ordered
+    int asked, placed;
+    uint32_t lowest;
 };
 
 // What a thread knows of it.
@@ -331,7 +335,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
     if (is_out(a, row)) return;
-    if (tid == 0) best.found = 0;
+    if (tid == 0) {
+        best.found = best.asked = best.placed = 0;
+        best.lowest = 0xFFFFFFFFu;
+        best.bound = 0;
+    }
     const int tiles = (end - first + kTile - 1) / kTile, span = (tiles + kCells - 1) / kCells;   // tiles of a cell
     float cell = -INFINITY;
     int in_cell = 0, cell_at = tid;
@@ -376,76 +384,73 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         sum += both.x + both.y;
     }
     if (in_cell) (&cells[0][0])[cell_at] = cell;
+    // ---- the chunk's reference and sum
+    if (fabsf(c) < kFar) sum *= exp2_fast(-fmaf(m, kLog2E, -c));   // from c to m
+    sum_warp(m, sum, stats);
     // ---- the best
     Bound b{-INFINITY, 0, 0};
-    __syncthreads();
     bool by_tiles = false;
     if (tiles == 1) {
         look_over<T>(best, raw, first, a.count, b);
     } else {
-        // A bound from below: `count` groups of threads at least have a value that reaches it.  Then the cells that do.
-        const int used = (tiles + span - 1) / span, group = group_shift(a.count);
-        const bool has = m > kFloor;
-        float low = -INFINITY;
-        if (groups_with(has, group) > a.count) {
-            kth_largest(has ? (uint64_t)ordered(m) << 32 | (uint32_t)~tid : 0, a.count, group, best.maxima, &best.bound);
-            __syncthreads();
-            low = of_ordered((uint32_t)(best.bound >> 32));
-        }
+        // A bound from below: `count` groups of threads have a value that reaches it.  Then the cells that do.
+        const int used = (tiles + span - 1) / span;
+        kth_largest(m > kFloor ? (uint64_t)ordered(m) << 32 | (uint32_t)~tid : 0, a.count, group_shift(a.count), best.maxima, &best.bound);
+        __syncthreads();
+        const float low = best.bound ? of_ordered((uint32_t)(best.bound >> 32)) : -INFINITY;   // 0: fewer groups have any
+        uint32_t* asked = reinterpret_cast<uint32_t*>(best.keys);   // maxima of cells, ordered, and
+        uint32_t* cell_of = asked + kMost;                          // the cells
         if (m >= low)
             for (int i = 0; i < used; ++i) {
                 const float x = cells[i][tid];
-                if (x >= low && x > -INFINITY) add_key(best, (uint64_t)ordered(x) << 32 | (uint32_t)(i * kThreads + tid));
+                if (x >= low && x > -INFINITY) {
+                    const int slot = atomicAdd(&best.asked, 1);
+                    if (slot < kMost) {
+                        asked[slot] = ordered(x);
+                        cell_of[slot] = i * kThreads + tid;
+                    }
+                }
             }
         __syncthreads();
-        int n = best.found;
+        const int n = best.asked;
         by_tiles = n > kMost;
         if (!by_tiles) {
-            if (n >= a.count) {
-                sort_best(best.keys, n, a.count, best.list);
-                __syncthreads();
-                b.lowest = of_ordered((uint32_t)(best.list[a.count - 1] >> 32));   // the count-th largest cell's
-            }
-            // The cells that reach it move to the front: keys, of which no two are equal, become places in that order.
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t k = best.keys[i];
-                if (of_ordered((uint32_t)(k >> 32)) < b.lowest) best.keys[i] = 0;
-            }
-            __syncthreads();
-            if (tid == 0) best.found = 0;
-            uint32_t mine[kMost / kThreads + 1];
-#pragma unroll
-            for (int i = 0; i <= kMost / kThreads; ++i) mine[i] = i * kThreads + tid < n && best.keys[i * kThreads + tid] ? (uint32_t)best.keys[i * kThreads + tid] : 0xFFFFFFFFu;
-            __syncthreads();
-            int* places = reinterpret_cast<int*>(best.maxima);   // of cells: no more are looked into
+            // Those that fewer than `count` others exceed hold the best.
+            int* places = reinterpret_cast<int*>(best.maxima);
             constexpr int kPlaces = sizeof(best.maxima) / sizeof(int);
-#pragma unroll
-            for (int i = 0; i <= kMost / kThreads; ++i)
-                if (mine[i] != 0xFFFFFFFFu) {
-                    const int slot = atomicAdd(&best.found, 1);
-                    if (slot < kPlaces) places[slot] = (int)mine[i];
+            for (int i = tid; i < n; i += kThreads) {
+                const uint32_t x = asked[i];
+                int above = 0, j = 0;
+#pragma unroll 4
+                for (; j + 4 <= n; j += 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(asked + j);
+                    above += (u.x > x) + (u.y > x) + (u.z > x) + (u.w > x);
                 }
+                for (; j < n; ++j) above += asked[j] > x;
+                if (above < a.count) {
+                    const int slot = atomicAdd(&best.placed, 1);
+                    if (slot < kPlaces) places[slot] = (int)cell_of[i];
+                    atomicMin(&best.lowest, x);
+                }
+            }
             __syncthreads();
-            n = best.found;
-            by_tiles = n > kPlaces;
-            __syncthreads();
-            if (tid == 0) best.found = 0;
-            __syncthreads();
+            const int placed = best.placed;
+            by_tiles = placed > kPlaces;
             if (!by_tiles) {
-                for (int i = tid; i < n * span * kVectors; i += kThreads) {
-                    const int cell_of = places[i / (span * kVectors)], in = i % (span * kVectors);
-                    const int q = first + (cell_of / kThreads * span + in / kVectors) * kTile + in % kVectors * kThreads + cell_of % kThreads;
+                if (n >= a.count) b.lowest = of_ordered(best.lowest);   // the count-th largest cell's
+                for (int i = tid; i < placed * span * kVectors; i += kThreads) {
+                    const int cell_at = places[i / (span * kVectors)], in = i % (span * kVectors);
+                    const int q = first + (cell_at / kThreads * span + in / kVectors) * kTile + in % kVectors * kThreads + cell_at % kThreads;
                     add_piece<T>(best, load(q), q * E, b);
                 }
                 __syncthreads();
-                n = best.found;
-                by_tiles = n > kMost;
+                const int found = best.found;
+                by_tiles = found > kMost;
                 if (!by_tiles) {
-                    sort_best(best.keys, n, a.count, best.list);
-                    b.held = min(n, a.count);
+                    sort_best(best.keys, found, a.count, best.list);
+                    b.held = min(found, a.count);
                 }
             }
-            __syncthreads();
         }
         if (by_tiles) {
             __syncthreads();   // everyone has read it
@@ -459,10 +464,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
             }
         }
     }
-    // ---- the chunk's reference and sum
-    if (fabsf(c) < kFar) sum *= exp2_fast(-fmaf(m, kLog2E, -c));   // from c to m
+    __syncthreads();
     const int64_t at = (int64_t)row * a.chunks + blockIdx.x;
-    Stat t = sum_block(Stat{m, sum}, stats);
+    Stat t = sum_block(stats);
     if (b.held && !(t.sum > 0.0f && t.sum < INFINITY)) {   // the largest beyond 2e38 either way, or a NaN or an infinity: the slow way
         m = of_ordered((uint32_t)(best.list[0] >> 32));
         sum = 0.0f;
@@ -474,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
             }
         }
         __syncthreads();
-        t = sum_block(Stat{m, sum}, stats);
+        sum_warp(m, sum, stats);
+        __syncthreads();
+        t = sum_block(stats);
     }
     if (tid == 0) a.stats[at] = t;
     if (tid < a.count) {
@@ -531,6 +537,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     Candidate early[kEarly];
 #pragma unroll
     for (int k = 0; k < kEarly; ++k) early[k] = tid + k * kThreads < n ? best[tid + k * kThreads] : Candidate{0.0f, -1};
+    const int lanes = a.chunks > 16 ? 16 : a.chunks > 8 ? 8 : a.chunks > 4 ? 4 : a.chunks > 1 ? 2 : 0;   // lane 0 has the sum of twice as many
     for (int w = tid >> 5; w < a.beams; w += kWarps) {            // a warp a beam
         const int row = b * a.beams + w;
         const float score = score_of[w];
@@ -542,12 +549,10 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
             } else {
                 const Stat* s = a.stats + (int64_t)row * a.chunks;
                 for (int i = lane; i < a.chunks; i += 32) top = fmaxf(top, s[i].m);
-#pragma unroll
-                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = of_ordered(__reduce_max_sync(0xffffffffu, ordered(top)));
                 Wide sum{0.0f, 0.0f};
                 for (int i = lane; i < a.chunks; i += 32) sum = plus(sum, Wide{s[i].sum * exp2_fast((s[i].m - top) * kLog2E), 0.0f});
-#pragma unroll
-                for (int d = 16; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+                for (int d = lanes; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
                 if (sum.hi > 0.0f && sum.hi < INFINITY) {   // not: a NaN or an infinity among the logits, or nothing above -infinity
                     const Wide l = plus(log_of(sum.hi), Wide{__fdividef(sum.lo, sum.hi), 0.0f});
                     o = plus(Wide{score, 0.0f}, Wide{-l.hi, -l.lo});
@@ -597,10 +602,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
         }
     }
     // few candidates are sorted as they are
-    if (n > kFew) {
-        const int shift = group_shift(a.count);
-        if (groups_with(mine != 0, shift) > a.count) kth_largest(mine, a.count, shift, maxima, &bound);
-    }
+    if (n > kFew) kth_largest(mine, a.count, group_shift(a.count), maxima, &bound);
     __syncthreads();
     const uint64_t least = bound;
     auto add = [&](int i, Candidate c) {
