@@ -100,6 +100,16 @@ def test_strides_alignments_and_broadcast(dtype):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_long_rows_that_begin_anywhere(dtype):
+    """Chunks of several tiles of rows of every alignment; the same bits where all rows begin on 16 bytes."""
+    x, s = logits((20, 8, 70009), dtype, 6)[..., 3:70004], scores_of(20, 8)
+    first = check(x, s, 4)
+    straight = torch.empty(20, 8, 70016, device="cuda", dtype=dtype)[..., :70001]
+    straight.copy_(x)
+    assert all(torch.equal(a, b) for a, b in zip(first, tkv.beam_select(straight, s, count=4)))
+
+
 def test_finished_beams_and_beams_that_are_out():
     x, s = logits((4, 6, 5000), BF16, 7), scores_of(4, 6)
     done = torch.zeros(4, 6, dtype=torch.bool, device="cuda")

@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     uint4 raw[kVectors], next[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) next[i] = load(first + i * kThreads + tid);
+    bool apart = false;   // next holds memory's pieces, of a row that does not begin on 16 bytes: put together when they are there
     if (is_out(a, row)) return;
     if (tid == 0) {
         best.found = best.asked = best.placed = 0;
@@ -347,7 +348,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     for (int p = first; p < end; p += kTile) {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) raw[i] = next[i];
-        if (!shift && p + 2 * kTile <= min(end, whole)) {
+        if (apart) {
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) {
+                uint4 v = make_uint4(__shfl_down_sync(0xffffffffu, raw[i].x, 1), __shfl_down_sync(0xffffffffu, raw[i].y, 1),
+                                     __shfl_down_sync(0xffffffffu, raw[i].z, 1), __shfl_down_sync(0xffffffffu, raw[i].w, 1));
+                if ((tid & 31) == 31) v = memory[p + i * kThreads + tid + 1];
+                raw[i] = shifted<T>(raw[i], v, shift);
+            }
+        }
+        apart = shift && p + 2 * kTile <= min(end, whole);
+        if (p + 2 * kTile <= min(end, whole)) {
 #pragma unroll
             for (int i = 0; i < kVectors; ++i) next[i] = memory[p + kTile + i * kThreads + tid];
         } else {
