@@ -549,7 +549,7 @@ int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_head
 /* Beam search: the best continuations of each sequence's beams.
  *   total[b][w][v] = scores[b][w] + logits[b][w][v] - log sum_v exp(logits[b][w][v])
  * and the outputs are the `count` largest over (w, v), in descending order, ties to the
- * lowest w * vocab + v: the total (rounded from 64 bits), the beam w and the token v.
+ * lowest w * vocab + v: the total, the beam w and the token v.
  * Within a beam the order is that of the logits.
  * finished (device uint8 [batch][beams], or NULL): a beam where it is not 0 offers
  * one candidate, token eos with the beam's own score; its logits are not read.

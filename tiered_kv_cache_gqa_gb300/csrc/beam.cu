@@ -663,7 +663,8 @@ Split split_rows(int64_t rows, int beams, int vocab, int count, int element, int
     int64_t chunks = std::max<int64_t>(1, (int64_t)sms * kCtas / rows);
     chunks = std::min<int64_t>(chunks, (pieces + 2 * kThreads - 1) / (2 * kThreads));
     chunks = std::min<int64_t>(chunks, std::max(1, kMostCandidates / (beams * count)));
-    const int64_t balanced = std::llrint(std::sqrt(pieces / (8.0 * beams * count))), cheap = std::min<int64_t>(kThreads / (beams * count), 2 * sms / rows);
+    const int64_t balanced = std::llrint(std::sqrt(pieces / (8.0 * beams * count)));
+    const int64_t cheap = std::min<int64_t>(kThreads / (beams * count), 2 * sms / rows);
     chunks = std::min(chunks, std::max<int64_t>({1, balanced, cheap}));
     Split s;
     s.per_chunk = (int)((pieces + chunks - 1) / chunks);
@@ -786,10 +787,10 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         return;
     }
     const int pieces = (rest + c.per - 1) / c.per * (c.unit / 16);       // of a part
-    const int total = pieces * c.parts * c.heads;
+    const uint32_t total = pieces * c.parts * c.heads;                   // below 2^31: i + step fits
     const int64_t part_bytes = c.head_bytes / c.parts, page_bytes = c.head_bytes * c.heads;
-    for (int i = at; i < total; i += step) {
-        const int q = i / pieces;                                        // head and part
+    for (uint32_t i = at; i < total; i += step) {
+        const uint32_t q = i / (uint32_t)pieces;                         // head and part
         uint8_t* to = c.pages + q * part_bytes + (int64_t)(i - q * pieces) * 16;
         uint4 v[W];
 #pragma unroll

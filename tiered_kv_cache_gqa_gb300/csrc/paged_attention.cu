@@ -215,7 +215,9 @@ template <int D, int NT, int KIND>
 struct Config {
     static constexpr int R = 8 * NT;
     static constexpr int ctas = (in_records(KIND) && NT == 1) ? 2 : 1;
-    static constexpr int stages = KIND == kE4m3 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : KIND == kInt4 ? (D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : (NT == 1 ? 5 : 10)) : (D == 128 ? 3 : 6);
+    static constexpr int stages = KIND == kE4m3 || (KIND == kInt4 && D == 128) ? (NT == 1 ? 3 : NT == 2 ? 6 : 5)
+                                  : KIND == kInt4                             ? (NT == 1 ? 5 : 10)
+                                                                              : (D == 128 ? 3 : 6);
     static constexpr int queue = stages <= 6 ? 8 : 16;   // pieces: the one computed, one a stage, one not yet copied
     static constexpr int warp_ring = stages * TileOf<D, KIND>::bytes;
     static constexpr int at_once = NT == 4 ? 1 : TileOf<D, KIND>::groups;   // groups of positions, by the registers
@@ -263,7 +265,11 @@ struct Rec4 {
 
 // The channels of component c of float4 j: row 2 cq + (c & 1).
 template <int D, int KIND>
-__device__ __forceinline__ int channel_of(int r, int j, int c) { return KIND == kE4m3 ? 8 * (r + 8 * (j >> 2)) + 2 * (j & 3) + (c >> 1) : KIND == kInt4 ? (D / 8) * r + 2 * j + (c >> 1) : 16 * j + r + 8 * (c >> 1); }
+__device__ __forceinline__ int channel_of(int r, int j, int c) {
+    return KIND == kE4m3   ? 8 * (r + 8 * (j >> 2)) + 2 * (j & 3) + (c >> 1)
+           : KIND == kInt4 ? (D / 8) * r + 2 * j + (c >> 1)
+                           : 16 * j + r + 8 * (c >> 1);
+}
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {
     return fp16 ? half2_bits(__floats2half2_rn(a, b)) : bf162_bits(__floats2bfloat162_rn(a, b));
@@ -1052,7 +1058,10 @@ cudaError_t launch_kind(PagedAttnArgs& a, int sms, int dev, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_rows(PagedAttnArgs& a, int nt, int sms, int dev, cudaStream_t st) {
-    return nt == 1 ? launch_kind<D, 1>(a, sms, dev, st) : nt == 2 ? launch_kind<D, 2>(a, sms, dev, st) : a.c.kv_type == TKV_E4M3 ? launch<D, 4, kE4m3>(a, sms, dev, st) : launch<D, 4, kInt4>(a, sms, dev, st);
+    return nt == 1                      ? launch_kind<D, 1>(a, sms, dev, st)
+           : nt == 2                    ? launch_kind<D, 2>(a, sms, dev, st)
+           : a.c.kv_type == TKV_E4M3    ? launch<D, 4, kE4m3>(a, sms, dev, st)
+                                        : launch<D, 4, kInt4>(a, sms, dev, st);
 }
 
 bool attention_shape_ok(const tkv_paged* c, int32_t hq, int32_t max_new) {
@@ -1121,7 +1130,8 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     const int nt = rows_of_32(a, max_new, sight, sms) ? 4 : row_tiles(a.group, max_new);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
     a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && has_records(cache->kv_type));
-    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (cache->kv_type == TKV_INT4 || (cache->kv_type == TKV_E4M3 && cache->head_dim == 64) ? 32 : 16) + 1);
+    const bool two_groups = cache->kv_type == TKV_INT4 || (cache->kv_type == TKV_E4M3 && cache->head_dim == 64);   // 32 positions a tile
+    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (two_groups ? 32 : 16) + 1);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
     e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
     if (e != cudaSuccess) {

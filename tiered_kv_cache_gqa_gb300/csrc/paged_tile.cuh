@@ -19,7 +19,8 @@
 // a row's largest channel (q is scaled by a power of two into fp16's range).
 // 8 bits: E4M3 codes are fp16 numbers by one conversion a pair.  A block's exponents stay out of the products: z = S scale log2 e 2^e_k
 // + e_v and p = 2^(z - m), which is the weight times V's scale, so O^T += V^T P^T adds up blocks of different scales; l += p 2^-e_v.
-// With e_v in -32 .. 31 what p loses below 2^-126 is below 2^-60 of the largest weight.
+// With e_v in -32 .. 31 what p loses below 2^-126 is below 2^-60 of the largest weight, and what it loses in fp16 is, times its
+// code, below 2^-29 of the largest weight times V's scale.
 // The channels that a lane holds of a position are those of its own bytes: K's products sum over all channels, so q is
 // laid out to match; for V the lanes' channels are rows of O^T.
 #pragma once
