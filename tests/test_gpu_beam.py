@@ -293,6 +293,20 @@ def test_reordering_that_makes_no_sense_is_reported():
     b.check([[1, 0, 1], [1, 0, 1], [2, 2, 2]], tkv.TKV_ECAPACITY)                # pages that there are not
 
 
+def test_reordering_of_caches_with_fewer_pages():
+    """A beam whose page one cache does not have stays there, and follows in the others."""
+    b = Beams(2, 5, 41, 16, ("bf16", "bf16", "e4m3", "fp16"))
+    for i, left in ((1, b.num_pages - 7), (2, b.num_pages - 4)):
+        b.pages[i], b.np_pages[i] = b.pages[i][:left], b.np_pages[i][:left]
+    b.caches = [tkv.PagedCache(t, b.table, b.lens) for t in b.pages]
+    b.layers = tkv.PagedLayers(b.caches)
+    assert (b.pt[:, 2] >= b.num_pages - 7).any()
+    parents = np.array([[1, 2, 3, 4, 0], [4, 0, 0, 1, 1]])
+    moved = np.concatenate([np.stack([b.pt[5 * g:5 * g + 5, 2], b.pt[5 * g + parents[g], 2]], 1) for g in range(2)])
+    b.check(parents, tkv.TKV_ECAPACITY if (moved >= b.num_pages - 7).any() else 0)
+    b.check([[0, 0, 0, 0, 0], [3, 3, 3, 3, 3]], tkv.TKV_ECAPACITY)
+
+
 def test_reordering_captured_behind_a_selection():
     """Selection, reordering and the next tokens' append in one graph: each replay reads what the last one left."""
     a, b = (Beams(2, 4, 40, 16, ("e4m3", "bf16"), seed=3) for _ in range(2))

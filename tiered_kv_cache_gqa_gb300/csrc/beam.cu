@@ -19,6 +19,7 @@
 // What bounds it is memory, then issue: a 16-bit value costs three and a half instructions (half of a maximum, one to unpack, half a
 // fused multiply-add, an exponential, half a sum).
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -689,46 +690,46 @@ cudaError_t device_sms(int* sms) {
 // The beams of a sequence go on from one another's caches: columns of the page table before the current page are exchanged, and
 // what the current, partly filled page holds is copied.  All beams of a thread's piece are read before any is written, so
 // a permutation needs no second buffer.  Pages before the current one are only read from then on, so that beams may share them.
-// A CTA serves one cache and one sequence of beams: it reads the sequence's parents, lengths and pages once (three trips to memory
-// in a row) and walks over 16-byte pieces.
-constexpr int kMaxCaches = 128;   // of a launch: 5 KB of arguments
-
-struct CacheRef {
-    uint8_t* pages;
-    int64_t num_pages;
-    int64_t head_bytes;      // of a page
-    int32_t heads;
-    int32_t parts;           // of a head's page that hold positions: 1 (records), or K and V
-    int32_t unit;            // bytes of a part's `per` positions
-    int32_t per;
-};
+// The current page is the same in all caches, so a CTA serves one sequence of beams in all caches of a launch, which have one shape: it
+// reads the sequence's parents, lengths and pages once (three trips to memory in a row) and walks over 16-byte pieces, those of one cache
+// behind those of the last.  With CTAs of one cache each, 7 layers of 8 x 12 beams took 36.2 us instead of 15.8, and 32 layers of two
+// positions in pages of 128 22 instead of 5.3.
+constexpr int kMaxCaches = 128;   // of a launch: 2 KB of arguments
 
 struct ReorderArgs {
-    CacheRef cache[kMaxCaches];
+    uint8_t* pages[kMaxCaches];
+    int64_t num_pages[kMaxCaches];
     int32_t* table;
     const int32_t* lengths;
     const int32_t* parents;
     int32_t* status;
-    int64_t groups;
+    int64_t groups, least_pages;   // sequences of beams; the least of num_pages
+    int64_t head_bytes;            // of a page
     int num_caches, beams, max_pages, page_shift;
-    int split, table_split;   // CTAs of a cache and sequence; of a sequence's table (0: the table stays)
+    int heads;
+    int parts;                     // of a head's page that hold positions: 1 (records), or K and V
+    int unit;                      // bytes of a part's `per` positions
+    int per;
+    int split, table_split;        // CTAs of a sequence; of its table (0: the table stays)
 };
 
+// CTAs of an SM, by the registers of a piece of W beams.
 template <int W>
-__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
-    __shared__ int page[W], length;
+constexpr int reorder_ctas() { return W <= 4 ? 8 : W <= 8 ? 4 : W == 16 ? 2 : 1; }
+
+template <int W>
+__global__ void __launch_bounds__(kThreads, reorder_ctas<W>()) reorder_kernel(const __grid_constant__ ReorderArgs a) {
+    __shared__ int page[W], length, last_page;
     __shared__ uint32_t children[W];   // beams that go on from this one, itself not among them
     let_next_start();
     wait_for_previous();
     const int tid = threadIdx.x;
     int64_t unit = blockIdx.x;
-    const int64_t copies = a.groups * a.num_caches * a.split;
+    const int64_t copies = a.groups * a.split;
     const bool is_table = unit >= copies;
     if (is_table) unit -= copies;
     const int parts_of = is_table ? a.table_split : a.split, part = (int)(unit % parts_of);
-    unit /= parts_of;
-    const int64_t group = unit % a.groups;
-    const CacheRef& c = a.cache[is_table ? 0 : (int)(unit / a.groups)];
+    const int64_t group = unit / parts_of;
     if (tid < 32) {   // a lane a beam
         const int64_t seq = group * a.beams + tid;
         const bool is_beam = tid < a.beams;
@@ -745,22 +746,19 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         }
         if (p < 0) p = tid;   // none: it stays
         const int from = __shfl_sync(0xffffffffu, pg, p);
-        bool goes = is_beam && p != tid && same && fits;
-        if (goes && !is_table) {
-            goes = from != pg;
-            if (rest && ((uint32_t)from >= c.num_pages || (uint32_t)pg >= c.num_pages)) {
-                report = max(report, (int)TKV_ECAPACITY);
-                goes = false;
-            }
-        }
+        const bool goes = is_beam && p != tid && same && fits && (is_table || (rest && from != pg));
         if (report != TKV_OK && part == 0) raise_status(a.status, report);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const uint32_t of = __ballot_sync(0xffffffffu, goes && p == i);
             if (tid == i) children[i] = of;
         }
+        const uint32_t last = __reduce_max_sync(0xffffffffu, goes ? max((uint32_t)from, (uint32_t)pg) : 0u);
         if (tid < W) page[tid] = pg;
-        if (tid == 0) length = len;
+        if (tid == 0) {
+            length = len;
+            last_page = (int)last;
+        }
     }
     __syncthreads();
     const int len = length, column = len >> a.page_shift, rest = len & ((1 << a.page_shift) - 1);
@@ -772,7 +770,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         any |= kids[p] != 0;
     }
     if (!any) return;
-    const int at = part * kThreads + tid, step = parts_of * kThreads;
+    const uint32_t at = part * kThreads + tid, step = parts_of * kThreads;
     if (is_table) {
         int32_t* table = a.table + group * a.beams * a.max_pages;
         for (int i = at; i < column; i += step) {
@@ -786,20 +784,39 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         }
         return;
     }
-    const int pieces = (rest + c.per - 1) / c.per * (c.unit / 16);       // of a part
-    const uint32_t total = pieces * c.parts * c.heads;                   // below 2^31: i + step fits
-    const int64_t part_bytes = c.head_bytes / c.parts, page_bytes = c.head_bytes * c.heads;
-    for (uint32_t i = at; i < total; i += step) {
-        const uint32_t q = i / (uint32_t)pieces;                         // head and part
-        uint8_t* to = c.pages + q * part_bytes + (int64_t)(i - q * pieces) * 16;
+    const bool all_there = (uint32_t)last_page < (uint64_t)a.least_pages;
+    if (!all_there && part == 0 && tid == 0) raise_status(a.status, TKV_ECAPACITY);
+    const uint32_t pieces = (rest + a.per - 1) / a.per * (a.unit / 16);   // of a part
+    const uint32_t total = pieces * a.parts * a.heads;                   // of a cache, below 2^31: i + step fits
+    const int64_t part_bytes = a.head_bytes / a.parts, page_bytes = a.head_bytes * a.heads;
+    uint32_t n = at / total, i = at - n * total;                         // cache, piece
+#pragma unroll 1
+    while (n < (uint32_t)a.num_caches) {
+        uint32_t there = ~0u;   // beams whose page there is
+        if (!all_there) {
+            for (int b = 0; b < a.beams; ++b)
+                if ((uint32_t)page[b] >= (uint64_t)a.num_pages[n]) there &= ~(1u << b);
+        }
+        const uint32_t q = i / pieces;                                   // head and part
+        uint8_t* to = a.pages[n] + q * part_bytes + (int64_t)(i - q * pieces) * 16;
         uint4 v[W];
 #pragma unroll
         for (int p = 0; p < W; ++p)
-            if (kids[p]) v[p] = *reinterpret_cast<const uint4*>(to + page[p] * page_bytes);
+            if (kids[p] && there >> p & 1) v[p] = *reinterpret_cast<const uint4*>(to + page[p] * page_bytes);
 #pragma unroll
         for (int p = 0; p < W; ++p)
-            for (uint32_t k = kids[p]; k; k &= k - 1) *reinterpret_cast<uint4*>(to + page[__ffs(k) - 1] * page_bytes) = v[p];
+            if (there >> p & 1)
+                for (uint32_t k = kids[p] & there; k; k &= k - 1) *reinterpret_cast<uint4*>(to + page[__ffs(k) - 1] * page_bytes) = v[p];
+        i += step;
+        const uint32_t further = i / total;
+        n += further;
+        i -= further * total;
     }
+}
+
+// Caches whose pages are moved alike: bf16 and fp16 are.
+bool same_shape(const tkv_paged& a, const tkv_paged& b) {
+    return a.num_kv_heads == b.num_kv_heads && a.head_dim == b.head_dim && (a.kv_type == b.kv_type || !(has_records(a.kv_type) || has_records(b.kv_type)));
 }
 
 }  // namespace
@@ -887,34 +904,44 @@ extern "C" tkv_status tkv_paged_reorder(const tkv_paged* caches, int32_t num_cac
     a.beams = beams;
     a.max_pages = caches[0].max_pages;
     a.page_shift = __builtin_ctz((unsigned)caches[0].page_size);
-    for (int from = 0; from < num_caches && e == cudaSuccess; from += kMaxCaches) {
-        a.num_caches = std::min(num_caches - from, kMaxCaches);
-        int64_t most = 1;
-        for (int i = 0; i < a.num_caches; ++i) {
-            const tkv_paged& c = caches[from + i];
-            CacheRef& r = a.cache[i];
-            const bool records = has_records(c.kv_type);
-            r.pages = reinterpret_cast<uint8_t*>(c.pages);
-            r.num_pages = c.num_pages;
-            r.heads = c.num_kv_heads;
-            r.parts = records ? 1 : 2;
-            r.per = records ? 16 : 1;
-            r.unit = c.kv_type == TKV_INT4 ? 18 * c.head_dim : records ? 32 * c.head_dim + 16 : 2 * c.head_dim;
-            r.head_bytes = (int64_t)(c.page_size / r.per) * r.unit * r.parts;
-            most = std::max(most, r.head_bytes * r.heads / 16);
+    // CTAs of an SM: several rounds, which even out what SMs get of the memory, but a round of CTAs without work costs 1.2 us.  80 layers of 8 x 8
+    // beams of 1,000 positions: 78.2 us with 20, 91.5 with four; 64 x 4 beams 144 with 48, 173 with eight.  32 layers of 8 x 12 beams of two
+    // positions in pages of 128: 5.3 us with four, 4.2 with two, 10.8 with sixteen.
+    const int ctas = beams <= 4 ? 48 : beams <= 8 ? 20 : beams <= 16 ? 4 : 2;
+    a.table_split = std::max(1, std::min((a.max_pages + kThreads - 1) / kThreads, 16));   // of the first launch
+    for (int first = 0; first < num_caches && e == cudaSuccess; ++first) {   // the caches of one shape after those of another
+        const tkv_paged& c = caches[first];
+        int before = 0;
+        while (before < first && !same_shape(caches[before], c)) ++before;
+        if (before < first) continue;
+        const bool records = has_records(c.kv_type);
+        a.heads = c.num_kv_heads;
+        a.parts = records ? 1 : 2;
+        a.per = records ? 16 : 1;
+        a.unit = c.kv_type == TKV_INT4 ? 18 * c.head_dim : records ? 32 * c.head_dim + 16 : 2 * c.head_dim;
+        a.head_bytes = (int64_t)(c.page_size / a.per) * a.unit * a.parts;
+        for (int at = first; at < num_caches && e == cudaSuccess;) {
+            a.num_caches = 0;
+            a.least_pages = LLONG_MAX;
+            for (; at < num_caches && a.num_caches < kMaxCaches; ++at) {
+                if (!same_shape(caches[at], c)) continue;
+                a.pages[a.num_caches] = reinterpret_cast<uint8_t*>(caches[at].pages);
+                a.num_pages[a.num_caches++] = caches[at].num_pages;
+                a.least_pages = std::min<int64_t>(a.least_pages, caches[at].num_pages);
+            }
+            if (a.num_caches == 0) break;
+            // none without a piece
+            const int64_t most = a.head_bytes / 16 * a.heads * a.num_caches;
+            a.split = (int)std::min(std::max<int64_t>(1, (int64_t)sms * ctas / a.groups), (most + kThreads - 1) / kThreads);
+            const int64_t grid = a.groups * (a.split + a.table_split);
+            if (grid > 0x7FFFFFFF) return TKV_EINVAL;
+            cudaStream_t st = (cudaStream_t)stream;
+            e = beams <= 4    ? launch_behind(reorder_kernel<4>, dim3((unsigned)grid), kThreads, 0, st, a)
+                : beams <= 8  ? launch_behind(reorder_kernel<8>, dim3((unsigned)grid), kThreads, 0, st, a)
+                : beams <= 16 ? launch_behind(reorder_kernel<16>, dim3((unsigned)grid), kThreads, 0, st, a)
+                              : launch_behind(reorder_kernel<32>, dim3((unsigned)grid), kThreads, 0, st, a);
+            a.table_split = 0;
         }
-        // CTAs: eight times what the device holds at once, none without a piece (80 layers of 8 x 8 beams: 80.5 us; with four times as many
-        // 84.6, with two 94, with sixteen 95)
-        const int64_t wanted = std::max<int64_t>(1, (int64_t)sms * 32 / (a.groups * a.num_caches));
-        a.split = (int)std::min(wanted, (most + kThreads - 1) / kThreads);
-        a.table_split = from ? 0 : std::max(1, std::min((a.max_pages + kThreads - 1) / kThreads, 16));
-        const int64_t grid = a.groups * ((int64_t)a.num_caches * a.split + a.table_split);
-        if (grid > 0x7FFFFFFF) return TKV_EINVAL;
-        cudaStream_t st = (cudaStream_t)stream;
-        e = beams <= 4    ? launch_behind(reorder_kernel<4>, dim3((unsigned)grid), kThreads, 0, st, a)
-            : beams <= 8  ? launch_behind(reorder_kernel<8>, dim3((unsigned)grid), kThreads, 0, st, a)
-            : beams <= 16 ? launch_behind(reorder_kernel<16>, dim3((unsigned)grid), kThreads, 0, st, a)
-                          : launch_behind(reorder_kernel<32>, dim3((unsigned)grid), kThreads, 0, st, a);
     }
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
