@@ -249,8 +249,8 @@ __device__ __forceinline__ void add_piece(Best& best, uint4 u, int v0, const Bou
     }
 }
 
-// A tile's part of the best: pieces p + i kThreads + tid.  Tiles come in order.
-template <typename T>
+// A tile's part of the best: pieces p + i kThreads + tid.  Tiles come in order; ONLY: there is one, and a barrier follows.
+template <typename T, bool ONLY>
 __device__ __forceinline__ void look_over(Best& best, const uint4 (&raw)[kVectors], int p, int count, Bound& b) {
     using P = typename Two<T>::type;
     constexpr int E = 16 / sizeof(T);
@@ -260,7 +260,7 @@ __device__ __forceinline__ void look_over(Best& best, const uint4 (&raw)[kVector
     for (int i = 0; i < kVectors; ++i) tops[i] = largest_of<P>(raw[i]);
     const float top = larger_of(max2(max2(tops[0], tops[1]), max2(tops[2], tops[3])));
     const bool has = top > -INFINITY && top >= b.lowest;
-    const int shift = group_shift(count), above = groups_with(has, shift);
+    const int shift = group_shift(count), above = ONLY ? count + 1 : groups_with(has, shift);
     if (above == 0) return;
     if (above > count) {   // otherwise all of theirs come into the list
         int at = 0;                                        // the lowest place of the largest
@@ -286,6 +286,7 @@ __device__ __forceinline__ void look_over(Best& best, const uint4 (&raw)[kVector
     const int n = best.found;
     sort_best(best.keys, n, count, best.list);
     b.held = min(n, count);
+    if (ONLY) return;
     __syncthreads();
     if (b.held == count) {
         b.least = best.list[count - 1] + 1;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
     Bound b{-INFINITY, 0, 0};
     bool by_tiles = false;
     if (tiles == 1) {
-        look_over<T>(best, raw, first, a.count, b);
+        look_over<T, true>(best, raw, first, a.count, b);
     } else {
         // A bound from below: `count` groups of threads have a value that reaches it.  Then the cells that do.
         const int used = (tiles + span - 1) / span;
@@ -466,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
         }
         if (by_tiles) {
             __syncthreads();   // everyone has read it
-            if (tid == 0) best.found = 0;
+            if (tid == 0) best.found = best.bound = 0;
             b = Bound{-INFINITY, 0, 0};
             __syncthreads();
             for (int p = first; p < end; p += kTile) {
 #pragma unroll
                 for (int i = 0; i < kVectors; ++i) raw[i] = load(p + i * kThreads + tid);
-                look_over<T>(best, raw, p, a.count, b);
+                look_over<T, false>(best, raw, p, a.count, b);
             }
         }
     }
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     __shared__ int tokens[kGroupThreads * kEach];
     __shared__ uint64_t bound;
     __shared__ int found;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, per_row = a.chunks * a.count, n = a.beams * per_row;
+    const int b = blockIdx.x, tid = threadIdx.x, per_row = a.chunks * a.count, n = a.beams * per_row;
     const Candidate* best = a.best + (int64_t)b * n;
     for (int w = tid; w < a.beams; w += kThreads) {               // what precedes the main kernel has been done before this one starts
         const int row = b * a.beams + w;
@@ -549,29 +550,28 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     Candidate early[kEarly];
 #pragma unroll
     for (int k = 0; k < kEarly; ++k) early[k] = tid + k * kThreads < n ? best[tid + k * kThreads] : Candidate{0.0f, -1};
-    const int lanes = a.chunks > 16 ? 16 : a.chunks > 8 ? 8 : a.chunks > 4 ? 4 : a.chunks > 1 ? 2 : 0;   // lane 0 has the sum of twice as many
-    for (int w = tid >> 5; w < a.beams; w += kWarps) {            // a warp a beam
-        const int row = b * a.beams + w;
-        const float score = score_of[w];
-        Wide o{NAN, 0.0f};
+    const int lanes = a.chunks > 16 ? 32 : a.chunks > 8 ? 16 : a.chunks > 4 ? 8 : a.chunks > 2 ? 4 : a.chunks;   // of a beam
+    const int mine_of = tid & (lanes - 1);
+    for (int from = 0; from < a.beams; from += kThreads / lanes) {
+        const int w = from + tid / lanes;
+        const Stat* s = a.stats + ((int64_t)b * a.beams + min(w, a.beams - 1)) * a.chunks;   // of a beam that is out: anything
         float top = kFloor;
-        if (fabsf(score) < INFINITY) {
-            if (is_done[w]) {
-                o = Wide{score, 0.0f};
-            } else {
-                const Stat* s = a.stats + (int64_t)row * a.chunks;
-                for (int i = lane; i < a.chunks; i += 32) top = fmaxf(top, s[i].m);
-                top = of_ordered(__reduce_max_sync(0xffffffffu, ordered(top)));
-                Wide sum{0.0f, 0.0f};
-                for (int i = lane; i < a.chunks; i += 32) sum = plus(sum, Wide{s[i].sum * exp2_fast((s[i].m - top) * kLog2E), 0.0f});
-                for (int d = lanes; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
-                if (sum.hi > 0.0f && sum.hi < INFINITY) {   // not: a NaN or an infinity among the logits, or nothing above -infinity
+        for (int i = mine_of; i < a.chunks; i += lanes) top = fmaxf(top, s[i].m);
+        for (int d = lanes / 2; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        Wide sum{0.0f, 0.0f};
+        for (int i = mine_of; i < a.chunks; i += lanes) sum = plus(sum, Wide{s[i].sum * exp2_fast((s[i].m - top) * kLog2E), 0.0f});
+        for (int d = lanes / 2; d; d >>= 1) sum = plus(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+        if (w < a.beams && mine_of == 0) {
+            const float score = score_of[w];
+            Wide o{NAN, 0.0f};
+            if (fabsf(score) < INFINITY) {
+                if (is_done[w]) {
+                    o = Wide{score, 0.0f};
+                } else if (sum.hi > 0.0f && sum.hi < INFINITY) {   // not: a NaN or an infinity among the logits, or nothing above -infinity
                     const Wide l = plus(log_of(sum.hi), Wide{__fdividef(sum.lo, sum.hi), 0.0f});
                     o = plus(Wide{score, 0.0f}, Wide{-l.hi, -l.lo});
                 }
             }
-        }
-        if (lane == 0) {
             reference[w] = top;
             offset[w] = o;
         }
