@@ -28,18 +28,23 @@ constexpr int kWarps = 7, kThreads = (kWarps + 1) * 32;   // warps that compute,
 constexpr int kCombineWarps = 8;
 constexpr int kMinTiles = kWarps;       // of a CTA's share: one a warp; below, joining costs more than it brings
 // Up to these numbers of positions in sight a CTA takes whole items, and nothing is left to join: always; where the items
-// may be as many as the SMs and the pages are of 4 or 8 bits.  One launch instead of two, but uneven shares.  Whole and cut, us, 8 KV
+// may be as many as the SMs and the pages are of 4 bits.  One launch instead of two, but uneven shares.  Whole and cut, us, 8 KV
 // heads, groups of 4:
 //   4 bits, d 128: batch 1, 256 positions 6.9 and 8.1, 512 positions 8.7 and 8.3; batch 8, 512 positions 10.5 and 9.9; batch 64,
 //     256 positions 11.8 and 13.7, 512 positions 16.7 and 19.7, 1,024 positions 25.2 and 26.5
 //   4 bits, d 64: batch 1, 256 positions 6.2 and 7.1; batch 64, 512 positions 11.7 and 13.5, 1,024 positions 18.1 and 18.9; but
 //     batch 67 of mixed lengths with a window of 700 positions 20.3 and 16.2, so not beyond 512
-//   8 bits, d 128: batch 1, 256 positions 7.0 and 7.4, 512 positions 8.1 and 7.6; batch 8, 512 positions 9.6 and 9.4; batch 64, 256
-//     positions 12.8 and 16.3, 512 positions 17.9 and 21.9; mixed lengths up to 1,024 31.8 and 26.5; d 64: 5.9 and 6.6, 7.0 and 6.8, 8.0
-//     and 8.0, 8.7 and 10.3, 11.6 and 13.8, 16.7 and 14.8
+//   8 bits, 24/4 heads of 128, the cut ones with kItemTiles: batch 8, 256 positions 7.9 and 8.6; batch 160, 256 positions 13.0 and 14.7, 512
+//     positions 22.1 and 23.4; of mixed lengths up to 256 12.3 and 11.8, up to 512 16.2 and 13.0, with two drafted tokens 26.5 and 18.6; of
+//     64: 6.7 and 7.9; 9.3 and 12.2, 13.7 and 15.0; 9.8 and 10.8, 12.3 and 11.5, 19.7 and 14.5; so not beyond 256, as lengths mostly differ
 //   bf16, d 128: batch 1, 64 positions 5.5 and 9.0, 256 positions 7.6 and 7.6; batch 64, 256 positions 20.0 and 20.4, 512 positions
 //     33.1 and 32.3; d 64: batch 64, 256 positions 15.8 and 16.0, 512 positions 24.6 and 23.7
 constexpr int kWholeShort = 256, kWholeMany = 512;
+// 8 bits: what an item costs beside its tiles, in tiles: q's rows, 0.7 us, its output and the next one's begin.  The deal counts them behind an
+// item's own tiles, or the short sequences of a batch would be one warp's: 16 sequences of 0 to 24,268 positions, 25/5 heads of 64, 28.8
+// us with none and 21.7 with 3; 19 mixed ones of 24/8 heads, drafted tokens and a window 16.4 and 12.1; 110 of up to 575 27.3 and 18.4;
+// with 1 or 6 up to 10 % more; of one length the same.
+constexpr int kItemTiles = 3;
 constexpr int kSpinLimit = 1 << 18;     // tries of a wait; 1.5 us each where nothing comes, so 0.4 s
 constexpr double kLog2E = 1.4426950408889634;
 
@@ -53,6 +58,7 @@ struct PagedAttnArgs {
     int32_t* status;
     int64_t rows, q_row, q_head, out_row, out_head;
     int hq, group, window, page_shift, grid, whole_items, q_fp16;
+    int pad;                             // tiles that an item counts for beyond its own: what its begin and end cost
     uint32_t group_mul;                  // floor((2^32 - 1) / group)
     int give_up;                         // this computing warp of the grid behaves as if its first wait had run out; -1: none
     float scale_log2;
@@ -125,7 +131,7 @@ __device__ __forceinline__ Seq sequence_of(const PagedAttnArgs& a, int c0, int c
     s.len = min(s.full, a.c.max_pages << a.page_shift);
     s.lo = 0;
     if (a.window > 0) s.lo = min(s.len, window_begin(a, s.full - s.n)) & ~31;
-    s.units = max(1, (s.len - s.lo + TP - 1) / TP);   // a row that sees nothing is written too
+    s.units = max(1, (s.len - s.lo + TP - 1) / TP) + a.pad;   // a row that sees nothing is written too
     s.tiles = s.n > 0 ? (int)(((int64_t)s.n * a.group + R - 1) / R) : 0;
     return s;
 }
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
             if (failed) break;
             const Piece& piece = sh.queue[warp][place];   // stays where it is: its place is taken again much later
             ++taken;
-            const int all_from = piece.rows.all_from, all_until = piece.rows.all_until, tiles = piece.tiles;
+            const int all_from = piece.rows.all_from, all_until = piece.rows.all_until, any_until = piece.rows.any_until, tiles = piece.tiles;
             Query<D, NT> q;
             q.s = sh.q[warp] + lane;
             load_query<D, NT, KIND>(reinterpret_cast<const uint16_t*>(a.q), a.q_row, a.q_head, a.q_fp16, a.group, a.group_mul, a.scale_log2,
@@ -738,7 +744,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
                 const uint8_t* at = sh.ring[warp] + stage * TB;
                 const uint32_t at_s = smem_u32(at);
                 const uint32_t bad = sh.bad[warp][stage][0] | (T::groups == 2 ? sh.bad[warp][stage][1] << 1 : 0);
-                if (!bad && p0 + TP <= all_until && p0 >= all_from) {
+                if (KIND == kE4m3 && p0 >= any_until) {
+                    // a tile that only counts
+                } else if (!bad && p0 + TP <= all_until && p0 >= all_from) {
 #pragma unroll 1
                     for (int g = 0; g < T::groups; g += C::at_once)
                         attend_tile<D, NT, KIND, C::at_once, true>(at + g * T::record, at_s, lane, p0 + 16 * g, false, piece.rows, a.group,
@@ -1129,9 +1137,10 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     cudaStream_t st = (cudaStream_t)stream;
     const int nt = rows_of_32(a, max_new, sight, sms) ? 4 : row_tiles(a.group, max_new);
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
-    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && has_records(cache->kv_type));
+    a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && cache->kv_type == TKV_INT4);
     const bool two_groups = cache->kv_type == TKV_INT4 || (cache->kv_type == TKV_E4M3 && cache->head_dim == 64);   // 32 positions a tile
-    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (two_groups ? 32 : 16) + 1);
+    a.pad = cache->kv_type == TKV_E4M3 && !a.whole_items ? kItemTiles : 0;
+    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (two_groups ? 32 : 16) + 1 + a.pad);
     if (tile_bound > kMostTiles) return TKV_EINVAL;
     e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
     if (e != cudaSuccess) {
