@@ -253,6 +253,21 @@ def test_attention_of_many_sequences(d):
         close(p, *p.cache.attend(q, p.cu_t, max_new=new, max_len=ln, return_lse=True), want, BF16)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths,n,G", [([36007], [1], 3), ([20001, 5], [3, 1], 4), ([2500], [6], 5), ([9000, 0, 41], [1, 1, 1], 8)])
+def test_items_of_many_pieces(dtype, d, lengths, n, G):
+    """Few long sequences: an item is cut between up to all CTAs, and several of them join it."""
+    p = Pool8(lengths, n, d=d, page=64).fill()
+    q = queries(p, G, int(p.cu[-1]), dtype)
+    want = p.oracle(q)
+    for new, ln in ((max(n), max(lengths)), (1, 1 << 20), (100, 1 << 20)):
+        out, lse = p.cache.attend(q, p.cu_t, max_new=new, max_len=ln, return_lse=True)
+        close(p, out, lse, want, dtype)
+        again = p.cache.attend(q, p.cu_t, max_new=new, max_len=ln, return_lse=True)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("new", [1, 3, 8])
 def test_blocks_of_very_different_scales(d, new):

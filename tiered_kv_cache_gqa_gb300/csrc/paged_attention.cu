@@ -892,6 +892,108 @@ __global__ void __launch_bounds__(kThreads, Config<D, NT, KIND>::ctas) paged_att
 // CTA i takes the item that is cut at the end of share i, if it began in share i: its pieces are record 1 of CTA i and
 // record 0 of the CTAs after it.  The pieces' references and sums are turned into weights first, a piece a lane and two
 // rows a warp at a time; the sums of O then have no order to wait for but their own.
+//
+// 8 bits: where an item has more than kFewPieces, the CTAs that are cut within it share its sums: an eighth each, 32 at least, and in a CTA
+// groups of threads take every so manieth piece.  The call for one sequence of 36,171 positions, 16/2 heads of 128, which is two items
+// of 152 pieces: 20.5 us with one CTA an item, 12.8 like this; of 100,000, 8/1 heads, 32.7 and 16.3; of 2,512, 28/4 heads, 9.4 and 8.6.
+constexpr int kFewPieces = 8, kBatchPieces = 128;
+template <int D, int NT>
+struct Slice {
+    static constexpr int slots = Rec4<D, NT>::sums / 8 > 32 ? Rec4<D, NT>::sums / 8 : 32, count = Rec4<D, NT>::sums / slots;
+    static_assert(count <= kFewPieces, "a CTA that is cut within the item for each");
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void join_many(const PagedAttnArgs& a, const Rows& rows, const float4* first, int pieces, int slice, bool fp16) {
+    constexpr int SLOTS = Rec4<D, NT>::sums, SIZE = Rec4<D, NT>::size, WIDE = Slice<D, NT>::slots, G = kCombineWarps * 32 / WIDE, IN_FLIGHT = 8;
+    static_assert(WIDE % 32 == 0 && WIDE <= 4 * D / 2 * NT && G >= 2, "whole warps, in one tile of 8 rows or several");
+    constexpr int TWOS = 4 * NT;
+    __shared__ float2 weight_of[kBatchPieces][TWOS];
+    __shared__ float4 scale_ml[TWOS], total_ml[TWOS];
+    __shared__ float4 part[kCombineWarps * 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = tid / WIDE, slot = slice * WIDE + tid % WIDE;
+    auto record = [&](int i) { return first + (i ? 2 * (int64_t)i * SIZE : SIZE); };
+    const int my_two = slot / (D / 16 * 32) * 4 + (tid & 3);
+    float4 x = make_float4(0, 0, 0, 0);
+    float4 ml_of[(TWOS + kCombineWarps - 1) / kCombineWarps];
+#pragma unroll
+    for (int k = 0; k < (TWOS + kCombineWarps - 1) / kCombineWarps; ++k) ml_of[k] = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < pieces; i0 += kBatchPieces) {
+        const int n = min(kBatchPieces, pieces - i0);
+        float4 y[IN_FLIGHT];
+        auto read = [&](int p) {   // pieces p + g, p + g + G, ..
+#pragma unroll
+            for (int q = 0; q < IN_FLIGHT; ++q) y[q] = record(i0 + min(p + q * G + g, n - 1))[slot];
+        };
+        read(0);
+#pragma unroll
+        for (int k = 0; k < (TWOS + kCombineWarps - 1) / kCombineWarps; ++k) {
+            const int two = warp + k * kCombineWarps;
+            if (two >= TWOS) break;
+            float4 v[kBatchPieces / 32];
+            float m0 = ml_of[k].x, m1 = ml_of[k].z;
+#pragma unroll
+            for (int q = 0; q < kBatchPieces / 32; ++q) {
+                const int i = q * 32 + lane;
+                v[q] = i < n ? record(i0 + i)[SLOTS + two] : make_float4(kLowest, 0.0f, kLowest, 0.0f);
+            }
+#pragma unroll
+            for (int q = 0; q < kBatchPieces / 32; ++q) {
+                m0 = fmaxf(m0, v[q].x);
+                m1 = fmaxf(m1, v[q].z);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            }
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kBatchPieces / 32; ++q) {
+                const float w0 = exp2_approx(v[q].x - m0), w1 = exp2_approx(v[q].z - m1);
+                l0 = fmaf(v[q].y, w0, l0);
+                l1 = fmaf(v[q].w, w1, l1);
+                weight_of[q * 32 + lane][two] = q * 32 + lane < n ? make_float2(w0, w1) : make_float2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+            }
+            const float f0 = exp2_approx(ml_of[k].x - m0), f1 = exp2_approx(ml_of[k].z - m1);
+            ml_of[k] = make_float4(m0, ml_of[k].y * f0 + l0, m1, ml_of[k].w * f1 + l1);
+            if (lane == 0) {
+                scale_ml[two] = make_float4(f0, f1, 0.0f, 0.0f);
+                total_ml[two] = ml_of[k];
+            }
+        }
+        __syncthreads();
+        const float4 f = scale_ml[my_two];
+        x = make_float4(x.x * f.x, x.y * f.y, x.z * f.x, x.w * f.y);
+#pragma unroll 1
+        for (int p = 0; p < n; p += IN_FLIGHT * G) {
+            if (p) read(p);
+#pragma unroll
+            for (int q = 0; q < IN_FLIGHT; ++q) {
+                const int i = p + q * G + g;
+                const float2 w = i < n ? weight_of[i][my_two] : make_float2(0.0f, 0.0f);
+                x = make_float4(fmaf(y[q].x, w.x, x.x), fmaf(y[q].y, w.y, x.y), fmaf(y[q].z, w.x, x.z), fmaf(y[q].w, w.y, x.w));
+            }
+        }
+        __syncthreads();
+    }
+    part[tid] = x;
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+        const float4 y = part[tid + k * WIDE];
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    emit4<D, kE4m3>(a, rows, slot / (D / 16 * 32), slot / 32 % (D / 16), lane, x, total_ml[my_two], 1.0f, fp16);
+}
+
 template <int D, int NT, int KIND>
 __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a, bool fp16) {
     constexpr int R = 8 * NT, TP = TileOf<D, KIND>::positions, SLOTS = Rec4<D, NT>::sums, SIZE = Rec4<D, NT>::size;
@@ -907,13 +1009,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     const int cut = total == kTooMany ? total : (int)min((int64_t)total, (int64_t)(blockIdx.x + 1) * share);
     locate<R, TP, kCombineWarps, 1>(a, cut, 0, before, own, &at);
     __syncthreads();
-    int pieces = 0;
+    int pieces = 0, slice = 0;
     Rows rows{};
     if (cut < total) {
         const Seq s = sequence<R, TP>(a, at.b);
         const int item = at.in_seq / s.units, c = at.in_seq - item * s.units;
-        if (c > 0 && c <= share) {   // something is cut here, and it began in this share
-            pieces = (cut - c + s.units - 1) / share - (int)blockIdx.x + 1;
+        const int begin = (cut - c) / share;   // the CTA in whose share it began
+        if (KIND == kE4m3 && c > 0) slice = (int)blockIdx.x - begin;
+        if (c > 0 && (c <= share || KIND == kE4m3)) {   // something is cut here, and it began in this share
+            pieces = (cut - c + s.units - 1) / share - begin + 1;
             rows.h = item / s.tiles;
             rows.row0 = (item - rows.h * s.tiles) * R;
             rows.first_row = s.first_row;
@@ -924,6 +1028,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
     // cu_tokens were read before.
     wait_for_previous();
     if (pieces == 0) return;
+    if constexpr (KIND == kE4m3) {
+        if (pieces > kFewPieces) {
+            if (slice < Slice<D, NT>::count) join_many<D, NT>(a, rows, a.part + (int64_t)2 * ((int)blockIdx.x - slice) * SIZE, pieces, slice, fp16);
+            return;
+        }
+        if (slice) return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float gain = KIND == kInt4 ? 16.0f * (a.c.v_gain ? a.c.v_gain[rows.h] : 1.0f) : 1.0f;
     const float4* first = a.part + (int64_t)2 * blockIdx.x * SIZE;
