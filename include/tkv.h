@@ -549,14 +549,14 @@ int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_head
 /* Beam search: the best continuations of each sequence's beams.
  *   total[b][w][v] = scores[b][w] + logits[b][w][v] - log sum_v exp(logits[b][w][v])
  * and the outputs are the `count` largest over (w, v), in descending order, ties to the
- * lowest w * vocab + v: the total, the beam w and the token v.
- * Within a beam the order is that of the logits.
+ * lowest w * vocab + v: the total, the beam w and the token v.  Totals are compared in 64 bits.
+ * Within a beam the order is that of the logits, even where their totals are equal in 64 bits.
  * finished (device uint8 [batch][beams], or NULL): a beam where it is not 0 offers
  * one candidate, token eos with the beam's own score; its logits are not read.
  * A beam with a score that is not finite, or with a NaN or +infinity among its logits, offers
  * none, and no candidate has a logit of -infinity or a total below the lowest fp32 number.
- * Places that are left over get score -infinity, beam -1 and token -1.  Totals are sums of two fp32
- * numbers; a row's log of its sum is good to about 2^-20, and the same for equal rows.
+ * Places that are left over get score -infinity, beam -1 and token -1.  A row's log of its sum is
+ * good to about 2^-20, and the same for equal rows.
  * logits: device [batch][beams][vocab] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, the
  * vocabulary contiguous, strides in elements (any alignment); scores: device fp32
  * [batch][beams]; out_scores, out_beams, out_tokens: device [batch][count].

@@ -34,7 +34,7 @@ constexpr int kMaxCount = 64, kMaxBeams = 64;
 constexpr int kVectors = 4;                       // 16-byte pieces of a thread and tile
 constexpr int kCtas = 4;                          // on an SM at once, by their registers
 constexpr int kCells = 16;                        // of a thread
-constexpr int kIndexBits = 12;                    // of a candidate's index in the joining kernel
+constexpr int kIndexBits = 12;                    // of a candidate's index in its rank, in the joining kernel
 constexpr int kMostCandidates = 1 << kIndexBits;  // of a sequence
 constexpr int kMostGroups = kThreads;
 constexpr int kFew = 64;                          // candidates of a sequence that are sorted whole
@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ joining
-// Totals are sums of two fp32 numbers, good to 2^-46 or so: fp64 instructions are few and slow here (20 us for this kernel with them).
+// A row's sum and its logarithm are sums of two fp32 numbers, good to 2^-46 or so: fp64 instructions are few and slow here (20 us for this
+// kernel with them).
 struct Wide {
     float hi, lo;   // hi is the nearest to hi + lo
 };
@@ -524,18 +525,54 @@ __device__ __forceinline__ Wide log_of(float x) {
     return plus(sum_of(__fmul_rn(k, 0.693145751953125f), __fmul_rn(k, 1.42860682030941723e-6f)), Wide{logf(m), 0.0f});   // ln 2 in 16 bits, and the rest
 }
 
-// One CTA a sequence.  A candidate's key: its total, to 2^-44 of it, then the lower index (w, chunk, place in the chunk's list): among
-// equal totals that is the lower place w V + v.
+// A candidate's rank.  Its total is (x - reference) + offset, two roundings to 64 bits that never turn the order of a row's x round, so
+// what is equal there is left to the logit itself: the larger total comes first, then the lower beam, the larger x, and the lower
+// candidate, whose token is lower where x is equal too.  All zeros: none.
+struct __align__(16) Rank {
+    uint64_t total, rest;
+};
+__device__ __forceinline__ bool precedes(Rank a, Rank b) { return a.total > b.total || (a.total == b.total && a.rest > b.rest); }
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    return u >> 63 ? ~u + (u << 1 == 0) : u | 1ull << 63;   // -0 is 0
+}
+__device__ __forceinline__ double of_ordered(uint64_t o) { return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o)); }
+
+constexpr int kMostRanks = 512;
+static_assert(kMostRanks >= kMaxCount + kThreads, "the best so far and a candidate of each thread");
+
+// *bound = the k-th largest of the maxima of groups of 2^shift threads, if so many are not 0.  A barrier follows before it is read.
+__device__ __forceinline__ void kth_largest(uint32_t mine, int k, int shift, uint32_t (&maxima)[kMostGroups], uint32_t* bound) {
+    for (int o = 1; o < 1 << shift; o <<= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    const int groups = kThreads >> shift, tid = threadIdx.x;
+    if ((tid & ((1 << shift) - 1)) == 0) maxima[tid >> shift] = mine;
+    __syncthreads();
+    if (tid >= groups) return;
+    mine = maxima[tid];
+    int above = 0, equal = 0;
+#pragma unroll 2
+    for (int i = 0; i < groups; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(maxima + i);
+        above += (u.x > mine) + (u.y > mine) + (u.z > mine) + (u.w > mine);
+        equal += (u.x == mine) + (u.y == mine) + (u.z == mine) + (u.w == mine);
+    }
+    if (mine && above < k && above + equal >= k) *bound = mine;   // all that are equal write the same
+}
+
+// One CTA a sequence.  Candidates are counted by beam, chunk and place in the chunk's list.  Which of them come into question is found in 32
+// bits, with room for what these round; only those get a rank, as an SM does two operations of 64 bits a cycle (0.1 to 0.3 us of the call).
+// The shared memory is kept below 16 KB: with 24 an SM that has run the main kernel is divided anew for this one, and the call for 64 x 8
+// beams of 131,072, 16 chosen, took 36.1 us instead of 31.8, for 16 x 4 of 32,000, 8 chosen, 13.2 instead of 9.8.
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_constant__ SelectArgs a) {
-    constexpr int kEach = kMostCandidates / kThreads;             // candidates of a thread
     __shared__ float reference[kMaxBeams], score_of[kMaxBeams];
     __shared__ bool is_done[kMaxBeams];
-    __shared__ Wide offset[kMaxBeams];                            // total = (x - reference) + offset
-    __shared__ __align__(16) uint64_t maxima[kMostGroups];
-    __shared__ uint64_t keys[kGroupThreads * kEach];
-    __shared__ int tokens[kGroupThreads * kEach];
-    __shared__ uint64_t bound;
-    __shared__ int found;
+    __shared__ Wide offset[kMaxBeams];                            // total = (x - reference) + offset; NaN: the beam offers none
+    __shared__ double offset64[kMaxBeams], reference64[kMaxBeams];
+    __shared__ __align__(16) uint32_t maxima[kMostGroups];
+    __shared__ Rank ranks[kMostRanks];                            // at first x and the candidate's number
+    __shared__ int tokens[kMostRanks];
+    __shared__ uint32_t least;
+    __shared__ int found, none;
     const int b = blockIdx.x, tid = threadIdx.x, per_row = a.chunks * a.count, n = a.beams * per_row;
     const Candidate* best = a.best + (int64_t)b * n;
     for (int w = tid; w < a.beams; w += kThreads) {               // what precedes the main kernel has been done before this one starts
@@ -577,29 +614,35 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
         }
     }
     if (tid == 0) {
-        found = 0;
-        bound = 1;   // below every candidate
+        found = none = 0;
+        least = ordered(-INFINITY);
     }
     __syncthreads();
-    // Candidate i of the sequence.  Thread t takes t, t + 256, ..
-    auto key_of_candidate = [&](int i, Candidate c) -> uint64_t {
-        const int w = i / per_row;
-        const Wide o = offset[w];
-        if (isnan(o.hi)) return 0;
-        Wide t = o;
-        if (is_done[w]) {
-            if (i != w * per_row) return 0;
-        } else {
-            if (c.v < 0) return 0;
-            t = plus(sum_of(c.x, -reference[w]), o);
-            if (!(fabsf(t.hi) < INFINITY)) return 0;   // below the lowest number
-        }
-        return (uint64_t)ordered(t.hi) << 32 | (ordered(t.lo) >> kIndexBits << kIndexBits) | (uint32_t)(kMostCandidates - 1 - i);
+    const uint32_t by_row = ((1u << 24) + per_row - 1) / per_row;   // i * by_row >> 24 = i / per_row, as i < 64 per_row and i per_row < 2^24
+    // Candidate i of the sequence: whether it is one, and what its total is at least and at most.  Thread t takes t, t + 256, ..
+    auto bounds_of = [&](int i, Candidate c, float* low, float* high) -> bool {
+        const int w = (int)(i * by_row >> 24);
+        const float o = offset[w].hi;
+        const bool done = is_done[w];
+        if (isnan(o) || (done ? i != w * per_row : c.v < 0)) return false;
+        const float x = done ? 0.0f : c.x - reference[w], t = x + o;
+        const float off = (fabsf(x) + fabsf(o)) * 0x1p-22f;   // x, t and the offset are rounded by 2^-24 of themselves, *low and *high too
+        *low = t - off;
+        *high = fabsf(t) < INFINITY ? t + off : INFINITY;
+        return true;
     };
-    uint64_t mine = 0;
+    uint32_t mine = 0;
+    float top = -INFINITY;
+    auto consider = [&](int i, Candidate c) {
+        float low, high = NAN;
+        if (!bounds_of(i, c, &low, &high)) return high;
+        mine = max(mine, ordered(low));
+        top = fmaxf(top, high);
+        return high;
+    };
+    float early_high[kEarly];
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-        if (tid + k * kThreads < n) mine = max(mine, key_of_candidate(tid + k * kThreads, early[k]));
+    for (int k = 0; k < kEarly; ++k) early_high[k] = tid + k * kThreads < n ? consider(tid + k * kThreads, early[k]) : NAN;
 #pragma unroll 1
     for (int i = tid + kEarly * kThreads; i < n; i += 4 * kThreads) {   // a few at once
         Candidate c[4];
@@ -607,44 +650,109 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k) c[k] = i + k * kThreads < n ? best[i + k * kThreads] : Candidate{0.0f, -1};
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-            if (i + k * kThreads < n) mine = max(mine, key_of_candidate(i + k * kThreads, c[0]));
+            if (i + k * kThreads < n) consider(i + k * kThreads, c[0]);
             c[0] = c[1];
             c[1] = c[2];
             c[2] = c[3];
         }
     }
     // few candidates are sorted as they are
-    if (n > kFew) kth_largest(mine, a.count, group_shift(a.count), maxima, &bound);
+    if (n > kFew) kth_largest(mine, a.count, group_shift(a.count), maxima, &least);
+    if (tid >= kThreads - a.beams) {   // the last warps, which have less to do there
+        const int w = kThreads - 1 - tid;
+        reference64[w] = reference[w];
+        offset64[w] = (double)offset[w].hi + (double)offset[w].lo;
+    }
     __syncthreads();
-    const uint64_t least = bound;
-    auto add = [&](int i, Candidate c) {
-        const uint64_t k = key_of_candidate(i, c);
-        if (k < least) return;
+    auto take = [&](int i, Candidate c) {
         const int slot = atomicAdd(&found, 1);
-        keys[slot] = k;
+        if (slot >= kMostRanks) return;
+        ranks[slot] = Rank{__float_as_uint(c.x), (uint64_t)i};
         tokens[slot] = c.v;
     };
-    if (mine >= least) {
+    const float reach = of_ordered(least);
+    if (top >= reach) {
+        auto add = [&](int i, Candidate c) {
+            float low, high;
+            if (bounds_of(i, c, &low, &high) && high >= reach) take(i, c);
+        };
 #pragma unroll
         for (int k = 0; k < kEarly; ++k)
-            if (tid + k * kThreads < n) add(tid + k * kThreads, early[k]);
+            if (early_high[k] >= reach) take(tid + k * kThreads, early[k]);
         for (int i = tid + kEarly * kThreads; i < n; i += kThreads) add(i, best[i]);
     }
     __syncthreads();
-    const int m = found;
+    auto rank_of = [&](int i, Candidate c) -> Rank {
+        const int w = (int)(i * by_row >> 24);
+        const bool done = is_done[w];
+        if (done ? i != w * per_row : c.v < 0) return Rank{0, 0};
+        const float x = done ? 0.0f : c.x;
+        const double o = offset64[w], t = done ? o : ((double)x - reference64[w]) + o;
+        if (!(fabs(t) < 0x1.ffffffp+127)) return Rank{0, 0};   // none, or below the lowest number of 32 bits
+        return Rank{ordered(t), (uint64_t)(kMaxBeams - 1 - w) << (32 + kIndexBits) | (uint64_t)ordered(x) << kIndexBits | (uint32_t)(kMostCandidates - 1 - i)};
+    };
+    int m = found;
+    if (m <= kMostRanks) {
+        for (int i = tid; i < m; i += kThreads) {
+            const Rank r = ranks[i] = rank_of((int)ranks[i].rest, Candidate{__uint_as_float((uint32_t)ranks[i].total), tokens[i]});
+            if (!r.total) atomicAdd(&none, 1);
+        }
+        __syncthreads();
+    } else {   // as many that are equal or nearly: a candidate of each thread joins the best so far, and so on
+        m = 0;
+        for (int i = tid; i - tid < n; i += kThreads) {
+            __syncthreads();
+            if (tid == 0) found = m;
+            __syncthreads();
+            const Candidate c = i < n ? best[i] : Candidate{0.0f, -1};
+            const Rank r = i < n ? rank_of(i, c) : Rank{0, 0};
+            if (r.total && (m < a.count || precedes(r, ranks[a.count - 1]))) {
+                const int slot = atomicAdd(&found, 1);
+                ranks[slot] = r;
+                tokens[slot] = c.v;
+            }
+            __syncthreads();
+            const int all = found;
+            Rank kept[2];
+            int token[2], place[2] = {kMaxCount, kMaxCount};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = tid + k * kThreads;
+                if (j >= all) continue;
+                kept[k] = ranks[j];
+                token[k] = tokens[j];
+                place[k] = 0;
+                for (int q = 0; q < all; ++q) place[k] += precedes(ranks[q], kept[k]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (place[k] < a.count) {
+                    ranks[place[k]] = kept[k];
+                    tokens[place[k]] = token[k];
+                }
+            m = min(all, a.count);
+        }
+        __syncthreads();
+    }
     const int64_t out = (int64_t)b * a.count;
-    for (int i = tid; i < m; i += kThreads) {
-        const uint64_t k = keys[i];
+    const int each = m <= kThreads / 4 ? 4 : m <= kThreads / 2 ? 2 : 1;   // threads of a candidate
+    for (int from = 0; from < m * each; from += kThreads) {
+        const int i = (from + tid) / each;
+        const Rank r = i < m ? ranks[i] : Rank{0, 0};
         int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < m; ++j) rank += keys[j] > k;
-        if (rank >= a.count) continue;
-        const int w = (kMostCandidates - 1 - (int)(k & (kMostCandidates - 1))) / per_row;
-        a.out_scores[out + rank] = of_ordered((uint32_t)(k >> 32));
+        if (r.total) {
+#pragma unroll 4
+            for (int j = tid & (each - 1); j < m; j += each) rank += precedes(ranks[j], r);
+        }
+        for (int o = each / 2; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+        if (rank >= a.count || !r.total || (tid & (each - 1))) continue;
+        const int w = kMaxBeams - 1 - (int)(r.rest >> (32 + kIndexBits));
+        a.out_scores[out + rank] = (float)of_ordered(r.total);
         a.out_beams[out + rank] = w;
         a.out_tokens[out + rank] = is_done[w] ? a.eos : tokens[i];
     }
-    for (int i = m + tid; i < a.count; i += kThreads) {
+    for (int i = m - none + tid; i < a.count; i += kThreads) {
         a.out_scores[out + i] = -INFINITY;
         a.out_beams[out + i] = a.out_tokens[out + i] = -1;
     }
