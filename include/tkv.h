@@ -521,7 +521,7 @@ tkv_status tkv_paged_gather(const tkv_paged* cache, void* k, void* v, int32_t dt
  * overlapping; lse:
  * device fp32 [rows][num_q_heads], contiguous.
  * A step's size is limited: (rows * num_q_heads / Hkv / 8 + batch) * Hkv *
- * (max_pages * page_size / 32) tiles (half as many positions a tile with 16-bit
+ * (max_pages * page_size / 32, rounded up) tiles (16 positions a tile with 16-bit
  * pages, and with 8-bit pages of d 128) are at most 2 * 10^9; a longer prompt enters in parts.
  * max_new and max_len are the host's estimates of the largest n_b and the largest
  * length.  They choose how the work is split, not what is computed: any

@@ -1250,9 +1250,11 @@ extern "C" tkv_status tkv_paged_attention(const tkv_paged* cache, const void* q,
     const double items = ((double)rows * a.group / (8 * nt) + cache->batch) * cache->num_kv_heads;   // at most
     a.whole_items = sight <= kWholeShort || (sight <= kWholeMany && items >= sms && cache->kv_type == TKV_INT4);
     const bool two_groups = cache->kv_type == TKV_INT4 || (cache->kv_type == TKV_E4M3 && cache->head_dim == 64);   // 32 positions a tile
-    a.pad = cache->kv_type == TKV_E4M3 && !a.whole_items ? kItemTiles : 0;
-    const double tile_bound = items * ((double)cache->max_pages * cache->page_size / (two_groups ? 32 : 16) + 1 + a.pad);
-    if (tile_bound > kMostTiles) return TKV_EINVAL;
+    const int tile = two_groups ? 32 : 16;
+    const double item_tiles = (double)(((int64_t)cache->max_pages * cache->page_size + tile - 1) / tile);
+    if (items * item_tiles > kMostTiles) return TKV_EINVAL;
+    // what an item counts beyond its tiles refuses no step
+    a.pad = cache->kv_type == TKV_E4M3 && !a.whole_items && items * (item_tiles + kItemTiles) <= kMostTiles ? kItemTiles : 0;
     e = cache->head_dim == 128 ? launch_rows<128>(a, nt, sms, dev, st) : launch_rows<64>(a, nt, sms, dev, st);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
