@@ -66,8 +66,8 @@ __device__ __forceinline__ float2 rotate_pair(float x0, float x1, float2 cs) {
                        __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y)));
 }
 
-// Two fp32 numbers an instruction.  A packed product and a packed sum of the same rounding may be fused into one; these two
-// have different ones.
+// Two fp32 numbers an instruction.  A packed product and a packed sum of the same rounding may be fused into one, which is why
+// mul2_rz, which a sum follows, has a rounding of its own.
 struct F2 {
     uint64_t v;
 };
@@ -86,9 +86,19 @@ __device__ __forceinline__ F2 mul2_rz(F2 a, F2 b) {
     asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
 

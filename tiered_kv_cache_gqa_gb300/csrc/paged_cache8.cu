@@ -99,12 +99,6 @@ __device__ __forceinline__ int exponent_for(float amax) {
 // Two values as codes, the first in the low byte.
 __device__ __forceinline__ uint32_t code_pair(float a, float b) { return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3); }
 
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
 // Four codes as values.
 __device__ __forceinline__ void decode4(uint32_t w, float scale, float (&x)[4]) {
     const float2 a = __half22float2(e4m3_pair((uint16_t)w)), b = __half22float2(e4m3_pair((uint16_t)(w >> 16)));

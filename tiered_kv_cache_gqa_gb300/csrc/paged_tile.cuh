@@ -452,12 +452,14 @@ __device__ __forceinline__ void attend_tile(const uint8_t* tile, uint32_t tile_s
             const float ks = power_of_two(block_exponent(e.x)), ev = (float)block_exponent(e.y);
             un[g] = power_of_two(-block_exponent(e.y));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float z0 = q.z0[nt] * ks, z1 = q.z1[nt] * ks;
-                z[g][nt][0] = fmaf(z[g][nt][0], z0, ev);
-                z[g][nt][1] = fmaf(z[g][nt][1], z1, ev);
-                z[g][nt][2] = fmaf(z[g][nt][2], z0, ev);
-                z[g][nt][3] = fmaf(z[g][nt][3], z1, ev);
+            for (int nt = 0; nt < NT; ++nt) {   // S 2^e_k first, which is within 2^-65 .. 2^62: z0 2^e_k may be infinite, and 0 times that NaN
+                const F2 k2 = f2(ks, ks), q2 = f2(q.z0[nt], q.z1[nt]), v2 = f2(ev, ev);
+                const float2 x = parts(fma2(mul2(f2(z[g][nt][0], z[g][nt][1]), k2), q2, v2));
+                const float2 y = parts(fma2(mul2(f2(z[g][nt][2], z[g][nt][3]), k2), q2, v2));
+                z[g][nt][0] = x.x;
+                z[g][nt][1] = x.y;
+                z[g][nt][2] = y.x;
+                z[g][nt][3] = y.y;
             }
         }
 #pragma unroll
