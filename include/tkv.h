@@ -457,7 +457,10 @@ typedef struct {
  *       2^-6 of the new scale can change.  A code is x 2^-e to nearest even, saturating (at
  *       448 * 2^31); an infinity or a NaN is stored as NaN, and the block's other values stay
  *       what they are.  The rows of a block that come after the step's are as good as free:
- *       sequences that share a block's page may not append to it. */
+ *       sequences that share a block's page may not append to it.  Rows that are taken back
+ *       (lengths set back behind drafted tokens) leave their block's e behind: a drafted row with a
+ *       magnitude 2^k times the others' leaves the rows that stay, and those that come, on a scale
+ *       that is 2^k as coarse, until the block's first position is written again. */
 typedef struct {
     void* pages;                /* device, 16-byte aligned */
     const int32_t* page_table;  /* device int32 [batch][max_pages] */
@@ -560,7 +563,7 @@ int64_t tkv_paged_attention_workspace(const tkv_paged* cache, int32_t num_q_head
  * logits: device [batch][beams][vocab] of dtype TKV_BF16, TKV_FP16 or TKV_FP32, the
  * vocabulary contiguous, strides in elements (any alignment); scores: device fp32
  * [batch][beams]; out_scores, out_beams, out_tokens: device [batch][count].
- * Limits: beams and count 1 .. 64, beams * vocab < 2^31 - 256.
+ * Limits: beams and count 1 .. 64, beams * vocab < 2^31 - 256; tkv_paged_reorder follows 32 beams at most.
  * workspace: tkv_beam_select_workspace(...) bytes on the current device, 16-byte aligned,
  * contents irrelevant; calls that may run at the same time need one each.
  * Errors: TKV_EINVAL (eos outside the vocabulary with `finished` among them), TKV_ECAPACITY

@@ -498,8 +498,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_rows_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ joining
-// A row's sum and its logarithm are sums of two fp32 numbers, good to 2^-46 or so: fp64 instructions are few and slow here (20 us for this
-// kernel with them).
+// A row's sum and its logarithm are sums of two fp32 numbers, good to 2^-46 or so: fp64 instructions are few and slow here (20 us for a
+// kernel with them throughout).  sum_of is Knuth's exact sum of two numbers, plus the usual sum of two double-length
+// numbers (after Dekker), and log_of splits ln 2 as Cody and Waite do.
 struct Wide {
     float hi, lo;   // hi is the nearest to hi + lo
 };
@@ -1009,7 +1010,9 @@ extern "C" tkv_status tkv_paged_reorder(const tkv_paged* caches, int32_t num_cac
     a.page_shift = __builtin_ctz((unsigned)caches[0].page_size);
     // CTAs of an SM: several rounds, which even out what SMs get of the memory, but a round of CTAs without work costs 1.2 us.  80 layers of 8 x 8
     // beams of 1,000 positions: 78.2 us with 20, 91.5 with four; 64 x 4 beams 144 with 48, 173 with eight.  32 layers of 8 x 12 beams of two
-    // positions in pages of 128: 5.3 us with four, 4.2 with two, 10.8 with sixteen.
+    // positions in pages of 128: 5.3 us with four, 4.2 with two, 10.8 with sixteen; 80 layers of 4 x 16 beams 134.6 with four, 138.6 with two, 131.3
+    // with eight.  Behind 16 beams, with one, two, four, eight: 80 layers of 2 x 32 158.8, 158.5, 160.8, 165.8 us; 32 layers of 4 x 32 of 16-bit pages
+    // 20.5, 18.5, 18.8, 24.9; 28 of 1 x 32 6.4, 8.6, 8.6, 8.6; but 16 layers of 16 x 24, heads of 64, 115, 113, 95, 92.
     const int ctas = beams <= 4 ? 48 : beams <= 8 ? 20 : beams <= 16 ? 4 : 2;
     a.table_split = std::max(1, std::min((a.max_pages + kThreads - 1) / kThreads, 16));   // of the first launch
     for (int first = 0; first < num_caches && e == cudaSuccess; ++first) {   // the caches of one shape after those of another

@@ -41,7 +41,8 @@ __device__ __forceinline__ uint4 pack(const float* x) {
 
 // How k is rotated.
 //   kNone      not at all
-//   kHalves    pairs % 16 == 0: the partners of 8 channels lie `pairs` channels away, in another block
+//   kHalves    the partners of 8 channels lie `pairs` channels away, in another piece: pairs % 8 == 0 for 8-bit pages, and for the others
+//              pairs % 16 == 0, in another block
 //   kAdjacent  pairs % 4 == 0: 8 channels hold their own 4 pairs
 //   kAny       channel by channel, partners read one at a time
 enum Turn { kNone, kHalves, kAdjacent, kAny };

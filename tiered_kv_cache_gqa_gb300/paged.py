@@ -254,10 +254,11 @@ def _rope(x, rotary, positions, out, inverse, status):
 
 
 class PagedCache:
-    """A paged cache in the caller's tensors; keeps them alive, writes nothing but pages.
+    """A paged cache in the caller's tensors; keeps them alive, writes nothing but pages (PagedLayers.reorder the page table too).
 
     pages       bf16 or fp16 [num_pages, Hkv, 2, page_size, d], or uint8 [num_pages, Hkv, page_size / 16, 18 d]: 4 bits,
-                [..., 32 d + 16]: 8 bits, E4M3 with a power of two for each block of 16 positions and head
+                [..., 32 d + 16]: 8 bits, E4M3 with a power of two for each block of 16 positions and head, which never falls while
+                the block lives: drafted rows that are taken back leave theirs behind
     page_table  int32 [batch, max_pages]: position p of sequence b lies in page page_table[b, p // page_size]
     lengths     int32 [batch]: positions of each sequence, the step's own included; read by every call, on the device
     k_gain, v_gain  fp32 [Hkv] > 0, 4 bits only: a value is code * scale * gain (1 if None)
@@ -515,7 +516,7 @@ def beam_select(logits, scores, count=None, finished=None, eos=None):
     scores    fp32 [batch, beams]: sums of log probabilities so far; -inf takes a beam out
     finished  bool or uint8 [batch, beams]: such a beam offers token `eos` with its own score, and nothing else
     A candidate's score is scores + log_softmax(logits); where there are fewer than `count`, score -inf, beam -1, token -1.
-    The call has no gradient."""
+    Up to 64 beams, of which PagedLayers.reorder follows 32.  The call has no gradient."""
     w, torch = "beam_select", _types()
     if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 3):
         _on(logits, w, "logits", None, 3)
