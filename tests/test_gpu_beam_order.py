@@ -78,3 +78,26 @@ def test_many_equal_candidates():
     done[0, ::2] = True
     check(torch.zeros(1, 64, 1, device="cuda"), torch.zeros(1, 64, device="cuda"), 64, done, 0)      # every total is 0, of either kind
     check(torch.zeros(1, 64, 1, device="cuda"), torch.zeros(1, 64, device="cuda") * (1 - 2 * done.float()), 64, done, 0)   # or -0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("scores", [[-3e38, 0.0, -1e30, -7.0], [3e38, -3e38, 3.4e38, 0.0], [-1e9, -1e9, 0.0, -1e9], [-3.4028234e38] * 4, [1e-40, -1e-40, 0.0, -0.0]])
+def test_scores_of_any_size(dtype, scores):
+    """Totals that 64 bits cannot tell apart go by beam, then logit, then token; one below the lowest fp32 number is none."""
+    g = torch.Generator("cuda").manual_seed(2)
+    x = (torch.randn(2, 4, 30011, generator=g, device="cuda") * 2.5).to(dtype)
+    s = torch.tensor([scores] * 2, device="cuda")
+    v, w = x.double().cpu().numpy(), s.double().cpu().numpy()
+    log_p = v - v.max(-1, keepdims=True)
+    total = w[..., None] + (log_p - np.log(np.exp(log_p).sum(-1, keepdims=True)))
+    for count in (1, 8, 64):
+        best, beams, tokens = (t.cpu().numpy() for t in tkv.beam_select(x, s, count=count))
+        for b in range(2):
+            beam, token = np.divmod(np.arange(4 * 30011), 30011)
+            order = np.lexsort((token, -v[b].ravel(), beam, -total[b].ravel()))[:count]
+            order = order[total[b].ravel()[order] > -(2.0 ** 128 - 2.0 ** 103)]
+            n = len(order)
+            assert np.array_equal(beams[b, :n], beam[order]) and np.array_equal(tokens[b, :n], token[order])
+            assert (beams[b, n:] == -1).all() and (tokens[b, n:] == -1).all() and np.isneginf(best[b, n:]).all()
+            # the logarithm's 2^-20, the sum's half a step
+            assert np.all(np.abs(best[b, :n] - total[b].ravel()[order]) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(total[b].ravel()[order]))
